@@ -247,9 +247,10 @@ def _workspace(nbytes, dev):
 def _own(s):
     from mixture_experts_layer_15_amd import binding as B
     if s["op"] == "clip":
-        ws = _workspace(B.moe_grad_workspace_size(s["grads"]), s["norm"].device)
-        B.moe_grad_norm(s["grads"], s["norm"], ws)
-        B.moe_grad_clip(s["grads"], s["norm"], s["max_norm"], out=s["out"])
+        tensors = B.grad_list(s["grads"], s["out"])
+        ws = _workspace(B.moe_grad_workspace_size(tensors), s["norm"].device)
+        B.moe_grad_norm(tensors, s["norm"], ws)
+        B.moe_grad_clip(tensors, s["norm"], s["max_norm"])
         return dict(norm=s["norm"], out32=s["out32"], out16=s["out16"])
     act = s.get("act", "f32")
     p = B.problem(s["T"], s.get("d", 128), s["E"], s["k"], 128, 0, s.get("local", s["E"]), act, act)
