@@ -93,7 +93,8 @@
  * Limits: 1 <= k <= E <= 512; T*k < 2^31; d, F multiples of 128 and
  * at most 65536; x (T*d elements) and one expert's weight matrix (F*d
  * elements) under 4 GiB each; T = 0 is accepted and enqueues nothing (no
- * output is written).
+ * output is written), except where a call's text says that sums over no
+ * tokens are written as zeros.
  */
 #ifndef MOE_MI355X_H
 #define MOE_MI355X_H
@@ -120,7 +121,9 @@ typedef enum {
   MOE_CALL_PERMUTE = 0,
   MOE_CALL_EXPERT_FFN = 1,
   MOE_CALL_FORWARD = 2,
-  MOE_CALL_ROUTE = 3
+  MOE_CALL_ROUTE = 3,
+  MOE_CALL_BALANCE_LOSS = 4,
+  MOE_CALL_ROUTE_BACKWARD = 5
 } moe_call_t;
 
 /* Layout of the expert weight matrices. */
@@ -336,6 +339,131 @@ moe_status_t moe_eplb_plan(const int64_t* load, int32_t E, int32_t G, int32_t R,
 moe_status_t moe_eplb_remap(int32_t T, int32_t k, int32_t E, int32_t G, const int32_t* topk_idx,
                             const int32_t* replicas, const int32_t* log_to_phys,
                             int32_t* topk_phys, void* stream);
+
+/* ---- Router training ----
+ *
+ * "Serving MoE models with expert parallelism on 8xH200" (reviosa), section
+ * "Routing imbalance", measures the load by per-expert token counts; a
+ * router that is trained to balance it needs the loss on those counts and
+ * the way back from the layer's output through its gates.  The pages give no
+ * formula; the balance loss is that of Fedus, Zoph and Shazeer 2021 ("Switch
+ * Transformers", for k = 1) extended to k slots per token, the z loss that of
+ * Zoph et al. 2022 ("ST-MoE").  A step of router tuning (experts in any
+ * weight format, not changed) is moe_route, moe_permute, moe_expert_ffn
+ * (topk_w NULL), moe_combine (topk_w given); then, from the gradient of the
+ * layer's output, moe_combine_backward, moe_balance_loss,
+ * moe_route_backward, moe_grad_norm and moe_grad_clip.
+ *
+ * Beyond the conventions above, these calls check that every array is
+ * 16-byte aligned (moe_grad_*: that a tensor's address is a multiple of its
+ * value size, which is all they need).  `token_mask` is NULL (every token
+ * counts) or [T] bytes: a token whose byte is 0 (padding) takes no part, and
+ * what the other arrays hold in its row is ignored, NaN included.
+ *
+ * moe_balance_loss - with V the tokens that the mask keeps, N = |V| and
+ * p[t] = softmax over all E logits of row t:
+ *    counts[e]    = number of slots (t, i), t in V, with topk_idx[t*k+i] = e
+ *    prob_mean[e] = (1/N) sum_{t in V} p[t][e]
+ *    losses[0]    = E / (N k) * sum_e counts[e] prob_mean[e]      (balance)
+ *    losses[1]    = (1/N) sum_{t in V} logsumexp(L[t])^2          (z)
+ * All zero for N = 0 (T = 0 included).  Ids outside [0, E) are not counted;
+ * an id that a row names twice counts twice.  -inf logits have p = 0; a row
+ * of -inf only adds nothing to prob_mean and losses[1]; a NaN or +inf logit
+ * of a kept token makes prob_mean and the losses NaN.
+ *  logits [T][E], topk_idx [T][k]: as written by moe_route.
+ *  counts [E] int32, n_tokens [1] int32 (N), prob_mean [E] float32,
+ *  losses [2] float32: outputs, all required.  Ranks that share a batch add
+ *  their counts and n_tokens before moe_route_backward.
+ *  Of p, only T, E and k matter (the rest must be valid).
+ *  ws, ws_bytes: scratch of moe_workspace_size(p, MOE_CALL_BALANCE_LOSS). */
+moe_status_t moe_balance_loss(const moe_problem_t* p, const float* logits, const int32_t* topk_idx,
+                              const uint8_t* token_mask, int32_t* counts, int32_t* n_tokens,
+                              float* prob_mean, float* losses, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* Arguments of moe_route_backward.  At least one of dtopk_w and dlosses, and
+ * at least one output, is given; each input is read only where noted. */
+typedef struct {
+  const void* x;             /* [T][d] act: with dw_router */
+  const void* w_router;      /* [d][E] act: with dx */
+  const float* logits;       /* [T][E]: with dlosses */
+  const int32_t* topk_idx;   /* [T][k]: with dtopk_w */
+  const float* topk_w;       /* [T][k] gates: with dtopk_w */
+  const float* dtopk_w;      /* [T][k] gradient of the gates, or NULL (zero) */
+  const uint8_t* token_mask; /* [T] or NULL */
+  const int32_t* counts;     /* [E]: with dlosses; of the whole batch */
+  const int32_t* n_tokens;   /* [1]: with dlosses; of the whole batch */
+  const float* dlosses;      /* [2] gradients of the two losses, or NULL (zero) */
+  float* dlogits;            /* [T][E] output or NULL */
+  void* dx;                  /* [T][d] act output or NULL */
+  float* dw_router;          /* [d][E] float32 output or NULL */
+  float* dbias;              /* [E] float32 output or NULL */
+} moe_route_backward_args_t;
+
+/* moe_route_backward - the backward pass of moe_route, with that of
+ * moe_balance_loss.  With g = dtopk_w, w = topk_w, N = *n_tokens:
+ *    dL[t][e] = sum_{i: topk_idx[t][i] = e} w[t][i] (g[t][i] - sum_j w[t][j] g[t][j])
+ *             + dlosses[0] E / (N^2 k) p[t][e] (counts[e] - sum_j counts[j] p[t][j])
+ *             + dlosses[1] (2 / N) logsumexp(L[t]) p[t][e]
+ *    dx[t][c] = sum_e dL[t][e] W_r[c][e],  dw_router[c][e] = sum_t x[t][c] dL[t][e],
+ *    dbias[e] = sum_t dL[t][e]
+ * (the counts are constants of the gradient, and the selection is piecewise
+ * constant: neither has one).  Rows of masked tokens are 0 in dlogits and dx.
+ * Slots with an id outside [0, E) are left out of every sum.  N <= 0 leaves
+ * the losses' terms out.  Sums are float32; with bf16 activations dx is
+ * formed from dL rounded to 16 significant bits, dw_router from all 24.
+ * T = 0 writes zeros to dw_router and dbias.
+ *  The outputs are distinct from the inputs (no gradient is formed in place).
+ *  ws, ws_bytes: scratch of moe_workspace_size(p, MOE_CALL_ROUTE_BACKWARD). */
+moe_status_t moe_route_backward(const moe_problem_t* p, const moe_route_backward_args_t* a,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* moe_combine_backward - the backward pass of moe_combine with gates:
+ *    dy[slot_pos[s]] = (topk_w ? topk_w[s] : 1) dout[t],    s = t*k + i
+ *    dtopk_w[s]      = sum_c dout[t][c] y[slot_pos[s]][c]   (float32 sums)
+ * for the kept slots; dtopk_w is 0 at the others, and rows of dy that no
+ * kept slot names (those behind the last kept one) are not written.
+ *  dout [T][d] act; y [T*k][d] act (unweighted expert outputs; with dtopk_w);
+ *  slot_pos [T*k] int32 as written by moe_permute; topk_w [T*k] or NULL;
+ *  dy [T*k][d] act output or NULL (distinct from y and dout); dtopk_w [T*k]
+ *  float32 output or NULL; not both NULL.  A slot_pos outside [0, T*k) means
+ *  not kept. */
+moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dout, const void* y,
+                                  const int32_t* slot_pos, const float* topk_w, void* dy,
+                                  float* dtopk_w, void* stream);
+
+/* One gradient tensor: numel consecutive values at `grad`, MOE_F32 or
+ * MOE_BF16.  `out` (moe_grad_clip only) is `grad` itself or overlaps no
+ * tensor and no other output of the list. */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t numel;
+  int32_t dtype;
+} moe_grad_t;
+
+/* Limits: at most MOE_GRAD_MAX_TENSORS tensors of fewer than 2^40 values. */
+#define MOE_GRAD_MAX_TENSORS 4096
+
+/* Bytes of scratch moe_grad_norm needs for the list (host array) g[n]; 0 if
+ * the list is invalid. */
+size_t moe_grad_workspace_size(const moe_grad_t* g, int32_t n);
+
+/* moe_grad_norm - *norm = sqrt(sum over all values of g^2), summed in
+ * float64 in a fixed order and rounded to float32; 0 for an empty list.
+ *  g: host array, read before the call returns (the list travels with the
+ *  launches).  norm: device float32.  Ranks that hold different parts of a
+ *  model's gradients join their norms as the root of the sum of squares. */
+moe_status_t moe_grad_norm(const moe_grad_t* g, int32_t n, float* norm, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* moe_grad_clip - with v = *norm (device float32, of these or of more
+ * tensors): out = grad * (max_norm / v) if max_norm < v < inf, else out = grad
+ * (a norm that is not finite changes nothing: the caller sees it in *norm and
+ * skips the step).  The scale and the product are float32, rounded once more
+ * for bf16.  max_norm > 0 (inf clips nothing). */
+moe_status_t moe_grad_clip(const moe_grad_t* g, int32_t n, const float* norm, float max_norm,
+                           void* stream);
 
 /* Blocked weight layout (for callers that convert weights once at load
  * time): each expert matrix [Nout][K] is stored as [Nout/32][K/64] units of

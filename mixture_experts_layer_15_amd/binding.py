@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -19,6 +20,8 @@ LIB_PATH = os.environ.get("MOE_MI355X_LIB", os.path.join(PKG, "libmoe_mi355x.so"
 MOE_OK, MOE_ERR_INVALID_ARGUMENT, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_HIP = range(5)
 MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_MXFP4 = range(4)
 MOE_CALL_PERMUTE, MOE_CALL_EXPERT_FFN, MOE_CALL_FORWARD, MOE_CALL_ROUTE = range(4)
+MOE_CALL_BALANCE_LOSS, MOE_CALL_ROUTE_BACKWARD = 4, 5
+MOE_GRAD_MAX_TENSORS = 4096   # include/moe.h
 MOE_FORWARD_EVENTS = 7
 MOE_LAYOUT_ROWS, MOE_LAYOUT_BLOCKED = range(2)
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20   # include/moe.h
@@ -44,6 +47,14 @@ class ForwardArgs(ctypes.Structure):
                  "s_down", "out", "logits", "topk_idx", "topk_w", "counts", "offsets",
                  "sorted_slot", "slot_pos", "events")]
 
+
+class RouteBackwardArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("x", "w_router", "logits", "topk_idx", "topk_w", "dtopk_w", "token_mask",
+                 "counts", "n_tokens", "dlosses", "dlogits", "dx", "dw_router", "dbias")]
+
+
+_GRAD = "PPqi4x"   # moe_grad_t
 
 _lib = None
 
@@ -74,8 +85,17 @@ def load_library() -> ctypes.CDLL:
     lib.moe_eplb_plan.argtypes = [i64p, i32, i32, i32, i32p, i32p, i32p, f64p]
     lib.moe_eplb_remap.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp]
     lib.moe_pack_weights.argtypes = [P, i32, vp, vp, vp]
+    lib.moe_balance_loss.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_route_backward.argtypes = [P, ctypes.POINTER(RouteBackwardArgs), vp, sz, vp]
+    lib.moe_combine_backward.argtypes = [P, vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_grad_workspace_size.argtypes = [vp, i32]
+    lib.moe_grad_workspace_size.restype = sz
+    lib.moe_grad_norm.argtypes = [vp, i32, vp, vp, sz, vp]
+    lib.moe_grad_clip.argtypes = [vp, i32, vp, ctypes.c_float, vp]
     for f in ("moe_route", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_forward",
-              "moe_forward_noalloc", "moe_eplb_plan", "moe_eplb_remap", "moe_pack_weights"):
+              "moe_forward_noalloc", "moe_eplb_plan", "moe_eplb_remap", "moe_pack_weights",
+              "moe_balance_loss", "moe_route_backward", "moe_combine_backward", "moe_grad_norm",
+              "moe_grad_clip"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -217,6 +237,188 @@ def moe_pack_weights(p, which: int, src, dst, stream=None) -> None:
     st = load_library().moe_pack_weights(ctypes.byref(p), which, _ptr(src), _ptr(dst),
                                          _stream(stream))
     _check("moe_pack_weights", st)
+
+
+# ---- router training
+#
+# These calls check the tensors they are given (type, size, contiguity, the
+# current device), since a gradient of another layout would be read wrongly
+# without an error; integers pass as device addresses, unchecked.
+
+def _refuse(call: str, text: str):
+    raise MoEError(call, MOE_ERR_INVALID_ARGUMENT, text)
+
+
+def _arg(call: str, name: str, t, dtype, numel: int, device: int) -> Optional[int]:
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not dtype:
+        _refuse(call, f"{name} is {t.dtype}, not {dtype}")
+    if t.numel() != numel:
+        _refuse(call, f"{name} has {t.numel()} values, not {numel}")
+    if not t.is_contiguous():
+        _refuse(call, f"{name} is not contiguous")
+    if t.get_device() != device:
+        _refuse(call, f"{name} is on {t.device}, not on the current device")
+    return t.data_ptr()
+
+
+def _ws_arg(call: str, ws, device: int):
+    if ws is None:
+        return None, 0
+    if not ws.is_contiguous() or ws.get_device() != device:
+        _refuse(call, "ws is not a contiguous tensor of the current device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _current(call: str, stream):
+    """(device, stream handle) of a call."""
+    device = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    if stream is None:
+        return device, torch.cuda.current_stream().cuda_stream if device >= 0 else None
+    if isinstance(stream, int):
+        return device, stream
+    if stream.device.index != device:
+        _refuse(call, f"the stream is one of {stream.device}, not of the current device")
+    return device, stream.cuda_stream
+
+
+_ACT_DTYPE = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
+
+
+def _act(call: str, p: Problem):
+    if p.act not in _ACT_DTYPE:
+        raise MoEError(call, MOE_ERR_UNSUPPORTED, "activations are f32 or bf16")
+    return _ACT_DTYPE[p.act]
+
+
+def _mask_arg(call: str, mask, T: int, device: int):
+    dtype = torch.uint8
+    if isinstance(mask, torch.Tensor) and mask.dtype is torch.bool:
+        dtype = torch.bool   # one byte, 0 or 1
+    return _arg(call, "token_mask", mask, dtype, T, device)
+
+
+def moe_balance_loss(p, logits, topk_idx, token_mask, counts, n_tokens, prob_mean, losses, ws,
+                     stream=None) -> None:
+    """Balance and z loss over the router's softmax, and per-expert counts (see moe.h).
+    ``token_mask``: uint8 or bool [T], or None."""
+    c = "moe_balance_loss"
+    dev, st = _current(c, stream)
+    f32, i32 = torch.float32, torch.int32
+    wp, wn = _ws_arg(c, ws, dev)
+    _check(c, load_library().moe_balance_loss(
+        ctypes.byref(p), _arg(c, "logits", logits, f32, p.T * p.E, dev),
+        _arg(c, "topk_idx", topk_idx, i32, p.T * p.k, dev), _mask_arg(c, token_mask, p.T, dev),
+        _arg(c, "counts", counts, i32, p.E, dev), _arg(c, "n_tokens", n_tokens, i32, 1, dev),
+        _arg(c, "prob_mean", prob_mean, f32, p.E, dev), _arg(c, "losses", losses, f32, 2, dev),
+        wp, wn, st))
+
+
+def moe_route_backward(p, *, ws, x=None, w_router=None, logits=None, topk_idx=None, topk_w=None,
+                       dtopk_w=None, token_mask=None, counts=None, n_tokens=None, dlosses=None,
+                       dlogits=None, dx=None, dw_router=None, dbias=None, stream=None) -> None:
+    """Gradient of the router from that of its gates and of the balance losses (see moe.h)."""
+    c = "moe_route_backward"
+    dev, st = _current(c, stream)
+    f32, i32, act = torch.float32, torch.int32, _act(c, p)
+    S = p.T * p.k
+    a = RouteBackwardArgs(
+        _arg(c, "x", x, act, p.T * p.d, dev), _arg(c, "w_router", w_router, act, p.d * p.E, dev),
+        _arg(c, "logits", logits, f32, p.T * p.E, dev), _arg(c, "topk_idx", topk_idx, i32, S, dev),
+        _arg(c, "topk_w", topk_w, f32, S, dev), _arg(c, "dtopk_w", dtopk_w, f32, S, dev),
+        _mask_arg(c, token_mask, p.T, dev), _arg(c, "counts", counts, i32, p.E, dev),
+        _arg(c, "n_tokens", n_tokens, i32, 1, dev), _arg(c, "dlosses", dlosses, f32, 2, dev),
+        _arg(c, "dlogits", dlogits, f32, p.T * p.E, dev), _arg(c, "dx", dx, act, p.T * p.d, dev),
+        _arg(c, "dw_router", dw_router, f32, p.d * p.E, dev),
+        _arg(c, "dbias", dbias, f32, p.E, dev))
+    wp, wn = _ws_arg(c, ws, dev)
+    _check(c, load_library().moe_route_backward(ctypes.byref(p), ctypes.byref(a), wp, wn, st))
+
+
+def moe_combine_backward(p, dout, y, slot_pos, topk_w, dy, dtopk_w, stream=None) -> None:
+    """Gradients of the expert rows and the gates from that of the layer's output (see moe.h)."""
+    c = "moe_combine_backward"
+    dev, st = _current(c, stream)
+    f32, act = torch.float32, _act(c, p)
+    S = p.T * p.k
+    _check(c, load_library().moe_combine_backward(
+        ctypes.byref(p), _arg(c, "dout", dout, act, p.T * p.d, dev),
+        _arg(c, "y", y, act, S * p.d, dev), _arg(c, "slot_pos", slot_pos, torch.int32, S, dev),
+        _arg(c, "topk_w", topk_w, f32, S, dev), _arg(c, "dy", dy, act, S * p.d, dev),
+        _arg(c, "dtopk_w", dtopk_w, f32, S, dev), st))
+
+
+class GradList:
+    """The host array of ``moe_grad_t`` for a list of gradient tensors, and the tensors
+    themselves, so that their memory lives as long as the list."""
+
+    def __init__(self, grads, out=None):
+        c = "grad_list"
+        grads = list(grads)
+        out = grads if out is None else list(out)
+        if len(out) != len(grads):
+            _refuse(c, f"{len(out)} outputs for {len(grads)} gradients")
+        kind = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+        flat = []
+        self.device = None
+        for g, o in zip(grads, out):
+            code = kind.get(g.dtype)
+            if code is None:
+                raise MoEError(c, MOE_ERR_UNSUPPORTED, f"a gradient is {g.dtype}, not float32 or bfloat16")
+            n = g.numel()
+            if not g.is_contiguous():
+                _refuse(c, "a gradient is not contiguous")
+            dev = g.get_device()
+            if self.device is None:
+                self.device = dev
+            if dev != self.device:
+                _refuse(c, "the gradients are on more than one device")
+            if o is not g and (o.dtype is not g.dtype or o.numel() != n or not o.is_contiguous()
+                               or o.get_device() != dev):
+                _refuse(c, "an output has another type, size, layout or device than its gradient")
+            flat += (g.data_ptr(), o.data_ptr(), n, code)
+        self.n = len(grads)
+        self.tensors = (grads, out)
+        self.array = struct.pack(_GRAD * self.n, *flat)
+
+
+def grad_list(grads, out=None) -> GradList:
+    """The gradients that moe_grad_norm and moe_grad_clip work on; ``out``: where clipping
+    writes (default: in place).  A program keeps it as long as the tensors stay."""
+    return GradList(grads, out)
+
+
+def _grads(call: str, grads, device: int) -> GradList:
+    if not isinstance(grads, GradList):
+        grads = GradList(grads)
+    if grads.n and device >= 0 and grads.device != device:
+        _refuse(call, "the gradients are not on the current device")
+    return grads
+
+
+def moe_grad_workspace_size(grads) -> int:
+    g = grads if isinstance(grads, GradList) else GradList(grads)
+    return int(load_library().moe_grad_workspace_size(g.array, g.n))
+
+
+def moe_grad_norm(grads, norm, ws, stream=None) -> None:
+    """Global L2 norm of a list of gradients (a sequence of tensors or a ``grad_list``)."""
+    c = "moe_grad_norm"
+    dev, st = _current(c, stream)
+    g = _grads(c, grads, dev)
+    wp, wn = _ws_arg(c, ws, dev)
+    _check(c, load_library().moe_grad_norm(g.array, g.n, _arg(c, "norm", norm, torch.float32, 1, dev),
+                                           wp, wn, st))
+
+
+def moe_grad_clip(grads, norm, max_norm: float, stream=None) -> None:
+    """Gradients scaled so that a global norm above ``max_norm`` becomes ``max_norm``."""
+    c = "moe_grad_clip"
+    dev, st = _current(c, stream)
+    g = _grads(c, grads, dev)
+    _check(c, load_library().moe_grad_clip(g.array, g.n, _arg(c, "norm", norm, torch.float32, 1, dev),
+                                           max_norm, st))
 
 
 def workspace(p: Problem, call: int, device="cuda") -> torch.Tensor:

@@ -117,7 +117,91 @@ __global__ __launch_bounds__(kMaxThreads) void combine_kernel(const void* y, con
   }
 }
 
+// ---- backward:  dy[pos] = w dout[t],  dw[t][i] = <dout[t], y[pos]>
+//
+// One wave per slot: it reads its token's dout row (the slots of a token are
+// neighbours, so all but the first find it in a cache) and its y row, writes
+// its dy row, and sums the product in float32 with a fixed butterfly.  Every
+// y and dy byte is touched once: HBM-bound.
+struct CombineGradArgs {
+  const void* dout;
+  const void* y;       // null: no dw
+  const int32_t* pos;
+  const float* w;      // null: 1
+  void* dy;            // null: no dy
+  float* dw;           // null: no dw
+  long long S;
+  int d, k;
+};
+
+template <bool kBF16>
+__global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(CombineGradArgs a) {
+  const int l = lane_id();
+  const long long s = (long long)blockIdx.x * (kMaxThreads / kWave) + threadIdx.x / kWave;
+  if (s >= a.S) return;  // whole waves
+  const int p = a.pos[s];
+  if (p < 0 || p >= a.S) {
+    if (a.dw && l == 0) a.dw[s] = 0.0f;
+    return;
+  }
+  const float w = a.w ? a.w[s] : 1.0f;
+  const long long din = s / a.k * a.d, yin = (long long)p * a.d;
+  float dot = 0.0f;
+  constexpr int V = kBF16 ? 8 : 4;  // values of a 16-byte load
+  for (int c = l * V; c < a.d; c += kWave * V) {
+    if constexpr (kBF16) {
+      const u32x4_t g = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.dout) + din + c);
+      if (a.dw) {
+        const u32x4_t y = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.y) + yin + c));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          dot = fmaf(bf16_to_f32(uint16_t(g[q])), bf16_to_f32(uint16_t(y[q])), dot);
+          dot = fmaf(bf16_to_f32(uint16_t(g[q] >> 16)), bf16_to_f32(uint16_t(y[q] >> 16)), dot);
+        }
+      }
+      if (a.dy) {
+        u32x4_t o;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          o[q] = pack_bf16x2(w * bf16_to_f32(uint16_t(g[q])), w * bf16_to_f32(uint16_t(g[q] >> 16)));
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.dy) + yin + c));
+      }
+    } else {
+      const f32x4_t g = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.dout) + din + c);
+      if (a.dw) {
+        const f32x4_t y = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.y) + yin + c);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) dot = fmaf(g[q], y[q], dot);
+      }
+      if (a.dy) {
+        f32x4_t o;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = w * g[q];
+        *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.dy) + yin + c) = o;
+      }
+    }
+  }
+  if (a.dw) {
+    dot = wave_sum(dot);
+    if (l == 0) a.dw[s] = dot;
+  }
+}
+
 }  // namespace
+
+hipError_t combine_backward(const Shape& s, const void* dout, const void* y,
+                            const int32_t* slot_pos, const float* topk_w, void* dy,
+                            float* dtopk_w, hipStream_t st) {
+  const CombineGradArgs a{dout, y, slot_pos, topk_w, dy, dtopk_w, s.S, s.d, s.k};
+  const int per = kMaxThreads / kWave;
+  const dim3 grid((unsigned)((s.S + per - 1) / per));
+  if (s.act == kBF16)
+    hipLaunchKernelGGL(combine_backward_kernel<true>, grid, dim3(kMaxThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL(combine_backward_kernel<false>, grid, dim3(kMaxThreads), 0, st, a);
+  return hipGetLastError();
+}
 
 hipError_t combine(const Shape& s, const void* y, const int32_t* slot_pos, const float* topk_w,
                    void* out, hipStream_t st) {

@@ -3,6 +3,8 @@
 // before anything is enqueued; no call allocates, frees or synchronises.
 #include "moe.h"
 
+#include <algorithm>
+#include <cmath>
 #include <new>
 
 #include "moe_internal.h"
@@ -56,6 +58,56 @@ moe_status_t check_problem(const moe_problem_t* p, Shape* s) {
 
 moe_status_t from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+template <class... P>
+bool all_aligned16(P... p) {
+  return (... && aligned16(p));
+}
+
+// A gradient list: sizes, types, addresses, and (for clipping) outputs that
+// are the tensor itself or overlap no tensor and no other output.
+moe_status_t check_grads(const moe_grad_t* g, int32_t n, bool outputs) {
+  if (n < 0 || (n > 0 && g == nullptr)) return MOE_ERR_INVALID_ARGUMENT;
+  if (n > MOE_GRAD_MAX_TENSORS) return MOE_ERR_UNSUPPORTED;
+  struct Range {
+    uintptr_t b, e;
+    int i;
+  };
+  Range out[MOE_GRAD_MAX_TENSORS];
+  int used = 0;
+  for (int i = 0; i < n; ++i) {
+    if (g[i].numel < 0) return MOE_ERR_INVALID_ARGUMENT;
+    if (g[i].dtype != MOE_F32 && g[i].dtype != MOE_BF16)
+      return g[i].dtype > MOE_BF16 && g[i].dtype <= MOE_MXFP4 ? MOE_ERR_UNSUPPORTED
+                                                              : MOE_ERR_INVALID_ARGUMENT;
+    if (g[i].numel >= (1LL << 40)) return MOE_ERR_UNSUPPORTED;
+    if (g[i].numel == 0) continue;
+    const uintptr_t size = g[i].dtype == MOE_F32 ? 4 : 2;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(g[i].grad);
+    if (g[i].grad == nullptr || b % size != 0) return MOE_ERR_INVALID_ARGUMENT;
+    if (!outputs) continue;
+    const uintptr_t o = reinterpret_cast<uintptr_t>(g[i].out);
+    if (g[i].out == nullptr || o % size != 0) return MOE_ERR_INVALID_ARGUMENT;
+    out[used++] = Range{o, o + size * (uintptr_t)g[i].numel, i};
+  }
+  if (used == 0) return MOE_OK;
+  std::sort(out, out + used, [](const Range& a, const Range& b) { return a.b < b.b; });
+  for (int q = 1; q < used; ++q)
+    if (out[q].b < out[q - 1].e) return MOE_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < n; ++i) {
+    if (g[i].numel == 0) continue;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(g[i].grad);
+    const uintptr_t e = b + (g[i].dtype == MOE_F32 ? 4 : 2) * (uintptr_t)g[i].numel;
+    // the outputs are disjoint: those that reach into [b, e) end behind b
+    int q = (int)(std::upper_bound(out, out + used, b,
+                                   [](uintptr_t v, const Range& r) { return v < r.e; }) - out);
+    for (; q < used && out[q].b < e; ++q)
+      if (out[q].i != i || g[i].out != g[i].grad) return MOE_ERR_INVALID_ARGUMENT;
+  }
+  return MOE_OK;
+}
+
 // Device-memory layout of the moe_forward workspace.
 struct ForwardLayout {
   size_t logits, idx, w, counts, offsets, sorted, pos, y, router, permute, ffn, total;
@@ -100,6 +152,10 @@ size_t moe_workspace_size(const moe_problem_t* p, int32_t call) {
       return forward_layout(s).total;
     case MOE_CALL_ROUTE:
       return moe::route_ws_bytes(s);
+    case MOE_CALL_BALANCE_LOSS:
+      return moe::balance_ws_bytes(s);
+    case MOE_CALL_ROUTE_BACKWARD:
+      return moe::route_backward_ws_bytes(s);
     default:
       return 0;
   }
@@ -240,6 +296,107 @@ moe_status_t moe_forward(const moe_problem_t* p, const moe_forward_args_t* a, vo
   if (e == hipSuccess) e = moe::combine(s, y, pos, nullptr, a->out, strm);
   if (e == hipSuccess) e = mark(6);
   return from_hip(e);
+}
+
+moe_status_t moe_balance_loss(const moe_problem_t* p, const float* logits, const int32_t* topk_idx,
+                              const uint8_t* token_mask, int32_t* counts, int32_t* n_tokens,
+                              float* prob_mean, float* losses, void* ws, size_t ws_bytes,
+                              void* stream) {
+  Shape s;
+  moe_status_t st = check_problem(p, &s);
+  if (st != MOE_OK) return st;
+  if (counts == nullptr || n_tokens == nullptr || prob_mean == nullptr || losses == nullptr)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (s.T > 0 && (logits == nullptr || topk_idx == nullptr)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!all_aligned16(logits, topk_idx, token_mask, counts, n_tokens, prob_mean, losses, ws))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (ws == nullptr || ws_bytes < moe::balance_ws_bytes(s)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return from_hip(moe::balance_loss(s, logits, topk_idx, token_mask, counts, n_tokens, prob_mean,
+                                    losses, ws, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_route_backward(const moe_problem_t* p, const moe_route_backward_args_t* a,
+                                void* ws, size_t ws_bytes, void* stream) {
+  Shape s;
+  moe_status_t st = check_problem(p, &s);
+  if (st != MOE_OK) return st;
+  if (a == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (a->dtopk_w == nullptr && a->dlosses == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (a->dlogits == nullptr && a->dx == nullptr && a->dw_router == nullptr && a->dbias == nullptr)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (a->dlogits != nullptr && a->dlogits == a->logits) return MOE_ERR_INVALID_ARGUMENT;
+  if (a->dx != nullptr && a->dx == a->x) return MOE_ERR_INVALID_ARGUMENT;
+  if (s.T > 0) {
+    if (a->dtopk_w != nullptr && (a->topk_idx == nullptr || a->topk_w == nullptr))
+      return MOE_ERR_INVALID_ARGUMENT;
+    if (a->dlosses != nullptr &&
+        (a->logits == nullptr || a->counts == nullptr || a->n_tokens == nullptr))
+      return MOE_ERR_INVALID_ARGUMENT;
+    if (a->dw_router != nullptr && a->x == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+    if (a->dx != nullptr && a->w_router == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  }
+  if (!all_aligned16(a->x, a->w_router, a->logits, a->topk_idx, a->topk_w, a->dtopk_w,
+                     a->token_mask, a->counts, a->n_tokens, a->dlosses, a->dlogits, a->dx,
+                     a->dw_router, a->dbias, ws))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (ws == nullptr || ws_bytes < moe::route_backward_ws_bytes(s))
+    return MOE_ERR_WORKSPACE_TOO_SMALL;
+  moe::RouteGradArgs g{};
+  g.gate.logits = a->logits;
+  g.gate.idx = a->topk_idx;
+  g.gate.topk_w = a->topk_w;
+  g.gate.dtopk_w = a->dtopk_w;
+  g.gate.mask = a->token_mask;
+  g.gate.counts = a->counts;
+  g.gate.n_tokens = a->n_tokens;
+  g.gate.dlosses = a->dlosses;
+  g.x = a->x;
+  g.w_router = a->w_router;
+  g.dlogits = a->dlogits;
+  g.dx = a->dx;
+  g.dw = a->dw_router;
+  g.dbias = a->dbias;
+  return from_hip(moe::route_backward(s, g, ws, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dout, const void* y,
+                                  const int32_t* slot_pos, const float* topk_w, void* dy,
+                                  float* dtopk_w, void* stream) {
+  Shape s;
+  moe_status_t st = check_problem(p, &s);
+  if (st != MOE_OK) return st;
+  if (dout == nullptr || slot_pos == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (dy == nullptr && dtopk_w == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (dtopk_w != nullptr && y == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (dy != nullptr && (dy == y || dy == dout)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!all_aligned16(dout, y, slot_pos, topk_w, dy, dtopk_w)) return MOE_ERR_INVALID_ARGUMENT;
+  if (s.T == 0) return MOE_OK;
+  return from_hip(moe::combine_backward(s, dout, y, slot_pos, topk_w, dy, dtopk_w,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_grad_workspace_size(const moe_grad_t* g, int32_t n) {
+  return check_grads(g, n, false) == MOE_OK ? moe::grad_ws_bytes(g, n) : 0;
+}
+
+moe_status_t moe_grad_norm(const moe_grad_t* g, int32_t n, float* norm, void* ws, size_t ws_bytes,
+                           void* stream) {
+  const moe_status_t st = check_grads(g, n, false);
+  if (st != MOE_OK) return st;
+  if (norm == nullptr || reinterpret_cast<uintptr_t>(norm) % 4 != 0 || !aligned16(ws))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (ws == nullptr || ws_bytes < moe::grad_ws_bytes(g, n)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return from_hip(moe::grad_norm(g, n, norm, ws, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_grad_clip(const moe_grad_t* g, int32_t n, const float* norm, float max_norm,
+                           void* stream) {
+  const moe_status_t st = check_grads(g, n, true);
+  if (st != MOE_OK) return st;
+  if (norm == nullptr || reinterpret_cast<uintptr_t>(norm) % 4 != 0)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!(max_norm > 0.0f)) return MOE_ERR_INVALID_ARGUMENT;
+  return from_hip(moe::grad_clip(g, n, norm, max_norm, static_cast<hipStream_t>(stream)));
 }
 
 moe_status_t moe_pack_weights(const moe_problem_t* p, int32_t which, const void* src, void* dst,

@@ -8,6 +8,8 @@
 
 #include <atomic>
 
+#include "moe.h"
+
 namespace moe {
 
 enum Fmt : int { kF32 = 0, kBF16 = 1, kFP8 = 2, kFP4 = 3 };
@@ -89,6 +91,56 @@ hipError_t permute(const Shape& s, const int32_t* topk_idx, int32_t* counts, int
 // ---- combine.hip
 hipError_t combine(const Shape& s, const void* y, const int32_t* slot_pos, const float* topk_w,
                    void* out, hipStream_t st);
+
+// The combine's backward pass (y, dy, topk_w, dtopk_w may be null).
+hipError_t combine_backward(const Shape& s, const void* dout, const void* y,
+                            const int32_t* slot_pos, const float* topk_w, void* dy,
+                            float* dtopk_w, hipStream_t st);
+
+// ---- balance.hip
+size_t balance_ws_bytes(const Shape& s);
+hipError_t balance_loss(const Shape& s, const float* logits, const int32_t* topk_idx,
+                        const uint8_t* mask, int32_t* counts, int32_t* n_tokens,
+                        float* prob_mean, float* losses, void* ws, hipStream_t st);
+
+// Gradient of gates (dtopk_w) and losses (dlosses) with respect to the logits.
+constexpr int kZeroLineBytes = 512;
+struct GateGradArgs {
+  const float* logits;     // read where dlosses is given
+  const int32_t* idx;      // idx, topk_w: read where dtopk_w is given
+  const float* topk_w;
+  const float* dtopk_w;    // [T][k] or null
+  const uint8_t* mask;     // [T] or null
+  const int32_t* counts;   // counts, n_tokens: read where dlosses is given
+  const int32_t* n_tokens;
+  const float* dlosses;    // [2] or null
+  float* dlogits;          // [T][E] or null
+  uint16_t* planes;        // [nplanes][T][Ep] bfloat16 planes whose sum is the gradient
+  int nplanes;
+  void* zero_line;         // kZeroLineBytes that the kernel clears
+  float* bias_part;        // [gate_grad_blocks][E] column sums per workgroup, or null
+};
+int gate_grad_blocks(const Shape& s);
+hipError_t gate_grad(const Shape& s, const GateGradArgs& a, int Ep, hipStream_t st);
+
+// ---- route_grad.hip
+struct RouteGradArgs {
+  GateGradArgs gate;       // the inputs
+  const void* x;           // read where dw is given
+  const void* w_router;    // read where dx is given
+  float* dlogits;          // each output may be null
+  void* dx;
+  float* dw;
+  float* dbias;
+};
+size_t route_backward_ws_bytes(const Shape& s);
+hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipStream_t st);
+
+// ---- grads.hip
+size_t grad_ws_bytes(const moe_grad_t* g, int n);
+hipError_t grad_norm(const moe_grad_t* g, int n, float* norm, void* ws, hipStream_t st);
+hipError_t grad_clip(const moe_grad_t* g, int n, const float* norm, float max_norm,
+                     hipStream_t st);
 
 // Blocked layout of one stored expert weight matrix [Nout][K] (any weight
 // format but float32): [Nout/32][K/64][32 rows][64 K values], each 32 x 64

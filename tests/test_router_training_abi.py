@@ -1,0 +1,260 @@
+"""Router training on the host side: argument checks of the balance loss, the
+router's and the combine's backward passes and the gradient norm and clipping
+(no call here reaches a kernel launch), the binding's tensor checks, and the
+loss gradients' formula against differences of the loss in 64 bits."""
+import ctypes
+import math
+import os
+
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_15_amd import binding as B
+
+FAKE = 0x1000  # never dereferenced: the calls below fail their host checks
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(B.LIB_PATH):
+        from mixture_experts_layer_15_amd import build
+        build.build()
+    return B.load_library()
+
+
+def _p(**kw):
+    base = dict(T=64, d=256, E=8, k=2, F=256, expert_begin=0, num_local=8, act="bf16", weight="bf16")
+    base.update(kw)
+    return B.problem(**base)
+
+
+def _balance(lib, p, **kw):
+    a = dict(logits=FAKE, idx=FAKE, mask=None, counts=FAKE, n=FAKE, mean=FAKE, losses=FAKE, ws=FAKE, bytes=BIG)
+    a.update(kw)
+    return lib.moe_balance_loss(ctypes.byref(p), a["logits"], a["idx"], a["mask"], a["counts"], a["n"],
+                                a["mean"], a["losses"], a["ws"], a["bytes"], None)
+
+
+def _route(lib, p, ws=FAKE, nbytes=BIG, **kw):
+    a = B.RouteBackwardArgs(**kw)
+    return lib.moe_route_backward(ctypes.byref(p), ctypes.byref(a), ws, nbytes, None)
+
+
+GATES = dict(topk_idx=FAKE, topk_w=FAKE, dtopk_w=FAKE)
+LOSSES = dict(logits=FAKE, counts=FAKE, n_tokens=FAKE, dlosses=FAKE)
+
+
+@pytest.mark.parametrize("missing", ["logits", "idx", "counts", "n", "mean", "losses"])
+def test_balance_needs_every_array(lib, missing):
+    assert _balance(lib, _p(), **{missing: None}) == B.MOE_ERR_INVALID_ARGUMENT
+
+
+def test_balance_checks_shape_alignment_and_workspace(lib):
+    assert _balance(lib, _p(k=9)) == B.MOE_ERR_INVALID_ARGUMENT
+    assert _balance(lib, _p(E=1024, num_local=1)) == B.MOE_ERR_UNSUPPORTED
+    for name in ("logits", "idx", "mask", "counts", "n", "mean", "losses", "ws"):
+        assert _balance(lib, _p(), **{name: FAKE + 4}) == B.MOE_ERR_INVALID_ARGUMENT
+    for T in (0, 1, 64, 100000):
+        need = B.moe_workspace_size(_p(T=T), B.MOE_CALL_BALANCE_LOSS)
+        assert need > 0 and need % 256 == 0
+        assert _balance(lib, _p(T=T), bytes=need - 1) == B.MOE_ERR_WORKSPACE_TOO_SMALL
+        assert _balance(lib, _p(T=T), ws=None) == B.MOE_ERR_WORKSPACE_TOO_SMALL
+
+
+@pytest.mark.parametrize("missing", ["topk_idx", "topk_w"])
+def test_route_backward_needs_what_the_gates_read(lib, missing):
+    assert _route(lib, _p(), dbias=FAKE, **{**GATES, missing: None}) == B.MOE_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("missing", ["logits", "counts", "n_tokens"])
+def test_route_backward_needs_what_the_losses_read(lib, missing):
+    assert _route(lib, _p(), dbias=FAKE, **{**LOSSES, missing: None}) == B.MOE_ERR_INVALID_ARGUMENT
+
+
+def test_route_backward_refusals(lib):
+    p = _p()
+    assert lib.moe_route_backward(ctypes.byref(p), None, FAKE, BIG, None) == B.MOE_ERR_INVALID_ARGUMENT
+    assert _route(lib, p, dbias=FAKE, topk_idx=FAKE, topk_w=FAKE) == B.MOE_ERR_INVALID_ARGUMENT  # no gradient
+    assert _route(lib, p, **GATES) == B.MOE_ERR_INVALID_ARGUMENT                                 # no output
+    assert _route(lib, p, dw_router=FAKE, **GATES) == B.MOE_ERR_INVALID_ARGUMENT                 # no x
+    assert _route(lib, p, dx=FAKE, **GATES) == B.MOE_ERR_INVALID_ARGUMENT                        # no matrix
+    assert _route(lib, p, dlogits=2 * FAKE, **{**LOSSES, "logits": 2 * FAKE}) == B.MOE_ERR_INVALID_ARGUMENT
+    assert _route(lib, p, dx=2 * FAKE, x=2 * FAKE, w_router=FAKE, **GATES) == B.MOE_ERR_INVALID_ARGUMENT
+    everything = dict(x=FAKE, w_router=FAKE, token_mask=FAKE, dlogits=2 * FAKE, dx=2 * FAKE, dw_router=FAKE,
+                      dbias=FAKE, **GATES, **LOSSES)
+    for name in everything:
+        assert _route(lib, p, **{**everything, name: everything[name] + 2}) == B.MOE_ERR_INVALID_ARGUMENT, name
+    assert _route(lib, _p(d=100), **everything) == B.MOE_ERR_INVALID_ARGUMENT
+    assert _route(lib, _p(weight="f32"), **everything) == B.MOE_ERR_UNSUPPORTED
+    for kw in (dict(), dict(act="f32", weight="f32"), dict(T=5000), dict(E=7, num_local=7)):
+        need = B.moe_workspace_size(_p(**kw), B.MOE_CALL_ROUTE_BACKWARD)
+        assert need > 0 and need % 256 == 0
+        assert _route(lib, _p(**kw), nbytes=need - 1, **everything) == B.MOE_ERR_WORKSPACE_TOO_SMALL
+        assert _route(lib, _p(**kw), ws=None, **everything) == B.MOE_ERR_WORKSPACE_TOO_SMALL
+
+
+def test_combine_backward_refusals(lib):
+    p = _p()
+
+    def call(dout=FAKE, y=2 * FAKE, pos=FAKE, w=FAKE, dy=3 * FAKE, dw=FAKE, p=p):
+        return lib.moe_combine_backward(ctypes.byref(p), dout, y, pos, w, dy, dw, None)
+    assert call(dout=None) == call(pos=None) == call(dy=None, dw=None) == B.MOE_ERR_INVALID_ARGUMENT
+    assert call(y=None) == B.MOE_ERR_INVALID_ARGUMENT            # the gates' gradient reads y
+    assert call(dy=2 * FAKE) == call(dy=FAKE) == B.MOE_ERR_INVALID_ARGUMENT   # aliases
+    for name in ("dout", "y", "pos", "w", "dy", "dw"):
+        assert call(**{name: 5 * FAKE + 8}) == B.MOE_ERR_INVALID_ARGUMENT
+    assert call(p=_p(T=-1)) == B.MOE_ERR_INVALID_ARGUMENT
+    assert call(p=_p(T=0)) == B.MOE_OK                            # nothing to do, nothing enqueued
+
+
+def _grads(*rows):
+    import struct
+    return struct.pack(B._GRAD * len(rows), *[v or 0 for r in rows for v in r])
+
+
+def test_gradient_list_refusals(lib):
+    ok = (FAKE, FAKE, 100, B.MOE_F32)
+
+    def norm(rows, n=None, out=FAKE, ws=FAKE, nbytes=BIG):
+        return lib.moe_grad_norm(_grads(*rows), len(rows) if n is None else n, out, ws, nbytes, None)
+
+    def clip(rows, out=FAKE, limit=1.0):
+        return lib.moe_grad_clip(_grads(*rows), len(rows), out, limit, None)
+    bad = [(None, FAKE, 4, B.MOE_F32), (FAKE, FAKE, -1, B.MOE_F32), (FAKE + 2, FAKE, 4, B.MOE_F32),
+           (FAKE + 1, FAKE, 4, B.MOE_BF16), (FAKE, FAKE, 4, 9), (FAKE, FAKE, 4, -1)]
+    for r in bad:
+        assert norm([ok, r]) == clip([ok, r]) == B.MOE_ERR_INVALID_ARGUMENT, r
+        assert lib.moe_grad_workspace_size(_grads(ok, r), 2) == 0
+    for r in [(FAKE, FAKE, 4, B.MOE_FP8_E4M3), (FAKE, FAKE, 1 << 40, B.MOE_BF16)]:
+        assert norm([r]) == clip([r]) == B.MOE_ERR_UNSUPPORTED, r
+    assert norm([ok], n=-1) == B.MOE_ERR_INVALID_ARGUMENT
+    assert lib.moe_grad_norm(None, 1, FAKE, FAKE, BIG, None) == B.MOE_ERR_INVALID_ARGUMENT
+    assert norm([ok] * (B.MOE_GRAD_MAX_TENSORS + 1)) == B.MOE_ERR_UNSUPPORTED
+    assert norm([ok], out=None) == clip([ok], out=None) == B.MOE_ERR_INVALID_ARGUMENT
+    assert norm([ok], ws=None) == norm([ok], nbytes=255) == B.MOE_ERR_WORKSPACE_TOO_SMALL
+    for limit in (0.0, -1.0, math.nan):
+        assert clip([ok], limit=limit) == B.MOE_ERR_INVALID_ARGUMENT
+    for r in [(FAKE, None, 4, B.MOE_F32), (FAKE, FAKE + 2, 4, B.MOE_F32)]:
+        assert clip([r]) == B.MOE_ERR_INVALID_ARGUMENT
+
+
+def test_clipping_outputs_may_not_overlap(lib):
+    def clip(*rows):
+        return lib.moe_grad_clip(_grads(*rows), len(rows), FAKE, 1.0, None)
+    f = B.MOE_F32
+    bad = B.MOE_ERR_INVALID_ARGUMENT
+    assert clip((0x1000, 0x1000, 16, f), (0x1000, 0x1000, 16, f)) == bad       # one tensor twice, in place
+    assert clip((0x1000, 0x9000, 16, f), (0x2000, 0x9020, 16, f)) == bad       # two outputs
+    assert clip((0x1000, 0x1010, 16, f)) == bad                                # its own input, shifted
+    assert clip((0x1000, 0x9000, 16, f), (0x2000, 0x1020, 4, f)) == bad        # another one's input
+    assert clip((0x1000, 0x9000, 400, f), (0x2000, 0xa000, 4, f), (0x9600, 0xb000, 4, f)) == bad
+    # empty tensors overlap nothing, whatever their addresses; an empty list is done
+    assert clip((0x1000, 0x1000, 0, f), (0x1000, 0x1000, 0, f)) == B.MOE_OK
+    assert lib.moe_grad_clip(None, 0, FAKE, 1.0, None) == B.MOE_OK
+
+
+def test_gradient_workspace_covers_every_launch(lib):
+    """One float64 per workgroup: a list of many tensors takes several launches of up to 2048."""
+    def size(rows):
+        return lib.moe_grad_workspace_size(_grads(*rows), len(rows))
+    assert size([(FAKE, FAKE, 1, B.MOE_F32)]) == 256
+    one = size([(FAKE, FAKE, 1 << 30, B.MOE_BF16)])
+    assert one == 2048 * 8
+    assert size([(FAKE, FAKE, 1 << 30, B.MOE_BF16)] * 400) >= 4 * one
+    assert lib.moe_grad_workspace_size(None, 0) == 256
+
+
+def test_binding_checks_tensors():
+    p = _p()
+    T, E, k, d = 64, 8, 2, 256
+    f = dict(logits=torch.zeros(T, E), topk_idx=torch.zeros(T, k, dtype=torch.int32), token_mask=None,
+             counts=torch.zeros(E, dtype=torch.int32), n_tokens=torch.zeros(1, dtype=torch.int32),
+             prob_mean=torch.zeros(E), losses=torch.zeros(2), ws=torch.zeros(1 << 20, dtype=torch.uint8))
+    wrong = dict(logits=[torch.zeros(T, E, dtype=torch.float64), torch.zeros(T, E + 1), torch.zeros(E, T).t()],
+                 topk_idx=[torch.zeros(T, k, dtype=torch.int64)], token_mask=[torch.zeros(T), torch.zeros(3, dtype=torch.bool)],
+                 losses=[torch.zeros(3)])
+    for name, values in wrong.items():
+        for v in values:
+            with pytest.raises(B.MoEError, match=name):
+                B.moe_balance_loss(p, **{**f, name: v})
+    with pytest.raises(B.MoEError, match="dout"):
+        B.moe_combine_backward(p, torch.zeros(T, d), None, None, None, None, None)
+    with pytest.raises(B.MoEError, match="w_router"):
+        B.moe_route_backward(p, ws=None, w_router=torch.zeros(E, d, dtype=torch.bfloat16).t())
+
+
+def test_grad_list_checks_tensors():
+    g = torch.zeros(4, 6)
+    with pytest.raises(B.MoEError, match="float64"):
+        B.grad_list([g, g.double()])
+    with pytest.raises(B.MoEError, match="contiguous"):
+        B.grad_list([g.t()])
+    with pytest.raises(B.MoEError, match="outputs"):
+        B.grad_list([g], [])
+    for o in (g.bfloat16(), g[:2], torch.zeros(6, 4).t()):
+        with pytest.raises(B.MoEError, match="output"):
+            B.grad_list([g], [o])
+    lst = B.grad_list([g, torch.zeros(0), torch.zeros(7, dtype=torch.bfloat16)])
+    assert lst.n == 3 and len(lst.array) == 96
+    rows = np.frombuffer(lst.array, dtype=np.int64).reshape(3, 4)
+    assert rows[0, 0] == rows[0, 1] == g.data_ptr() and list(rows[:, 2]) == [24, 0, 7]
+    assert [int(v) & 0xffffffff for v in rows[:, 3]] == [B.MOE_F32, B.MOE_F32, B.MOE_BF16]
+
+
+def losses64(L, idx, counts, mask, k):
+    """The two losses of moe_balance_loss in 64 bits, with the counts given."""
+    E = L.shape[1]
+    V = L[mask]
+    n = len(V)
+    m = V.max(axis=1, keepdims=True)
+    ex = np.exp(V - m)
+    p = ex / ex.sum(axis=1, keepdims=True)
+    lse = (m + np.log(ex.sum(axis=1, keepdims=True)))[:, 0]
+    return np.array([E / (n * k) * (counts * p.mean(axis=0)).sum(), (lse ** 2).mean()])
+
+
+def dlogits64(L, idx, w, g, counts, n, dl, mask):
+    """moe_route_backward's dL in 64 bits."""
+    T, E = L.shape
+    k = idx.shape[1]
+    m = L.max(axis=1, keepdims=True)
+    ex = np.exp(L - m)
+    p = ex / ex.sum(axis=1, keepdims=True)
+    lse = m + np.log(ex.sum(axis=1, keepdims=True))
+    r = dl[0] * E / (n * n * k) * p * (counts - (counts * p).sum(axis=1, keepdims=True)) + dl[1] * 2 / n * lse * p
+    s = w * (g - (w * g).sum(axis=1, keepdims=True))
+    for t in range(T):
+        for i in range(k):
+            r[t, idx[t, i]] += s[t, i]
+    r[~mask] = 0
+    return r
+
+
+def test_gradient_formula_against_differences():
+    """Central differences of the losses and the gates in 64 bits: step h = 1e-5, whose h^2 term is below
+    1e-9 of the slopes' scale and whose rounding is about 1e-16 / h = 1e-11."""
+    rng = np.random.default_rng(3)
+    T, E, k = 13, 10, 3
+    L = rng.standard_normal((T, E)) * 2
+    idx = np.argsort(-L, axis=1)[:, :k]
+    mask = rng.random(T) < 0.8
+    counts = np.bincount(idx[mask].reshape(-1), minlength=E).astype(float)
+    n = mask.sum()
+    g = rng.standard_normal((T, k))
+    dl = np.array([0.7, -0.3])
+
+    def gates(L):
+        c = np.take_along_axis(L, idx, axis=1)
+        e = np.exp(c - c.max(axis=1, keepdims=True))
+        return e / e.sum(axis=1, keepdims=True)
+
+    def total(L):
+        return (losses64(L, idx, counts, mask, k) * dl).sum() + (gates(L) * g)[mask].sum()
+    got = dlogits64(L, idx, gates(L), g, counts, n, dl, mask)
+    h = 1e-5
+    for _ in range(20):
+        v = rng.standard_normal((T, E))
+        diff = (total(L + h * v) - total(L - h * v)) / (2 * h)
+        assert abs(diff - (got * v).sum()) <= 1e-8 * np.abs(got * v).sum()
