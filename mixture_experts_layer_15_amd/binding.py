@@ -250,17 +250,17 @@ def _refuse(call: str, text: str):
 
 
 def _arg(call: str, name: str, t, dtype, numel: int, device: int) -> Optional[int]:
-    if t is None or isinstance(t, int):
+    if t is None or type(t) is int:
         return t
+    if t.dtype is dtype and t.numel() == numel and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
     if t.dtype is not dtype:
         _refuse(call, f"{name} is {t.dtype}, not {dtype}")
     if t.numel() != numel:
         _refuse(call, f"{name} has {t.numel()} values, not {numel}")
     if not t.is_contiguous():
         _refuse(call, f"{name} is not contiguous")
-    if t.get_device() != device:
-        _refuse(call, f"{name} is on {t.device}, not on the current device")
-    return t.data_ptr()
+    _refuse(call, f"{name} is on {t.device}, not on the current device")
 
 
 def _ws_arg(call: str, ws, device: int):
@@ -271,11 +271,18 @@ def _ws_arg(call: str, ws, device: int):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+_gpu = None
+
+
 def _current(call: str, stream):
-    """(device, stream handle) of a call."""
-    device = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    """(device, stream handle) of a call; device -1 without a GPU."""
+    global _gpu
+    if _gpu is None:
+        _gpu = torch.cuda.is_available()
+    device = torch.cuda.current_device() if _gpu else -1
     if stream is None:
-        return device, torch.cuda.current_stream().cuda_stream if device >= 0 else None
+        # the handle alone: building a torch.cuda.Stream for it takes 2.8 us
+        return device, torch._C._cuda_getCurrentRawStream(device) if _gpu else None
     if isinstance(stream, int):
         return device, stream
     if stream.device.index != device:
@@ -361,17 +368,14 @@ class GradList:
             _refuse(c, f"{len(out)} outputs for {len(grads)} gradients")
         kind = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
         flat = []
-        self.device = None
+        self.device = grads[0].get_device() if grads else None
         for g, o in zip(grads, out):
             code = kind.get(g.dtype)
             if code is None:
                 raise MoEError(c, MOE_ERR_UNSUPPORTED, f"a gradient is {g.dtype}, not float32 or bfloat16")
-            n = g.numel()
+            n, dev = g.numel(), g.get_device()
             if not g.is_contiguous():
                 _refuse(c, "a gradient is not contiguous")
-            dev = g.get_device()
-            if self.device is None:
-                self.device = dev
             if dev != self.device:
                 _refuse(c, "the gradients are on more than one device")
             if o is not g and (o.dtype is not g.dtype or o.numel() != n or not o.is_contiguous()

@@ -17,10 +17,12 @@
 // are centred on their mean (exactly, in integers), which leaves no
 // cancellation for a load near balance.
 //
-// Both passes read the [T][E] logits once and are bound by that read; small
-// batches by the launches.  A row is held by a group of L lanes (L the
-// smallest power of two that covers it, at most a wave), so several short
-// rows share a wave and every lane of a load carries a logit.
+// Both passes read the [T][E] logits once; small batches are bound by the
+// launches, large ones by that read and the exponentials (a quarter of the
+// rate of other instructions).  A row lies on a group of L lanes with up to
+// 16 logits each: the fewer lanes a row has, the fewer steps its maximum and
+// sum take, and the several rows of a wave share each step; L is at least
+// four where E allows, so that a load covers 64 consecutive bytes of a row.
 #include <algorithm>
 
 #include "moe_device.h"
@@ -29,22 +31,47 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / kWave;
+constexpr int kMaxRowBlocks = 512;
 
 // A row of E logits on L lanes: lane g holds elements (c L + g) V + v,
 // c < C, v < V (V = 4: 16-byte loads, E a multiple of 4).
-template <int V, int L, int C>
-__device__ __forceinline__ int row_elem(int g, int q) {
-  return ((q / V) * L + g) * V + q % V;
+template <int V_, int L_, int C_>
+struct RowShape {
+  static constexpr int V = V_, L = L_, C = C_;
+  static constexpr int Q = C * V;       // logits of a lane
+  static constexpr int R = kWave / L;   // rows of a wave
+  __device__ static int elem(int g, int q) { return ((q / V) * L + g) * V + q % V; }
+};
+
+template <class F>
+void with_row_shape(int E, F f) {
+  if (E % 4 == 0) {
+    if (E <= 4) return f(RowShape<4, 1, 1>{});
+    if (E <= 8) return f(RowShape<4, 2, 1>{});
+    if (E <= 16) return f(RowShape<4, 4, 1>{});
+    if (E <= 32) return f(RowShape<4, 4, 2>{});
+    if (E <= 64) return f(RowShape<4, 4, 4>{});
+    if (E <= 128) return f(RowShape<4, 8, 4>{});
+    if (E <= 256) return f(RowShape<4, 16, 4>{});
+    return f(RowShape<4, 32, 4>{});
+  }
+  if (E <= 4) return f(RowShape<1, 4, 1>{});
+  if (E <= 16) return f(RowShape<1, 16, 1>{});
+  if (E <= 32) return f(RowShape<1, 16, 2>{});
+  if (E <= 64) return f(RowShape<1, 16, 4>{});
+  if (E <= 128) return f(RowShape<1, 16, 8>{});
+  if (E <= 256) return f(RowShape<1, 16, 16>{});
+  return f(RowShape<1, 32, 16>{});
 }
 
-template <int V, int L, int C>
-__device__ __forceinline__ void load_row(const float* row, int E, int g, float (&v)[C * V]) {
+template <class S>
+__device__ __forceinline__ void load_row(const float* row, int E, int g, float (&v)[S::Q]) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int e = (c * L + g) * V;
-    if constexpr (V == 4) {
+  for (int c = 0; c < S::C; ++c) {
+    const int e = (c * S::L + g) * S::V;
+    if constexpr (S::V == 4) {
       f32x4_t r = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       if (e < E) r = *reinterpret_cast<const f32x4_t*>(row + e);
 #pragma unroll
@@ -55,43 +82,78 @@ __device__ __forceinline__ void load_row(const float* row, int E, int g, float (
   }
 }
 
+// Reduction over the aligned groups of L lanes; every lane gets the result
+// (the steps pair equal partial results, so all lanes have the same bits).
+// Up to 16 lanes by DPP: exchanges inside quads, then mirrors of 8 and 16.
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xF, 0xF, false));
+}
+
+template <int L, class F>
+__device__ __forceinline__ float group_reduce(float v, F f) {
+  if constexpr (L >= 2) v = f(v, dpp<0xB1>(v));
+  if constexpr (L >= 4) v = f(v, dpp<0x4E>(v));
+  if constexpr (L >= 8) v = f(v, dpp<0x141>(v));
+  if constexpr (L >= 16) v = f(v, dpp<0x140>(v));
+  if constexpr (L >= 32) v = f(v, __shfl_xor(v, 16, kWave));
+  return v;
+}
 template <int L>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int o = L / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o, kWave);
-  return v;
+  return group_reduce<L>(v, [](float a, float b) { return a + b; });
 }
-
 template <int L>
 __device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int o = L / 2; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
-  return v;
+  return group_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// Logits -> softmax in place; returns the log-sum-exp.  A row of -inf only
-// gives p = 0 and 0; a NaN or +inf makes the whole row NaN (the maximum drops
-// NaN, the sum does not).  The exponential is the hardware one: its argument
-// is at most 0, and its absolute error is below 2^-22 of the largest term.
-template <int Q, int L>
-__device__ __forceinline__ float row_softmax(float (&v)[Q]) {
+// Logits -> exponentials of the softmax, in place; returns the log-sum-exp,
+// and `inv`, the factor that makes them probabilities.  A row of -inf only
+// gives zeros; a NaN or +inf makes the whole row NaN (the maximum drops NaN,
+// the sum does not).  The exponential is the hardware one: its argument is at
+// most 0, and its absolute error is below 2^-22 of the largest term.
+template <class S>
+__device__ __forceinline__ float row_exp(float (&v)[S::Q], float& inv) {
   float m = v[0];
 #pragma unroll
-  for (int q = 1; q < Q; ++q) m = fmaxf(m, v[q]);
-  m = group_max<L>(m);
+  for (int q = 1; q < S::Q; ++q) m = fmaxf(m, v[q]);
+  m = group_max<S::L>(m);
   const float base = m == -INFINITY ? 0.0f : m;
   float s = 0.0f;
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
+  for (int q = 0; q < S::Q; ++q) {
     v[q] = __expf(v[q] - base);
     s += v[q];
   }
-  s = group_sum<L>(s);
+  s = group_sum<S::L>(s);
   const bool dead = s == 0.0f;
-  const float inv = dead ? 0.0f : 1.0f / s;
-#pragma unroll
-  for (int q = 0; q < Q; ++q) v[q] *= inv;
+  inv = dead ? 0.0f : 1.0f / s;
   return dead ? 0.0f : base + logf(s);
+}
+
+// Column sums of a workgroup: the lanes' sums acc over their rows, added over
+// the rows of a wave by lane exchanges and over the waves through LDS
+// (red [kWaves][E], filled here; sums in float64 by col_total after a
+// barrier), all in a fixed order.
+template <class S>
+__device__ __forceinline__ void col_partials(float (&acc)[S::Q], int E, float* red) {
+  const int l = threadIdx.x % kWave, w = threadIdx.x / kWave;
+  const int g = l % S::L;
+#pragma unroll
+  for (int q = 0; q < S::Q; ++q) {
+#pragma unroll
+    for (int o = S::L; o < kWave; o *= 2) acc[q] += __shfl_xor(acc[q], o, kWave);
+    const int e = S::elem(g, q);
+    if (l < S::L && e < E) red[w * E + e] = acc[q];
+  }
+}
+__device__ __forceinline__ double col_total(const float* red, int E, int e) {
+  double s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) s += red[w * E + e];
+  return s;
 }
 
 // One expert's share of a workgroup's partial sums.
@@ -119,70 +181,72 @@ struct BalanceArgs {
   int nb;
 };
 
-// Sum of a double over the workgroup (fixed order); every thread gets it.
-__device__ __forceinline__ double block_sum(double v, double* lds) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, kWave);
-  const int w = threadIdx.x / kWave;
-  __syncthreads();
-  if (lane_id() == 0) lds[w] = v;
-  __syncthreads();
-  double s = 0.0;
-  for (int i = 0; i < (int)blockDim.x / kWave; ++i) s += lds[i];
-  return s;
-}
-
 // First pass: workgroup b sums the softmax rows, the squared log-sum-exps and
 // the slots per expert of its consecutive rows.  kSolo: the only workgroup,
 // which also forms the results.
-template <int V, int L, int C, bool kSolo>
+template <class S, bool kSolo>
 __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
-  constexpr int Q = C * V;
-  constexpr int R = kWave / L;  // rows of a wave
-  __shared__ float red[kThreads * Q];
+  __shared__ float red[kWaves * kMaxExperts];
   __shared__ int hist[kMaxExperts];
-  __shared__ double wsum[kWaves];
+  __shared__ double wz[kWaves];
+  __shared__ int wn[kWaves];
   const int tid = threadIdx.x;
   const int w = tid / kWave, l = tid % kWave;
-  const int g = l % L, r = l / L;
+  const int g = l % S::L, r = l / S::L;
   const long long t0 = blockIdx.x * a.rows_per_block;
-  const long long t1 = min(t0 + a.rows_per_block, a.T);
+  const int rows = (int)min((long long)a.rows_per_block, a.T - t0);
+  const float* logits = a.logits + t0 * a.E;
+  const int32_t* idx = a.idx + t0 * a.k;
+  const uint8_t* mask = a.mask ? a.mask + t0 : nullptr;
   for (int e = tid; e < a.E; e += kThreads) hist[e] = 0;
   if (!kSolo && blockIdx.x == 0 && tid == 0) *a.ticket = 0;
   __syncthreads();
   // slots per expert: integer sums, so the order of the atomics is free
-  for (long long s = t0 * a.k + tid; s < t1 * a.k; s += kThreads) {
-    if (a.mask && a.mask[s / a.k] == 0) continue;
-    const int e = a.idx[s];
+  const long long slots = (long long)rows * a.k;
+  for (long long s = tid; s < slots; s += kThreads) {
+    if (mask && mask[slots < (1LL << 31) ? (uint32_t)s / (uint32_t)a.k : s / a.k] == 0) continue;
+    const int e = idx[s];
     if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
   }
-  float acc[Q];
+  float acc[S::Q];
 #pragma unroll
-  for (int q = 0; q < Q; ++q) acc[q] = 0.0f;
+  for (int q = 0; q < S::Q; ++q) acc[q] = 0.0f;
   double z = 0.0;
   int n = 0;
-  for (long long t = t0 + w * R + r; t < t1; t += kWaves * R) {
-    if (a.mask && a.mask[t] == 0) continue;  // the same for the group's lanes
-    float v[Q];
-    load_row<V, L, C>(a.logits + t * a.E, a.E, g, v);
-    const float lse = row_softmax<Q, L>(v);
+  for (int t = w * S::R + r; t < rows; t += kWaves * S::R) {
+    if (mask && mask[t] == 0) continue;  // the same for the group's lanes
+    float v[S::Q], inv;
+    load_row<S>(logits + (long long)t * a.E, a.E, g, v);
+    const float lse = row_exp<S>(v, inv);
 #pragma unroll
-    for (int q = 0; q < Q; ++q) acc[q] += v[q];
+    for (int q = 0; q < S::Q; ++q) acc[q] = fmaf(v[q], inv, acc[q]);
     if (g == 0) {
       z += (double)lse * lse;
       ++n;
     }
   }
+  col_partials<S>(acc, a.E, red);
 #pragma unroll
-  for (int q = 0; q < Q; ++q) red[((w * R + r) * Q + q) * L + g] = acc[q];
-  const double zsum = block_sum(z, wsum);
-  const int nsum = (int)block_sum((double)n, wsum);
+  for (int o = 32; o >= 1; o >>= 1) {
+    z += __shfl_xor(z, o, kWave);
+    n += __shfl_xor(n, o, kWave);
+  }
+  if (l == 0) {
+    wz[w] = z;
+    wn[w] = n;
+  }
+  __syncthreads();
+  z = 0.0;
+  n = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    z += wz[i];
+    n += wn[i];
+  }
+  const double inv_n = n > 0 ? 1.0 / n : 0.0;
   double bal = 0.0;
-  const double inv_n = nsum > 0 ? 1.0 / nsum : 0.0;
-  for (int e = tid; e < a.E; e += kThreads) {
-    const int q = e / (L * V) * V + e % V, gg = e / V % L;
-    double s = 0.0;
-    for (int i = 0; i < kWaves * R; ++i) s += red[(i * Q + q) * L + gg];
+  for (int e = tid; e < a.E; e += kThreads) {  // (at most one: E <= kThreads)
+    const double s = col_total(red, a.E, e);
     if constexpr (kSolo) {
       a.counts[e] = hist[e];
       a.prob_mean[e] = (float)(s * inv_n);
@@ -192,79 +256,107 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
     }
   }
   if constexpr (kSolo) {
-    bal = block_sum(bal, wsum);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) bal += __shfl_xor(bal, o, kWave);
+    __syncthreads();  // wz has been read
+    if (l == 0) wz[w] = bal;
+    __syncthreads();
     if (tid == 0) {
-      *a.n_tokens = nsum;
+      bal = 0.0;
+      for (int i = 0; i < kWaves; ++i) bal += wz[i];
+      *a.n_tokens = n;
       a.losses[0] = (float)(bal * a.E / a.k * inv_n);
-      a.losses[1] = (float)(zsum * inv_n);
+      a.losses[1] = (float)(z * inv_n);
     }
   } else if (tid == 0) {
-    a.zpart[blockIdx.x] = zsum;
-    a.npart[blockIdx.x] = nsum;
+    a.zpart[blockIdx.x] = z;
+    a.npart[blockIdx.x] = n;
   }
 }
 
-// Second pass: workgroup j adds the partial sums of 32 experts (32 threads
-// abreast, 32 partials at a time) in a fixed order; the last one to arrive
-// adds the workgroups' shares of the loss, again in a fixed order.
+// Second pass: workgroup j adds the partial sums of 16 experts, 64 of them
+// abreast, in a fixed order; the last one to arrive adds the workgroups'
+// shares of the loss, again in a fixed order.
 constexpr int kFinThreads = 1024;
-constexpr int kFinCols = 32;
+constexpr int kFinCols = 16;
+constexpr int kFinRows = kFinThreads / kFinCols;
+constexpr int kFinWaves = kFinThreads / kWave;
 
 __global__ __launch_bounds__(kFinThreads) void balance_finish(BalanceArgs a) {
-  constexpr int kRows = kFinThreads / kFinCols;
-  __shared__ double sp[kRows][kFinCols];
-  __shared__ int sc[kRows][kFinCols];
-  __shared__ double wsum[kFinThreads / kWave];
-  __shared__ bool last;
+  __shared__ double sp[kFinWaves][kFinCols];
+  __shared__ int sc[kFinWaves][kFinCols];
+  __shared__ double wz[kFinWaves];
+  __shared__ int wn[kFinWaves];
   const int tid = threadIdx.x;
+  const int w = tid / kWave, l = tid % kWave;
   const int j = tid % kFinCols, r = tid / kFinCols;
   const int e = blockIdx.x * kFinCols + j;
+  static_assert(kMaxRowBlocks <= kFinThreads && kMaxRowBlocks % kFinRows == 0, "one load each");
+  double z = tid < a.nb ? a.zpart[tid] : 0.0;
+  int n = tid < a.nb ? a.npart[tid] : 0;
+  ColPart v[kMaxRowBlocks / kFinRows];  // all loads at once
+#pragma unroll
+  for (int i = 0; i < kMaxRowBlocks / kFinRows; ++i) {
+    const int b = r + i * kFinRows;
+    v[i] = ColPart{0.0f, 0};
+    if (b < a.nb && e < a.E) v[i] = a.part[(size_t)b * a.E + e];
+  }
   double p = 0.0;
   int c = 0;
-  if (e < a.E) {
-    for (int b = r; b < a.nb; b += kRows) {
-      const ColPart v = a.part[(size_t)b * a.E + e];
-      p += v.p;
-      c += v.c;
-    }
+#pragma unroll
+  for (int i = 0; i < kMaxRowBlocks / kFinRows; ++i) {
+    p += v[i].p;
+    c += v[i].c;
   }
-  sp[r][j] = p;
-  sc[r][j] = c;
-  int n = 0;
-  double z = 0.0;
-  for (int b = tid; b < a.nb; b += kFinThreads) {
-    n += a.npart[b];
-    z += a.zpart[b];
+#pragma unroll
+  for (int o = kFinCols; o < kWave; o *= 2) {
+    p += __shfl_xor(p, o, kWave);
+    c += __shfl_xor(c, o, kWave);
   }
-  const int nsum = (int)block_sum((double)n, wsum);
-  const double zsum = block_sum(z, wsum);
-  const double inv_n = nsum > 0 ? 1.0 / nsum : 0.0;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    z += __shfl_xor(z, o, kWave);
+    n += __shfl_xor(n, o, kWave);
+  }
+  if (l < kFinCols) {
+    sp[w][l] = p;
+    sc[w][l] = c;
+  }
+  if (l == 0) {
+    wz[w] = z;
+    wn[w] = n;
+  }
+  __syncthreads();
+  if (w != 0) return;
+  p = z = 0.0;
+  c = n = 0;
+#pragma unroll
+  for (int i = 0; i < kFinWaves; ++i) {
+    p += sp[i][j];
+    c += sc[i][j];
+    z += wz[i];
+    n += wn[i];
+  }
+  const double inv_n = n > 0 ? 1.0 / n : 0.0;
   double bal = 0.0;
-  if (r == 0 && e < a.E) {
-    p = 0.0;
-    c = 0;
-    for (int i = 0; i < kRows; ++i) {
-      p += sp[i][j];
-      c += sc[i][j];
-    }
+  if (l < kFinCols && e < a.E) {
     a.counts[e] = c;
     a.prob_mean[e] = (float)(p * inv_n);
     bal = c * (p * inv_n);
   }
-  bal = block_sum(bal, wsum);
-  if (tid == 0) {
-    __hip_atomic_store(&a.lpart[blockIdx.x], bal, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-           (int)gridDim.x - 1;
-    if (last) {
-      double s = 0.0;
-      for (unsigned i = 0; i < gridDim.x; ++i)
-        s += __hip_atomic_load(&a.lpart[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      *a.n_tokens = nsum;
-      a.losses[0] = (float)(s * a.E / a.k * inv_n);
-      a.losses[1] = (float)(zsum * inv_n);
-    }
-  }
+#pragma unroll
+  for (int o = kFinCols / 2; o >= 1; o >>= 1) bal += __shfl_xor(bal, o, kWave);
+  if (l != 0) return;
+  __hip_atomic_store(&a.lpart[blockIdx.x], bal, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const int arrived =
+      __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+  if (arrived != (int)gridDim.x - 1) return;
+  double s = 0.0;
+  for (unsigned i = 0; i < gridDim.x; ++i)
+    s += __hip_atomic_load(&a.lpart[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  *a.n_tokens = n;
+  a.losses[0] = (float)(s * a.E / a.k * inv_n);
+  a.losses[1] = (float)(z * inv_n);
 }
 
 // ---- gradient with respect to the logits
@@ -288,38 +380,48 @@ __device__ __forceinline__ uint16_t split_bf16(float& v) {
 // Workgroup b: consecutive rows.  Writes the float32 gradient, its split into
 // `nplanes` bfloat16 planes [T][Ep] (their sum is the value: three hold all 24
 // bits; columns E .. Ep - 1 are zero), and the workgroup's column sums.
-template <int V, int L, int C>
+//
+// The gates' gradient has k values of a row's E.  Lane j of the row's group
+// forms that of slot j (then j + L, ...) and adds it to a row of zeros in LDS
+// (wave-private; the additions of one instruction to one address are made in
+// lane order, and the LDS keeps a wave's instructions in order), from which
+// every lane picks its logits' values; comparing every logit with every id
+// instead took 2 k instructions a logit.
+template <class S>
 __global__ __launch_bounds__(kThreads) void gate_grad_rows(GateGradKernelArgs ka) {
-  constexpr int Q = C * V;
-  constexpr int R = kWave / L;
-  __shared__ float red[kThreads * Q];
+  __shared__ float red[kWaves * kMaxExperts];
+  __shared__ __align__(16) float sparse[kWaves * kWave * S::Q];  // [wave][row][L Q >= E]
   __shared__ int wtot[kWaves];
   const GateGradArgs& a = ka.a;
   const int E = ka.E, k = ka.k;
   const int tid = threadIdx.x;
   const int w = tid / kWave, l = tid % kWave;
-  const int g = l % L, r = l / L;
+  const int g = l % S::L, r = l / S::L;
   const bool losses = a.dlosses != nullptr;
-  float cen[Q];  // centred counts
+  float* srow = sparse + (w * S::R + r) * (S::L * S::Q);
+  float cen[S::Q];  // centred counts
   float ca = 0.0f, cz = 0.0f;
 #pragma unroll
-  for (int q = 0; q < Q; ++q) cen[q] = 0.0f;
+  for (int q = 0; q < S::Q; ++q) {
+    cen[q] = 0.0f;
+    srow[S::elem(g, q)] = 0.0f;
+  }
   if (losses) {
-    // the sum of the counts, in integers (below 2^31 slots)
-    int s = 0;
-    for (int e = tid; e < E; e += kThreads) s += a.counts[e];
+    // the sum of the counts, in integers
+    int s = tid < E ? a.counts[tid] : 0;
+    const int n = *a.n_tokens;
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, kWave);
     if (l == 0) wtot[w] = s;
     __syncthreads();
     long long total = 0;
+#pragma unroll
     for (int i = 0; i < kWaves; ++i) total += wtot[i];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int e = row_elem<V, L, C>(g, q);
+    for (int q = 0; q < S::Q; ++q) {
+      const int e = S::elem(g, q);
       if (e < E) cen[q] = (float)((double)((long long)a.counts[e] * E - total) / E);
     }
-    const int n = *a.n_tokens;
     if (n > 0) {
       ca = (float)((double)a.dlosses[0] * E / ((double)n * n * k));
       cz = (float)((double)a.dlosses[1] * 2.0 / n);
@@ -327,49 +429,66 @@ __global__ __launch_bounds__(kThreads) void gate_grad_rows(GateGradKernelArgs ka
   }
   if (blockIdx.x == 0 && tid < kZeroLineBytes / 4)
     reinterpret_cast<uint32_t*>(a.zero_line)[tid] = 0;
-  float colsum[Q];
+  float colsum[S::Q];
 #pragma unroll
-  for (int q = 0; q < Q; ++q) colsum[q] = 0.0f;
+  for (int q = 0; q < S::Q; ++q) colsum[q] = 0.0f;
   const long long t0 = blockIdx.x * ka.rows_per_block;
   const long long t1 = min(t0 + ka.rows_per_block, ka.T);
-  for (long long t = t0 + w * R + r; t < t1; t += kWaves * R) {
-    float v[Q];
+  for (long long t = t0 + w * S::R + r; t < t1; t += kWaves * S::R) {
+    float v[S::Q];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) v[q] = 0.0f;
+    for (int q = 0; q < S::Q; ++q) v[q] = 0.0f;
     if (!a.mask || a.mask[t] != 0) {
+      float gmean = 0.0f;
+      if (a.dtopk_w) {
+        for (int j = g; j < k; j += S::L)
+          if ((unsigned)a.idx[t * k + j] < (unsigned)E)
+            gmean = fmaf(a.topk_w[t * k + j], a.dtopk_w[t * k + j], gmean);
+        gmean = group_sum<S::L>(gmean);
+        for (int j = g; j < k; j += S::L) {
+          const int e = a.idx[t * k + j];
+          if ((unsigned)e < (unsigned)E)
+            unsafeAtomicAdd(&srow[e], a.topk_w[t * k + j] * (a.dtopk_w[t * k + j] - gmean));
+        }
+      }
       if (losses) {
-        load_row<V, L, C>(a.logits + t * E, E, g, v);
-        const float lse = row_softmax<Q, L>(v);
+        float inv;
+        load_row<S>(a.logits + t * E, E, g, v);
+        const float lse = row_exp<S>(v, inv);
         float mean = 0.0f;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) mean = fmaf(v[q], cen[q], mean);
-        mean = group_sum<L>(mean);
+        for (int q = 0; q < S::Q; ++q) mean = fmaf(v[q], cen[q], mean);
+        mean = group_sum<S::L>(mean) * inv;
         const float zl = cz * lse;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) v[q] *= fmaf(ca, cen[q] - mean, zl);
+        for (int q = 0; q < S::Q; ++q) v[q] = v[q] * inv * fmaf(ca, cen[q] - mean, zl);
       }
       if (a.dtopk_w) {
-        const int32_t* id = a.idx + t * k;
-        const float* gw = a.topk_w + t * k;
-        const float* dg = a.dtopk_w + t * k;
-        float mean = 0.0f;
-        for (int i = 0; i < k; ++i)
-          if ((unsigned)id[i] < (unsigned)E) mean = fmaf(gw[i], dg[i], mean);
-        for (int i = 0; i < k; ++i) {
-          const int e = id[i];
-          const float d = gw[i] * (dg[i] - mean);
+        asm volatile("" ::: "memory");
 #pragma unroll
-          for (int q = 0; q < Q; ++q)
-            if (e == row_elem<V, L, C>(g, q) && e < E) v[q] += d;
+        for (int c = 0; c < S::C; ++c) {
+          if constexpr (S::V == 4) {
+            const f32x4_t x = *reinterpret_cast<const f32x4_t*>(srow + (c * S::L + g) * 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[c * 4 + i] += x[i];
+          } else {
+            v[c] += srow[c * S::L + g];
+          }
         }
+        asm volatile("" ::: "memory");
+        for (int j = g; j < k; j += S::L) {
+          const int e = a.idx[t * k + j];
+          if ((unsigned)e < (unsigned)E) srow[e] = 0.0f;
+        }
+        asm volatile("" ::: "memory");
       }
     }
 #pragma unroll
-    for (int q = 0; q < Q; ++q) colsum[q] += v[q];
+    for (int q = 0; q < S::Q; ++q) colsum[q] += v[q];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int e = (c * L + g) * V;
-      if constexpr (V == 4) {
+    for (int c = 0; c < S::C; ++c) {
+      const int e = (c * S::L + g) * S::V;
+      if constexpr (S::V == 4) {
         if (a.dlogits && e < E)
           *reinterpret_cast<f32x4_t*>(a.dlogits + t * E + e) =
               f32x4_t{v[c * 4], v[c * 4 + 1], v[c * 4 + 2], v[c * 4 + 3]};
@@ -380,70 +499,39 @@ __global__ __launch_bounds__(kThreads) void gate_grad_rows(GateGradKernelArgs ka
     for (int pl = 0; pl < a.nplanes; ++pl) {
       uint16_t* row = a.planes + ((size_t)pl * ka.T + t) * ka.Ep;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int e = (c * L + g) * V;
-        if constexpr (V == 4) {
-          u32x2_t o;
+      for (int c = 0; c < S::C; ++c) {
+        const int e = (c * S::L + g) * S::V;
+        if constexpr (S::V == 4) {
           uint16_t h[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) h[i] = split_bf16(v[c * 4 + i]);
-          o[0] = h[0] | (uint32_t(h[1]) << 16);
-          o[1] = h[2] | (uint32_t(h[3]) << 16);
-          if (e < E) *reinterpret_cast<u32x2_t*>(row + e) = o;
+          if (e < E)
+            *reinterpret_cast<u32x2_t*>(row + e) =
+                u32x2_t{h[0] | (uint32_t(h[1]) << 16), h[2] | (uint32_t(h[3]) << 16)};
         } else {
           const uint16_t h = split_bf16(v[c]);
           if (e < E) row[e] = h;
         }
       }
-      for (int e = E + g; e < ka.Ep; e += L) row[e] = 0;
+      for (int e = E + g; e < ka.Ep; e += S::L) row[e] = 0;
     }
   }
   if (!a.bias_part) return;
-#pragma unroll
-  for (int q = 0; q < Q; ++q) red[((w * R + r) * Q + q) * L + g] = colsum[q];
+  col_partials<S>(colsum, E, red);
   __syncthreads();
-  for (int e = tid; e < E; e += kThreads) {
-    const int q = e / (L * V) * V + e % V, gg = e / V % L;
-    double s = 0.0;
-    for (int i = 0; i < kWaves * R; ++i) s += red[(i * Q + q) * L + gg];
-    a.bias_part[(size_t)blockIdx.x * E + e] = (float)s;
-  }
+  for (int e = tid; e < E; e += kThreads)
+    a.bias_part[(size_t)blockIdx.x * E + e] = (float)col_total(red, E, e);
 }
 
-// Row groups for E experts: calls f with the lanes, vector width and chunks
-// as compile-time constants.
-template <int V, int L, int C>
-struct RowShape {
-  static constexpr int v = V, l = L, c = C;
-};
-
-template <class F>
-void with_row_shape(int E, F f) {
-  if (E % 4 == 0) {
-    const int n = E / 4;
-    if (n <= 1) return f(RowShape<4, 1, 1>{});
-    if (n <= 2) return f(RowShape<4, 2, 1>{});
-    if (n <= 4) return f(RowShape<4, 4, 1>{});
-    if (n <= 8) return f(RowShape<4, 8, 1>{});
-    if (n <= 16) return f(RowShape<4, 16, 1>{});
-    if (n <= 32) return f(RowShape<4, 32, 1>{});
-    if (n <= 64) return f(RowShape<4, 64, 1>{});
-    return f(RowShape<4, 64, 2>{});
-  }
-  if (E <= 4) return f(RowShape<1, 4, 1>{});
-  if (E <= 16) return f(RowShape<1, 16, 1>{});
-  if (E <= 32) return f(RowShape<1, 32, 1>{});
-  if (E <= 64) return f(RowShape<1, 64, 1>{});
-  if (E <= 128) return f(RowShape<1, 64, 2>{});
-  if (E <= 256) return f(RowShape<1, 64, 4>{});
-  return f(RowShape<1, 64, 8>{});
-}
-
-// Workgroups of the row kernels: at least 16 rows each, at most 512.
-int row_blocks(long long T, long long* rows_per_block) {
-  const long long nb = std::min<long long>(std::max<long long>((T + 15) / 16, 1), 512);
-  *rows_per_block = std::max<long long>((T + nb - 1) / nb, 1);
-  return (int)std::max<long long>((T + *rows_per_block - 1) / *rows_per_block, 1);
+// Workgroups of the row kernels: whole passes of the workgroup's waves, as
+// many workgroups as there are passes up to kMaxRowBlocks.
+int row_blocks(long long T, int E, long long* rows_per_block) {
+  long long pass = 0;
+  with_row_shape(E, [&](auto sh) { pass = kWaves * decltype(sh)::R; });
+  const long long passes = std::max<long long>((T + pass - 1) / pass, 1);
+  const long long each = (passes + kMaxRowBlocks - 1) / kMaxRowBlocks;
+  *rows_per_block = each * pass;
+  return (int)((passes + each - 1) / each);
 }
 
 struct BalanceLayout {
@@ -453,7 +541,7 @@ struct BalanceLayout {
 BalanceLayout balance_layout(const Shape& s) {
   BalanceLayout L{};
   long long rows;
-  const int nb = row_blocks(s.T, &rows);
+  const int nb = row_blocks(s.T, s.E, &rows);
   size_t o = 0;
   auto take = [&o](size_t bytes) {
     const size_t at = o;
@@ -485,7 +573,7 @@ hipError_t balance_loss(const Shape& s, const float* logits, const int32_t* topk
   a.T = s.T;
   a.E = s.E;
   a.k = s.k;
-  a.nb = row_blocks(s.T, &a.rows_per_block);
+  a.nb = row_blocks(s.T, s.E, &a.rows_per_block);
   a.part = reinterpret_cast<ColPart*>(base + lay.part);
   a.zpart = reinterpret_cast<double*>(base + lay.zpart);
   a.npart = reinterpret_cast<int*>(base + lay.npart);
@@ -498,9 +586,9 @@ hipError_t balance_loss(const Shape& s, const float* logits, const int32_t* topk
   with_row_shape(s.E, [&](auto sh) {
     using S = decltype(sh);
     if (a.nb == 1)
-      hipLaunchKernelGGL((balance_rows<S::v, S::l, S::c, true>), dim3(1), dim3(kThreads), 0, st, a);
+      hipLaunchKernelGGL((balance_rows<S, true>), dim3(1), dim3(kThreads), 0, st, a);
     else
-      hipLaunchKernelGGL((balance_rows<S::v, S::l, S::c, false>), dim3(a.nb), dim3(kThreads), 0,
+      hipLaunchKernelGGL((balance_rows<S, false>), dim3(a.nb), dim3(kThreads), 0,
                          st, a);
   });
   if (a.nb > 1)
@@ -511,7 +599,7 @@ hipError_t balance_loss(const Shape& s, const float* logits, const int32_t* topk
 
 int gate_grad_blocks(const Shape& s) {
   long long rows;
-  return row_blocks(s.T, &rows);
+  return row_blocks(s.T, s.E, &rows);
 }
 
 hipError_t gate_grad(const Shape& s, const GateGradArgs& a, int Ep, hipStream_t st) {
@@ -521,10 +609,10 @@ hipError_t gate_grad(const Shape& s, const GateGradArgs& a, int Ep, hipStream_t 
   ka.E = s.E;
   ka.k = s.k;
   ka.Ep = Ep;
-  const int nb = row_blocks(s.T, &ka.rows_per_block);
+  const int nb = row_blocks(s.T, s.E, &ka.rows_per_block);
   with_row_shape(s.E, [&](auto sh) {
     using S = decltype(sh);
-    hipLaunchKernelGGL((gate_grad_rows<S::v, S::l, S::c>), dim3(nb), dim3(kThreads), 0, st, ka);
+    hipLaunchKernelGGL((gate_grad_rows<S>), dim3(nb), dim3(kThreads), 0, st, ka);
   });
   return hipGetLastError();
 }

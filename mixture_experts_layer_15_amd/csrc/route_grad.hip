@@ -509,28 +509,38 @@ struct SumArgs {
   int nb, E;
 };
 
-__global__ __launch_bounds__(kThreads) void router_grad_sum(SumArgs a) {
+constexpr int kSumThreads = 512;
+constexpr int kSumCols = 16;
+
+__global__ __launch_bounds__(kSumThreads) void router_grad_sum(SumArgs a) {
   if ((int)blockIdx.x < a.w_blocks) {
-    const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * 4;
+    const long long i = ((long long)blockIdx.x * kSumThreads + threadIdx.x) * 4;
     if (i >= a.n) return;
     f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int p = 0; p < a.splits; ++p)
       s += *reinterpret_cast<const f32x4_t*>(a.part + (size_t)p * a.n + i);
     *reinterpret_cast<f32x4_t*>(a.dw + i) = s;
     return;
   }
-  // 32 experts, eight partials abreast
-  __shared__ double sp[8][32];
-  const int j = threadIdx.x % 32, r = threadIdx.x / 32;
-  const int e = ((int)blockIdx.x - a.w_blocks) * 32 + j;
+  // 16 experts, 32 partials abreast
+  constexpr int kRows = kSumThreads / kSumCols;
+  __shared__ double sp[kSumThreads / kWave][kSumCols];
+  const int j = threadIdx.x % kSumCols, r = threadIdx.x / kSumCols;
+  const int w = threadIdx.x / kWave, l = threadIdx.x % kWave;
+  const int e = ((int)blockIdx.x - a.w_blocks) * kSumCols + j;
   double s = 0.0;
-  if (e < a.E)
-    for (int b = r; b < a.nb; b += 8) s += a.bias_part[(size_t)b * a.E + e];
-  sp[r][j] = s;
+  if (e < a.E) {
+#pragma unroll 16
+    for (int b = r; b < a.nb; b += kRows) s += a.bias_part[(size_t)b * a.E + e];
+  }
+#pragma unroll
+  for (int o = kSumCols; o < kWave; o *= 2) s += __shfl_xor(s, o, kWave);
+  if (l < kSumCols) sp[w][l] = s;
   __syncthreads();
   if (r == 0 && e < a.E) {
     s = 0.0;
-    for (int i = 0; i < 8; ++i) s += sp[i][j];
+    for (int i = 0; i < kSumThreads / kWave; ++i) s += sp[i][j];
     a.dbias[e] = (float)s;
   }
 }
@@ -659,13 +669,13 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
     a.dw = g.dw;
     a.n = (long long)s.d * s.E;
     a.splits = s.T == 0 ? 0 : ns;
-    a.w_blocks = sum_w ? (int)((a.n / 4 + kThreads - 1) / kThreads) : 0;
+    a.w_blocks = sum_w ? (int)((a.n / 4 + kSumThreads - 1) / kSumThreads) : 0;
     a.bias_part = bias_part;
     a.dbias = g.dbias;
     a.nb = s.T == 0 ? 0 : gate_grad_blocks(s);
     a.E = s.E;
-    hipLaunchKernelGGL(router_grad_sum, dim3(a.w_blocks + (g.dbias ? (s.E + 31) / 32 : 0)),
-                       dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL(router_grad_sum, dim3(a.w_blocks + (g.dbias ? (s.E + kSumCols - 1) / kSumCols : 0)),
+                       dim3(kSumThreads), 0, st, a);
   }
   if (g.dx && s.T > 0 && bf16) {
     const uint16_t* w = static_cast<const uint16_t*>(g.w_router);
