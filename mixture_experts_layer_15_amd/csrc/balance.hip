@@ -31,9 +31,12 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;      // of the balance loss
 constexpr int kWaves = kThreads / kWave;
 constexpr int kMaxRowBlocks = 512;
+constexpr int kGradThreads = 256;  // of the gradient
+constexpr int kGradWaves = kGradThreads / kWave;
+constexpr int kMaxGradBlocks = 1024;
 
 // A row of E logits on L lanes: lane g holds elements (c L + g) V + v,
 // c < C, v < V (V = 4: 16-byte loads, E a multiple of 4).
@@ -135,7 +138,7 @@ __device__ __forceinline__ float row_exp(float (&v)[S::Q], float& inv) {
 
 // Column sums of a workgroup: the lanes' sums acc over their rows, added over
 // the rows of a wave by lane exchanges and over the waves through LDS
-// (red [kWaves][E], filled here; sums in float64 by col_total after a
+// (red [waves][E], filled here; sums in float64 by col_total after a
 // barrier), all in a fixed order.
 template <class S>
 __device__ __forceinline__ void col_partials(float (&acc)[S::Q], int E, float* red) {
@@ -149,10 +152,11 @@ __device__ __forceinline__ void col_partials(float (&acc)[S::Q], int E, float* r
     if (l < S::L && e < E) red[w * E + e] = acc[q];
   }
 }
+template <int kW>
 __device__ __forceinline__ double col_total(const float* red, int E, int e) {
   double s = 0.0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) s += red[w * E + e];
+  for (int w = 0; w < kW; ++w) s += red[w * E + e];
   return s;
 }
 
@@ -172,8 +176,7 @@ struct BalanceArgs {
   ColPart* part;   // [nb][E]
   double* zpart;   // [nb]
   int* npart;      // [nb]
-  int* ticket;     // arrivals of the second kernel, cleared by the first
-  double* lpart;   // [E / 32] the second kernel's sums of counts * P
+  unsigned long long* joined;  // the second kernel's arrivals and sum, cleared by the first
   int32_t* counts;
   int32_t* n_tokens;
   float* prob_mean;
@@ -199,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
   const int32_t* idx = a.idx + t0 * a.k;
   const uint8_t* mask = a.mask ? a.mask + t0 : nullptr;
   for (int e = tid; e < a.E; e += kThreads) hist[e] = 0;
-  if (!kSolo && blockIdx.x == 0 && tid == 0) *a.ticket = 0;
+  if (!kSolo && blockIdx.x == 0 && tid == 0) *a.joined = 0;
   __syncthreads();
   // slots per expert: integer sums, so the order of the atomics is free
   const long long slots = (long long)rows * a.k;
@@ -246,7 +249,7 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
   const double inv_n = n > 0 ? 1.0 / n : 0.0;
   double bal = 0.0;
   for (int e = tid; e < a.E; e += kThreads) {  // (at most one: E <= kThreads)
-    const double s = col_total(red, a.E, e);
+    const double s = col_total<kWaves>(red, a.E, e);
     if constexpr (kSolo) {
       a.counts[e] = hist[e];
       a.prob_mean[e] = (float)(s * inv_n);
@@ -275,8 +278,11 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
 }
 
 // Second pass: workgroup j adds the partial sums of 16 experts, 64 of them
-// abreast, in a fixed order; the last one to arrive adds the workgroups'
-// shares of the loss, again in a fixed order.
+// abreast, in a fixed order.  The workgroups' shares of the balance loss meet
+// in one 64-bit atomic: arrivals in the top six bits (at most 32 workgroups),
+// below them the sum in fixed point, 48 bits behind the point (the loss is at
+// most E = 512).  An integer sum has no order, and the last to arrive has it
+// from the atomic itself, without a fence (which cost 2 us).
 constexpr int kFinThreads = 1024;
 constexpr int kFinCols = 16;
 constexpr int kFinRows = kFinThreads / kFinCols;
@@ -342,20 +348,21 @@ __global__ __launch_bounds__(kFinThreads) void balance_finish(BalanceArgs a) {
   if (l < kFinCols && e < a.E) {
     a.counts[e] = c;
     a.prob_mean[e] = (float)(p * inv_n);
-    bal = c * (p * inv_n);
+    bal = c * (p * inv_n) * a.E / a.k * inv_n;
   }
 #pragma unroll
   for (int o = kFinCols / 2; o >= 1; o >>= 1) bal += __shfl_xor(bal, o, kWave);
   if (l != 0) return;
-  __hip_atomic_store(&a.lpart[blockIdx.x], bal, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const int arrived =
-      __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-  if (arrived != (int)gridDim.x - 1) return;
-  double s = 0.0;
-  for (unsigned i = 0; i < gridDim.x; ++i)
-    s += __hip_atomic_load(&a.lpart[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // a NaN (which z shows) adds nothing
+  const unsigned long long fixed =
+      z == z ? (unsigned long long)(bal * (double)(1ULL << 48) + 0.5) : 0;
+  const unsigned long long mine = (1ULL << 58) + fixed;
+  const unsigned long long before =
+      __hip_atomic_fetch_add(a.joined, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (before >> 58 != gridDim.x - 1) return;
+  const unsigned long long sum = (before & ((1ULL << 58) - 1)) + fixed;
   *a.n_tokens = n;
-  a.losses[0] = (float)(s * a.E / a.k * inv_n);
+  a.losses[0] = z == z ? (float)((double)sum / (double)(1ULL << 48)) : (float)z;
   a.losses[1] = (float)(z * inv_n);
 }
 
@@ -388,10 +395,10 @@ __device__ __forceinline__ uint16_t split_bf16(float& v) {
 // every lane picks its logits' values; comparing every logit with every id
 // instead took 2 k instructions a logit.
 template <class S>
-__global__ __launch_bounds__(kThreads) void gate_grad_rows(GateGradKernelArgs ka) {
-  __shared__ float red[kWaves * kMaxExperts];
-  __shared__ __align__(16) float sparse[kWaves * kWave * S::Q];  // [wave][row][L Q >= E]
-  __shared__ int wtot[kWaves];
+__global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArgs ka) {
+  __shared__ float red[kGradWaves * kMaxExperts];
+  __shared__ __align__(16) float sparse[kGradWaves * kWave * S::Q];  // [wave][row][L Q >= E]
+  __shared__ int wtot[kGradWaves];
   const GateGradArgs& a = ka.a;
   const int E = ka.E, k = ka.k;
   const int tid = threadIdx.x;
@@ -408,7 +415,8 @@ __global__ __launch_bounds__(kThreads) void gate_grad_rows(GateGradKernelArgs ka
   }
   if (losses) {
     // the sum of the counts, in integers
-    int s = tid < E ? a.counts[tid] : 0;
+    int s = 0;
+    for (int e = tid; e < E; e += kGradThreads) s += a.counts[e];
     const int n = *a.n_tokens;
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, kWave);
@@ -416,7 +424,7 @@ __global__ __launch_bounds__(kThreads) void gate_grad_rows(GateGradKernelArgs ka
     __syncthreads();
     long long total = 0;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) total += wtot[i];
+    for (int i = 0; i < kGradWaves; ++i) total += wtot[i];
 #pragma unroll
     for (int q = 0; q < S::Q; ++q) {
       const int e = S::elem(g, q);
@@ -434,18 +442,28 @@ __global__ __launch_bounds__(kThreads) void gate_grad_rows(GateGradKernelArgs ka
   for (int q = 0; q < S::Q; ++q) colsum[q] = 0.0f;
   const long long t0 = blockIdx.x * ka.rows_per_block;
   const long long t1 = min(t0 + ka.rows_per_block, ka.T);
-  for (long long t = t0 + w * S::R + r; t < t1; t += kWaves * S::R) {
+  for (long long t = t0 + w * S::R + r; t < t1; t += kGradWaves * S::R) {
     float v[S::Q];
 #pragma unroll
     for (int q = 0; q < S::Q; ++q) v[q] = 0.0f;
     if (!a.mask || a.mask[t] != 0) {
-      float gmean = 0.0f;
+      // every load of the row first
+      if (losses) load_row<S>(a.logits + t * E, E, g, v);
+      int id = -1;
+      float gw = 0.0f, dg = 0.0f;
+      if (a.dtopk_w && g < k) {
+        id = a.idx[t * k + g];
+        gw = a.topk_w[t * k + g];
+        dg = a.dtopk_w[t * k + g];
+      }
       if (a.dtopk_w) {
-        for (int j = g; j < k; j += S::L)
+        float gmean = (unsigned)id < (unsigned)E ? gw * dg : 0.0f;
+        for (int j = g + S::L; j < k; j += S::L)
           if ((unsigned)a.idx[t * k + j] < (unsigned)E)
             gmean = fmaf(a.topk_w[t * k + j], a.dtopk_w[t * k + j], gmean);
         gmean = group_sum<S::L>(gmean);
-        for (int j = g; j < k; j += S::L) {
+        if ((unsigned)id < (unsigned)E) unsafeAtomicAdd(&srow[id], gw * (dg - gmean));
+        for (int j = g + S::L; j < k; j += S::L) {
           const int e = a.idx[t * k + j];
           if ((unsigned)e < (unsigned)E)
             unsafeAtomicAdd(&srow[e], a.topk_w[t * k + j] * (a.dtopk_w[t * k + j] - gmean));
@@ -453,7 +471,6 @@ __global__ __launch_bounds__(kThreads) void gate_grad_rows(GateGradKernelArgs ka
       }
       if (losses) {
         float inv;
-        load_row<S>(a.logits + t * E, E, g, v);
         const float lse = row_exp<S>(v, inv);
         float mean = 0.0f;
 #pragma unroll
@@ -476,7 +493,8 @@ __global__ __launch_bounds__(kThreads) void gate_grad_rows(GateGradKernelArgs ka
           }
         }
         asm volatile("" ::: "memory");
-        for (int j = g; j < k; j += S::L) {
+        if ((unsigned)id < (unsigned)E) srow[id] = 0.0f;
+        for (int j = g + S::L; j < k; j += S::L) {
           const int e = a.idx[t * k + j];
           if ((unsigned)e < (unsigned)E) srow[e] = 0.0f;
         }
@@ -519,29 +537,35 @@ __global__ __launch_bounds__(kThreads) void gate_grad_rows(GateGradKernelArgs ka
   if (!a.bias_part) return;
   col_partials<S>(colsum, E, red);
   __syncthreads();
-  for (int e = tid; e < E; e += kThreads)
-    a.bias_part[(size_t)blockIdx.x * E + e] = (float)col_total(red, E, e);
+  for (int e = tid; e < E; e += kGradThreads)
+    a.bias_part[(size_t)blockIdx.x * E + e] = (float)col_total<kGradWaves>(red, E, e);
 }
 
-// Workgroups of the row kernels: whole passes of the workgroup's waves, as
-// many workgroups as there are passes up to kMaxRowBlocks.
-int row_blocks(long long T, int E, long long* rows_per_block) {
+// Workgroups of a row kernel of `waves` waves: whole passes of them, as many
+// workgroups as there are passes up to `most`.
+int row_blocks(long long T, int E, int waves, int most, long long* rows_per_block) {
   long long pass = 0;
-  with_row_shape(E, [&](auto sh) { pass = kWaves * decltype(sh)::R; });
+  with_row_shape(E, [&](auto sh) { pass = waves * decltype(sh)::R; });
   const long long passes = std::max<long long>((T + pass - 1) / pass, 1);
-  const long long each = (passes + kMaxRowBlocks - 1) / kMaxRowBlocks;
+  const long long each = (passes + most - 1) / most;
   *rows_per_block = each * pass;
   return (int)((passes + each - 1) / each);
 }
+int balance_blocks(const Shape& s, long long* rows) {
+  return row_blocks(s.T, s.E, kWaves, kMaxRowBlocks, rows);
+}
+int grad_blocks(const Shape& s, long long* rows) {
+  return row_blocks(s.T, s.E, kGradWaves, kMaxGradBlocks, rows);
+}
 
 struct BalanceLayout {
-  size_t part, zpart, npart, ticket, lpart, total;
+  size_t part, zpart, npart, joined, total;
 };
 
 BalanceLayout balance_layout(const Shape& s) {
   BalanceLayout L{};
   long long rows;
-  const int nb = row_blocks(s.T, s.E, &rows);
+  const int nb = balance_blocks(s, &rows);
   size_t o = 0;
   auto take = [&o](size_t bytes) {
     const size_t at = o;
@@ -551,8 +575,7 @@ BalanceLayout balance_layout(const Shape& s) {
   L.part = take((size_t)nb * s.E * sizeof(ColPart));
   L.zpart = take((size_t)nb * sizeof(double));
   L.npart = take((size_t)nb * sizeof(int));
-  L.ticket = take(sizeof(int));
-  L.lpart = take((size_t)((s.E + kFinCols - 1) / kFinCols) * sizeof(double));
+  L.joined = take(sizeof(unsigned long long));
   L.total = o;
   return L;
 }
@@ -573,12 +596,11 @@ hipError_t balance_loss(const Shape& s, const float* logits, const int32_t* topk
   a.T = s.T;
   a.E = s.E;
   a.k = s.k;
-  a.nb = row_blocks(s.T, s.E, &a.rows_per_block);
+  a.nb = balance_blocks(s, &a.rows_per_block);
   a.part = reinterpret_cast<ColPart*>(base + lay.part);
   a.zpart = reinterpret_cast<double*>(base + lay.zpart);
   a.npart = reinterpret_cast<int*>(base + lay.npart);
-  a.ticket = reinterpret_cast<int*>(base + lay.ticket);
-  a.lpart = reinterpret_cast<double*>(base + lay.lpart);
+  a.joined = reinterpret_cast<unsigned long long*>(base + lay.joined);
   a.counts = counts;
   a.n_tokens = n_tokens;
   a.prob_mean = prob_mean;
@@ -599,7 +621,7 @@ hipError_t balance_loss(const Shape& s, const float* logits, const int32_t* topk
 
 int gate_grad_blocks(const Shape& s) {
   long long rows;
-  return row_blocks(s.T, s.E, &rows);
+  return grad_blocks(s, &rows);
 }
 
 hipError_t gate_grad(const Shape& s, const GateGradArgs& a, int Ep, hipStream_t st) {
@@ -609,10 +631,10 @@ hipError_t gate_grad(const Shape& s, const GateGradArgs& a, int Ep, hipStream_t 
   ka.E = s.E;
   ka.k = s.k;
   ka.Ep = Ep;
-  const int nb = row_blocks(s.T, s.E, &ka.rows_per_block);
+  const int nb = grad_blocks(s, &ka.rows_per_block);
   with_row_shape(s.E, [&](auto sh) {
     using S = decltype(sh);
-    hipLaunchKernelGGL((gate_grad_rows<S>), dim3(nb), dim3(kThreads), 0, st, ka);
+    hipLaunchKernelGGL((gate_grad_rows<S>), dim3(nb), dim3(kGradThreads), 0, st, ka);
   });
   return hipGetLastError();
 }
