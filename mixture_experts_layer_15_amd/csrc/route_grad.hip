@@ -12,6 +12,7 @@
 // end, so two planes (16 bits, 2^-17 off) do for it.
 // float32 activations: both products on the float32 matrix instructions.
 #include <algorithm>
+#include <cmath>
 
 #include "moe_device.h"
 #include "moe_internal.h"
@@ -46,92 +47,43 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// 16 bytes per lane, global -> LDS: lane i's land at lds + 16 i.
-__device__ __forceinline__ void dma16(const void* src, unsigned char* lds) {
+// LDS address of a shared-memory pointer.
+__device__ __forceinline__ uint32_t lds_addr(const unsigned char* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) unsigned char*)p;
+}
+
+// 16 bytes per lane, global -> LDS: lane i's land at lds + 16 i.  Written as
+// an instruction: with the builtin the compiler lets every transposing LDS
+// read wait for all loads in flight.  It has no register result; the kernel
+// waits by wait_vm and a barrier before it reads what arrives.
+__device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+  asm volatile(
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %0, off"
+      :
+      : "v"(src), "s"(lds)
+      : "memory", "m0");
 #else
   (void)src;
   (void)lds;
 #endif
 }
 
-// LDS address of a shared-memory pointer.
-__device__ __forceinline__ uint32_t lds_addr(const unsigned char* p) {
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) unsigned char*)p;
-}
-
-// Transposing LDS reads (ds_read_b64_tr_b16) of one 16-deep step: of 16
-// lanes, lane j gives the address of four 16-bit values of row j / 4, columns
-// 4 (j % 4) .. + 3, and gets column j of the four rows.  Two reads, four rows
-// apart, make the eight K values of an MFMA operand.  One statement issues
-// all reads of a step and waits for them: the builtin would make the compiler
-// wait for the next stage's global loads as well (they write LDS).
-//   x: MB blocks at ax[m];  p: three planes of NB blocks at ap[n]
-template <int MB, int NB>
-struct StepRegs {
-  u32x2_t x[MB][2];
-  u32x2_t p[3][NB][2];
-};
-
-#define MOE_TR(D, A, OFF) "ds_read_b64_tr_b16 %" #D ", %" #A " offset:" #OFF "\n\t"
-
-// rows of 256 bytes of both operands; a plane is 8192 bytes
-__device__ __forceinline__ void read_step(StepRegs<2, 2>& r, const uint32_t (&ax)[2],
-                                          const uint32_t (&ap)[2]) {
+// Transposing LDS read (ds_read_b64_tr_b16): of 16 lanes, lane j gives the
+// address of four 16-bit values of row j / 4, columns 4 (j % 4) .. + 3, and
+// gets column j of the four rows.
+__device__ __forceinline__ u32x2_t read_tr(uint32_t lds) {
+  typedef short s16x4_t __attribute__((ext_vector_type(4)));
 #if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile(
-      MOE_TR(0, 16, 0) MOE_TR(1, 16, 1024) MOE_TR(2, 17, 0) MOE_TR(3, 17, 1024)
-      MOE_TR(4, 18, 0) MOE_TR(5, 18, 1024) MOE_TR(6, 19, 0) MOE_TR(7, 19, 1024)
-      MOE_TR(8, 18, 8192) MOE_TR(9, 18, 9216) MOE_TR(10, 19, 8192) MOE_TR(11, 19, 9216)
-      MOE_TR(12, 18, 16384) MOE_TR(13, 18, 17408) MOE_TR(14, 19, 16384) MOE_TR(15, 19, 17408)
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(r.x[0][0]), "=&v"(r.x[0][1]), "=&v"(r.x[1][0]), "=&v"(r.x[1][1]),
-        "=&v"(r.p[0][0][0]), "=&v"(r.p[0][0][1]), "=&v"(r.p[0][1][0]), "=&v"(r.p[0][1][1]),
-        "=&v"(r.p[1][0][0]), "=&v"(r.p[1][0][1]), "=&v"(r.p[1][1][0]), "=&v"(r.p[1][1][1]),
-        "=&v"(r.p[2][0][0]), "=&v"(r.p[2][0][1]), "=&v"(r.p[2][1][0]), "=&v"(r.p[2][1][1])
-      : "v"(ax[0]), "v"(ax[1]), "v"(ap[0]), "v"(ap[1])
-      : "memory");
+  return __builtin_bit_cast(
+      u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                   (__attribute__((address_space(3))) s16x4_t*)(uintptr_t)lds));
+#else
+  (void)lds;
+  return u32x2_t{};
 #endif
-}
-
-// x rows of 256 bytes, plane rows of 128; a plane is 4096 bytes
-__device__ __forceinline__ void read_step(StepRegs<1, 2>& r, const uint32_t (&ax)[1],
-                                          const uint32_t (&ap)[2]) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile(
-      MOE_TR(0, 14, 0) MOE_TR(1, 14, 1024)
-      MOE_TR(2, 15, 0) MOE_TR(3, 15, 512) MOE_TR(4, 16, 0) MOE_TR(5, 16, 512)
-      MOE_TR(6, 15, 4096) MOE_TR(7, 15, 4608) MOE_TR(8, 16, 4096) MOE_TR(9, 16, 4608)
-      MOE_TR(10, 15, 8192) MOE_TR(11, 15, 8704) MOE_TR(12, 16, 8192) MOE_TR(13, 16, 8704)
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(r.x[0][0]), "=&v"(r.x[0][1]),
-        "=&v"(r.p[0][0][0]), "=&v"(r.p[0][0][1]), "=&v"(r.p[0][1][0]), "=&v"(r.p[0][1][1]),
-        "=&v"(r.p[1][0][0]), "=&v"(r.p[1][0][1]), "=&v"(r.p[1][1][0]), "=&v"(r.p[1][1][1]),
-        "=&v"(r.p[2][0][0]), "=&v"(r.p[2][0][1]), "=&v"(r.p[2][1][0]), "=&v"(r.p[2][1][1])
-      : "v"(ax[0]), "v"(ap[0]), "v"(ap[1])
-      : "memory");
-#endif
-}
-
-// x rows of 256 bytes, plane rows of 64; a plane is 2048 bytes
-__device__ __forceinline__ void read_step(StepRegs<1, 1>& r, const uint32_t (&ax)[1],
-                                          const uint32_t (&ap)[1]) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile(
-      MOE_TR(0, 8, 0) MOE_TR(1, 8, 1024) MOE_TR(2, 9, 0) MOE_TR(3, 9, 256)
-      MOE_TR(4, 9, 2048) MOE_TR(5, 9, 2304) MOE_TR(6, 9, 4096) MOE_TR(7, 9, 4352)
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(r.x[0][0]), "=&v"(r.x[0][1]), "=&v"(r.p[0][0][0]), "=&v"(r.p[0][0][1]),
-        "=&v"(r.p[1][0][0]), "=&v"(r.p[1][0][1]), "=&v"(r.p[2][0][0]), "=&v"(r.p[2][0][1])
-      : "v"(ax[0]), "v"(ap[0])
-      : "memory");
-#endif
-}
-#undef MOE_TR
-
-__device__ __forceinline__ bf16x8_t operand(const u32x2_t (&v)[2]) {
-  return __builtin_bit_cast(bf16x8_t, u32x4_t{v[0][0], v[0][1], v[1][0], v[1][1]});
 }
 
 // ---- dW_r, bf16
@@ -141,7 +93,11 @@ __device__ __forceinline__ bf16x8_t operand(const u32x2_t (&v)[2]) {
 // staged row is cut into blocks of 64 bytes (32 columns, one MFMA block);
 // block b of row t sits at b ^ swz(t), so that the four rows which a group of
 // 16 lanes reads together lie in different banks (256 bytes a sweep).
-constexpr int kKT = 32;          // tokens per stage
+//
+// A wave has MB x NB blocks of 32 x 32.  The three planes of dL share the
+// operands of x, so a wave is taller in columns of x than in experts: LDS
+// bandwidth bounds it otherwise.  The waves are WC x WE, times KG groups that
+// take every KG-th step of 16 tokens and are added at the end.
 constexpr int kSegment = 16384;  // tokens whose mask bits are held in LDS
 
 template <int kRowBytes>
@@ -160,82 +116,102 @@ struct DwArgs {
   long long T;
   int d, E, Ep;
   int c_tiles, e_tiles, splits;
-  long long t_per_split;   // a multiple of kKT
+  long long t_per_split;   // a multiple of 64
 };
 
-template <int BC, int BE, int WC, int WE, bool kMask>
-__global__ __launch_bounds__(kThreads) void router_dw_bf16(DwArgs a) {
-  constexpr int MB = BC / 32 / WC, NB = BE / 32 / WE;
-  static_assert(WC * WE == 4 && MB >= 1 && NB >= 1, "four waves");
-  static_assert(BC == 128 && BE == (MB == 2 ? 128 : 32 * NB), "row sizes that read_step knows");
-  constexpr int kRowX = BC * 2, kRowP = BE * 2;
-  constexpr int kStageX = kKT * kRowX, kStageP = kKT * kRowP;
-  constexpr int kStage = kStageX + 3 * kStageP;
-  constexpr int kInstr = kStage / 1024;  // 1 KB loads of a stage
-  constexpr int kPerWave = (kInstr + 3) / 4;
+template <int MB_, int NB_, int WC_, int WE_, int KG_, int KT_, int NST_>
+struct DwCfg {
+  static constexpr int MB = MB_, NB = NB_, WC = WC_, WE = WE_, KG = KG_, KT = KT_, NST = NST_;
+  static constexpr int kWaves = WC * WE * KG;
+  static constexpr int kThreads = kWaves * kWave;
+  static constexpr int BC = 32 * MB * WC, BE = 32 * NB * WE;
+  static constexpr int kRowX = BC * 2, kRowP = BE * 2;
+  static constexpr int kStageX = KT * kRowX, kStageP = KT * kRowP;
+  static constexpr int kStage = kStageX + 3 * kStageP;
+  static constexpr int kInstr = kStage / 1024;  // 1 KB loads of a stage
+  static constexpr int kPerWave = (kInstr + kWaves - 1) / kWaves;
+  static constexpr int kSteps = KT / 16 / KG;   // steps of a wave per stage
+  static constexpr int kLds = NST * kStage;
   static_assert(kStageX % 1024 == 0 && kStageP % 1024 == 0, "whole loads");
-  __shared__ __align__(1024) unsigned char stage[2][kStage];
-  __shared__ uint64_t keep[kMask ? kSegment / 64 : 1];
+  static_assert(KT % (16 * KG) == 0 && 64 % KT == 0, "whole steps");
+  static_assert((NST - 1) * kPerWave < 64, "vmcnt range");
+  // the sum over the K groups passes one block row of every wave through LDS
+  static_assert(KG == 1 || WC * WE * NB * 4096 <= kLds, "room for the sums");
+};
+
+template <class C, bool kMask>
+__global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void router_dw_bf16(DwArgs a) {
+  constexpr int MB = C::MB, NB = C::NB;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  uint64_t* keep = reinterpret_cast<uint64_t*>(smem + C::kLds);  // kMask: kSegment bits
   const int item = xcd_item(a.splits * a.e_tiles * a.c_tiles);
   if (item < 0) return;  // the whole workgroup
   const int ct = item % a.c_tiles;
   const int et = item / a.c_tiles % a.e_tiles;
   const int split = item / (a.c_tiles * a.e_tiles);
-  const int c0 = ct * BC, e0 = et * BE;
+  const int c0 = ct * C::BC, e0 = et * C::BE;
   const long long t0 = split * a.t_per_split;
   const long long t1 = min(t0 + a.t_per_split, a.T);
   const int tid = threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int l = tid % kWave;
+  const uint32_t lds0 = lds_addr(smem);
 
-  // one 1 KB load of the stage whose first token is `t` into buffer `b`
-  auto load = [&](int n, long long t, int b) {
-    const bool isx = n * 1024 < kStageX;
-    unsigned char* dst = &stage[b][n * 1024];
-    if (isx) {
-      const int q = n * 64 + l;
-      const int r = q / (kRowX / 16), pc = q % (kRowX / 16);
-      const int c = pc ^ (tr_swz<kRowX>(r) << 2);
-      bool live = t + r < t1;
-      if constexpr (kMask) {
-        const int i = (int)((t + r - t0) % kSegment);
-        live = live && (keep[i / 64] >> (i % 64) & 1);
-      }
-      const void* src = live ? (const void*)(a.x + (t + r) * a.d + c0 + c * 8) : (const void*)a.zero;
-      dma16(src, dst);
-    } else {
-      const int m = n * 1024 - kStageX;
-      const int pl = m / kStageP;
-      const int q = (m % kStageP) / 16 + l;
-      const int r = q / (kRowP / 16), pc = q % (kRowP / 16);
-      const int c = pc ^ (tr_swz<kRowP>(r) << 2);
-      const bool live = t + r < t1 && e0 + c * 8 < a.Ep;
-      const void* src = live ? (const void*)(a.planes + (pl * a.T + t + r) * a.Ep + e0 + c * 8)
-                             : (const void*)a.zero;
-      dma16(src, dst);
-    }
-  };
-  auto load_stage = [&](long long t, int b) {
+  // this wave's loads of a stage: source of token 0 of the range, bytes per
+  // token, and the token within the stage
+  const unsigned char* src[C::kPerWave];
+  int row[C::kPerWave];
 #pragma unroll
-    for (int i = 0; i < kPerWave; ++i) {
-      const int n = w + 4 * i;
-      if (n < kInstr) load(n, t, b);
+  for (int i = 0; i < C::kPerWave; ++i) {
+    const int n = w + C::kWaves * i;
+    if (n * 1024 < C::kStageX) {
+      const int q = n * 64 + l;
+      const int r = q / (C::kRowX / 16), pc = q % (C::kRowX / 16);
+      const int c = pc ^ (tr_swz<C::kRowX>(r) << 2);
+      row[i] = r;
+      src[i] = reinterpret_cast<const unsigned char*>(a.x + (t0 + r) * a.d + c0 + c * 8);
+      if (c0 + c * 8 >= a.d) src[i] = nullptr;
+    } else {
+      const int m = n * 1024 - C::kStageX;
+      const int pl = m / C::kStageP;
+      const int q = (m % C::kStageP) / 16 + l;
+      const int r = q / (C::kRowP / 16), pc = q % (C::kRowP / 16);
+      const int c = pc ^ (tr_swz<C::kRowP>(r) << 2);
+      row[i] = r;
+      src[i] = reinterpret_cast<const unsigned char*>(a.planes + (pl * a.T + t0 + r) * a.Ep + e0 + c * 8);
+      if (e0 + c * 8 >= a.Ep) src[i] = nullptr;
+    }
+  }
+  auto load_stage = [&](long long t, int b) {  // t: tokens from t0
+#pragma unroll
+    for (int i = 0; i < C::kPerWave; ++i) {
+      const int n = w + C::kWaves * i;
+      if (C::kInstr % C::kWaves != 0 && n >= C::kInstr) continue;
+      const bool isx = n * 1024 < C::kStageX;
+      const unsigned char* p = src[i] + t * (isx ? a.d : a.Ep) * 2;
+      bool live = src[i] != nullptr && t0 + t + row[i] < t1;
+      if (kMask && isx) {
+        const int k = (int)((t + row[i]) % kSegment);
+        live = live && (keep[k / 64] >> (k % 64) & 1);
+      }
+      dma16(live ? p : a.zero, lds0 + b * C::kStage + n * 1024);
     }
   };
 
   // operand read offsets: lane l covers column l % 32 of a block, tokens
   // 8 (l / 32) + 0 .. 7 of each 16-deep step (two reads of four)
-  const int wc = w % WC, we = w / WC;
+  const int kg = w / (C::WC * C::WE), wc = w % C::WC, we = w / C::WC % C::WE;
   const int j = l % 16;
-  const int row = 8 * (l / 32) + j / 4;
+  const int r0 = 8 * (l / 32) + j / 4 + 16 * kg;
   const int in_block = ((l % 32) / 16) * 32 + (j % 4) * 8;
-  int offx[MB], offp[NB];
+  uint32_t offx[MB], offp[NB];
 #pragma unroll
   for (int m = 0; m < MB; ++m)
-    offx[m] = row * kRowX + (((wc * MB + m) ^ tr_swz<kRowX>(j / 4)) * 64) + in_block;
+    offx[m] = lds0 + r0 * C::kRowX + (((wc * MB + m) ^ tr_swz<C::kRowX>(j / 4)) * 64) + in_block;
 #pragma unroll
   for (int n = 0; n < NB; ++n)
-    offp[n] = kStageX + row * kRowP + (((we * NB + n) ^ tr_swz<kRowP>(j / 4)) * 64) + in_block;
+    offp[n] = lds0 + C::kStageX + r0 * C::kRowP +
+              (((we * NB + n) ^ tr_swz<C::kRowP>(j / 4)) * 64) + in_block;
 
   f32x16_t acc[MB][NB];
 #pragma unroll
@@ -243,52 +219,90 @@ __global__ __launch_bounds__(kThreads) void router_dw_bf16(DwArgs a) {
 #pragma unroll
     for (int n = 0; n < NB; ++n) acc[m][n] = f32x16_t{};
 
-  for (long long s0 = t0; s0 < t1; s0 += kSegment) {
-    const long long s1 = min(s0 + kSegment, t1);
+  auto operand = [](uint32_t at, int row4) {  // row4: bytes of four rows
+    const u32x2_t lo = read_tr(at), hi = read_tr(at + row4);
+    return __builtin_bit_cast(bf16x8_t, u32x4_t{lo[0], lo[1], hi[0], hi[1]});
+  };
+  for (long long s0 = 0; s0 < t1 - t0; s0 += kSegment) {
+    const int len = (int)min((long long)kSegment, t1 - t0 - s0);
     if constexpr (kMask) {
       __syncthreads();
-      for (int i = w; i < kSegment / 64 && s0 + i * 64 < s1; i += 4) {
-        const long long t = s0 + i * 64 + l;
-        const unsigned long long m = __ballot(t < s1 && a.mask[min(t, a.T - 1)] != 0);
+      for (int i = w; i * 64 < len; i += C::kWaves) {
+        const long long t = t0 + s0 + i * 64 + l;
+        const unsigned long long m = __ballot(i * 64 + l < len && a.mask[min(t, a.T - 1)] != 0);
         if (l == 0) keep[i] = m;
       }
       __syncthreads();
     }
-    load_stage(s0, 0);
+    const int stages = (len + C::KT - 1) / C::KT;
+#pragma unroll
+    for (int i = 0; i < C::NST - 1; ++i)
+      if (i < stages) load_stage(s0 + i * C::KT, i);
     int b = 0;
-    for (long long t = s0; t < s1; t += kKT, b ^= 1) {
-      if (t + kKT < s1) {
-        load_stage(t + kKT, b ^ 1);
-        // at most the next stage's loads still in flight
-        if (w + 4 * (kPerWave - 1) < kInstr) wait_vm<kPerWave>();
-        else wait_vm<kPerWave - 1>();
+    for (int s = 0; s < stages; ++s) {
+      // stage s has landed: at most those behind it are in flight
+      if (s + C::NST - 1 <= stages) {
+        constexpr int kBehind = C::NST - 2;
+        if (C::kInstr % C::kWaves == 0 || w < C::kInstr % C::kWaves) wait_vm<kBehind * C::kPerWave>();
+        else wait_vm<kBehind * (C::kPerWave - 1)>();
       } else {
         wait_vm<0>();
       }
-      lds_barrier();
-      const uint32_t st = lds_addr(stage[b]);
+      lds_barrier();  // ... for every wave, and nobody reads stage s - 1 any more
+      if (s + C::NST - 1 < stages)
+        load_stage(s0 + (long long)(s + C::NST - 1) * C::KT, b == 0 ? C::NST - 1 : b - 1);
+      const uint32_t st = b * C::kStage;
 #pragma unroll
-      for (int ks = 0; ks < kKT / 16; ++ks) {
-        uint32_t ax[MB], ap[NB];
+      for (int ks = 0; ks < C::kSteps; ++ks) {
+        bf16x8_t xa[MB];
 #pragma unroll
-        for (int m = 0; m < MB; ++m) ax[m] = st + offx[m] + ks * 16 * kRowX;
-#pragma unroll
-        for (int n = 0; n < NB; ++n) ap[n] = st + offp[n] + ks * 16 * kRowP;
-        StepRegs<MB, NB> r;
-        read_step(r, ax, ap);
+        for (int m = 0; m < MB; ++m)
+          xa[m] = operand(offx[m] + st + ks * 16 * C::KG * C::kRowX, 4 * C::kRowX);
 #pragma unroll
         for (int pl = 0; pl < 3; ++pl)
 #pragma unroll
-          for (int n = 0; n < NB; ++n)
+          for (int n = 0; n < NB; ++n) {
+            const bf16x8_t pb =
+                operand(offp[n] + st + pl * C::kStageP + ks * 16 * C::KG * C::kRowP, 4 * C::kRowP);
 #pragma unroll
             for (int m = 0; m < MB; ++m)
-              acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(operand(r.x[m]), operand(r.p[pl][n]),
-                                                                  acc[m][n], 0, 0, 0);
+              acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[m], pb, acc[m][n], 0, 0, 0);
+          }
       }
-      // every wave's reads of this buffer have returned before it is filled
-      // again
-      lds_barrier();
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads of the stage have returned
+      b = b + 1 == C::NST ? 0 : b + 1;
     }
+    lds_barrier();
+  }
+
+  if constexpr (C::KG > 1) {
+    // the K groups' sums, in order, one block row at a time
+    f32x4_t* buf = reinterpret_cast<f32x4_t*>(smem) + (w % (C::WC * C::WE)) * NB * 4 * kWave + l;
+    for (int grp = 1; grp < C::KG; ++grp)
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        __syncthreads();
+        if (kg == grp) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              buf[(n * 4 + q) * kWave] = f32x4_t{acc[m][n][4 * q], acc[m][n][4 * q + 1],
+                                                 acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
+        }
+        __syncthreads();
+        if (kg == 0) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f32x4_t v = buf[(n * 4 + q) * kWave];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[m][n][4 * q + i] += v[i];
+            }
+        }
+      }
+    if (kg != 0) return;
   }
   // lane l holds expert l % 32 of a block, columns 8 (q / 4) + 4 (l / 32) + q % 4
   float* out = a.out + (size_t)split * a.d * a.E;
@@ -301,116 +315,150 @@ __global__ __launch_bounds__(kThreads) void router_dw_bf16(DwArgs a) {
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
         const int c = c0 + (wc * MB + m) * 32 + 8 * (q / 4) + 4 * (l / 32) + q % 4;
-        out[(size_t)c * a.E + e] = acc[m][n][q];
+        if (C::BC <= 128 || c < a.d) out[(size_t)c * a.E + e] = acc[m][n][q];
       }
     }
 }
 
 // ---- dx, bf16
-// Tile: 128 columns by 128 tokens, the sum over the experts (at most 512) in
-// stages of 32.  The router matrix is the A operand with its rows staged in
-// an order that leaves a lane 16 consecutive columns of one token.  A staged
-// row is 64 bytes; chunk c of row r sits at c ^ (r / 4) % 4 (four rows make a
-// bank sweep).
+// The sum is short (the experts, at most 512), the output long: each wave
+// keeps its columns' share of the router matrix in registers as MFMA operands
+// (MB blocks of 32 columns, KS steps of 16 experts: 4 MB KS registers) and
+// runs over the tokens, whose planes pass through LDS, 32 NB tokens a stage, in
+// two buffers.  The waves of a workgroup have neighbouring columns and share
+// the stage.  The matrix is the A operand, with its rows in an order that
+// leaves a lane 16 consecutive columns of one token.
+// A staged row (one token, one plane) of P bytes: 16-byte chunk c of row t
+// sits at c ^ swz(t) within its aligned group of 16 chunks (8, 4 where P is
+// no multiple of 256, 128), so that 16 consecutive rows at one logical chunk
+// lie in different banks.
 struct DxArgs {
   const uint16_t* planes;  // [2 of 3][T][Ep]
-  const uint16_t* w;       // [d][Ep]
+  const uint16_t* w;       // [d][w_pitch], experts behind E not read
   uint16_t* dx;            // [T][d]
   long long T;
-  int d, Ep;
-  int c_tiles, t_tiles;
+  int d, E, w_pitch;
+  int c_groups, t_ranges;  // workgroups: column groups x token ranges
+  int steps_per_range;     // stages
 };
 
-constexpr int kDxTile = 128;
-
-// LDS row r of a 32-row block holds matrix row dx_feat(r): the MFMA result
-// register q of lane half h is row 8 (q / 4) + 4 h + q % 4, and column
-// 16 h + q this way.
+// Column 16 h + q of a 32-column block is register q of lane half h of the
+// MFMA result, row 8 (q / 4) + 4 h + q % 4: the row r operand is column
+// dx_feat(r).
 __device__ __forceinline__ int dx_feat(int r) { return ((r >> 2) & 1) * 16 + (r >> 3) * 4 + (r & 3); }
 
-__global__ __launch_bounds__(kThreads) void router_dx_bf16(DxArgs a) {
-  constexpr int kPart = kDxTile * 64;  // bytes of one staged matrix
-  constexpr int kStage = 3 * kPart;
-  constexpr int kPerWave = kStage / 1024 / 4;
-  __shared__ __align__(1024) unsigned char stage[2][kStage];
-  const int item = xcd_item(a.c_tiles * a.t_tiles);
-  if (item < 0) return;
-  const int ct = item % a.c_tiles;
-  const long long t0 = (long long)(item / a.c_tiles) * kDxTile;
-  const int c0 = ct * kDxTile;
+template <int KS>
+__device__ __forceinline__ int dx_swz(int t) {
+  constexpr int P = KS * 32;
+  return P % 256 == 0 ? t & 15 : P % 128 == 0 ? (t >> 1) & 7 : (t >> 2) & 3;
+}
+
+template <int MB, int KS, int NB, int NW, int kMinWaves>
+__global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx_bf16(DxArgs a) {
+  constexpr int kDxTokens = 32 * NB;
+  constexpr int P = KS * 32;                 // bytes of a staged row
+  constexpr int kPlane = kDxTokens * P;
+  constexpr int kStage = 2 * kPlane;
+  constexpr int kPerWave = kStage / 1024 / NW;
+  static_assert(kStage % (1024 * NW) == 0, "whole loads per wave");
+  constexpr int kStores = MB * NB * 2;       // 16-byte stores of a lane per stage
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int item = xcd_item(a.c_groups * a.t_ranges);
+  if (item < 0) return;  // the whole workgroup
+  // the column groups of a token range run on one XCD (they share the planes)
+  const int cg = item % a.c_groups;
+  const int range = item / a.c_groups;
   const int tid = threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int l = tid % kWave;
+  const int h = l / 32;
+  const int c0 = (cg * NW + w) * MB * 32;    // this wave's columns (may be behind d)
+  const long long steps = (a.T + kDxTokens - 1) / kDxTokens;
+  const long long s0 = (long long)range * a.steps_per_range;
+  const int ns = (int)min((long long)a.steps_per_range, steps - s0);
+  if (ns <= 0) return;  // the whole workgroup
 
-  const uint16_t* src[kPerWave];
+  // loads of a stage: 1 KB is 1024 / P rows (or a part of one)
+  const uint32_t lds0 = lds_addr(smem);
+  auto load_stage = [&](int s, int b) {
 #pragma unroll
-  for (int i = 0; i < kPerWave; ++i) {
-    const int n = w + 4 * i;        // 1 KB: 16 rows
-    const int part = n * 1024 / kPart;
-    const int r = (n * 1024 % kPart) / 64 + l / 4;
-    const int c = (l % 4) ^ ((r / 4) % 4);
-    if (part == 0)
-      src[i] = a.w + (size_t)(c0 + (r & ~31) + dx_feat(r & 31)) * a.Ep + c * 8;
-    else
-      src[i] = a.planes + ((part - 1) * a.T + min(t0 + r, a.T - 1)) * a.Ep + c * 8;
-  }
-  auto load_stage = [&](int k0, int b) {
-#pragma unroll
-    for (int i = 0; i < kPerWave; ++i) dma16(src[i] + k0, &stage[b][(w + 4 * i) * 1024]);
-  };
-  const int wc = w % 2, wt = w / 2;
-  // lane l: row l % 32 of a block, chunk 2 ks + l / 32
-  auto off = [&](int r, int ks) { return r * 64 + (((2 * ks + l / 32) ^ ((r / 4) % 4)) << 4); };
-  f32x16_t acc[2][2];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int n = 0; n < 2; ++n) acc[m][n] = f32x16_t{};
-  load_stage(0, 0);
-  int b = 0;
-  for (int k0 = 0; k0 < a.Ep; k0 += 32, b ^= 1) {
-    if (k0 + 32 < a.Ep) {
-      load_stage(k0 + 32, b ^ 1);
-      wait_vm<kPerWave>();
-    } else {
-      wait_vm<0>();
+    for (int i = 0; i < kPerWave; ++i) {
+      const int n = w * kPerWave + i;
+      const int q = n * 64 + l;               // 16-byte chunk of the stage
+      const int row = q / (P / 16), pc = q % (P / 16);
+      const int pl = row / kDxTokens, r = row % kDxTokens;
+      const int c = pc ^ dx_swz<KS>(r);
+      const long long t = min((s0 + s) * kDxTokens + r, a.T - 1);
+      dma16(a.planes + (pl * a.T + t) * (KS * 16) + c * 8, lds0 + b * kStage + n * 1024);
     }
-    lds_barrier();
-    const unsigned char* st = stage[b];
+  };
+  load_stage(0, 0);
+
+  // lane l: matrix row dx_feat(l % 32) of a block, experts 16 ks + 8 h .. + 7
+  bf16x8_t wf[MB][KS];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      bf16x8_t wa[2];
+  for (int m = 0; m < MB; ++m) {
+    const int c = min(c0 + m * 32 + dx_feat(l % 32), a.d - 1);
+    const uint16_t* row = a.w + (size_t)c * a.w_pitch + 8 * h;
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-        wa[m] = *reinterpret_cast<const bf16x8_t*>(st + off(wc * 64 + m * 32 + l % 32, ks));
+    for (int ks = 0; ks < KS; ++ks) {
+      u32x4_t v = {0, 0, 0, 0};
+      if (16 * ks + 8 * h < a.E) v = *reinterpret_cast<const u32x4_t*>(row + 16 * ks);
+      wf[m][ks] = __builtin_bit_cast(bf16x8_t, v);
+    }
+  }
+  // operand read: lane l has token l % 32 of a block, chunk 2 ks + h
+  constexpr int kGroup = P % 256 == 0 ? 8 : P % 128 == 0 ? 4 : 2;  // steps of a swizzle group
+  uint32_t base[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int r = n * 32 + l % 32;
+    base[n] = r * P + ((h ^ dx_swz<KS>(r)) << 4);
+  }
+  const bool all_cols = c0 + MB * 32 <= a.d;
+  int b = 0;
+  for (int s = 0; s < ns; ++s, b ^= 1) {
+    // the stage's loads; all stores of the last stage may be in flight, where
+    // all were made (it had no token behind T: only a range's end has)
+    if (s == 0 || !all_cols) wait_vm<0>();
+    else wait_vm<kStores>();
+    lds_barrier();            // ... of every wave, and nobody reads the other buffer any more
+    if (s + 1 < ns) load_stage(s + 1, b ^ 1);
+    f32x16_t acc[MB][NB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) acc[m][n] = f32x16_t{};
+    const unsigned char* st = smem + b * kStage;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
       for (int pl = 0; pl < 2; ++pl)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < NB; ++n) {
           const bf16x8_t pb = *reinterpret_cast<const bf16x8_t*>(
-              st + (1 + pl) * kPart + off(wt * 64 + n * 32 + l % 32, ks));
+              st + pl * kPlane + (base[n] ^ ((ks % kGroup) << 5)) + ks / kGroup * kGroup * 32);
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
-            acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa[m], pb, acc[m][n], 0, 0, 0);
+          for (int m = 0; m < MB; ++m)
+            acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[m][ks], pb, acc[m][n], 0, 0, 0);
         }
-    }
-    __builtin_amdgcn_s_waitcnt(0xC07F);
-    lds_barrier();
-  }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads of the stage have returned
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const long long t = t0 + wt * 64 + n * 32 + l % 32;
-    if (t >= a.T) continue;
+    for (int n = 0; n < NB; ++n) {
+      const long long t = (s0 + s) * kDxTokens + n * 32 + l % 32;
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      uint16_t* o = a.dx + t * a.d + c0 + wc * 64 + m * 32 + 16 * (l / 32);
-      const f32x16_t& v = acc[m][n];
+      for (int m = 0; m < MB; ++m) {
+        const f32x16_t& v = acc[m][n];
+        uint16_t* o = a.dx + t * a.d + c0 + m * 32 + 16 * h;
+        if (t < a.T && c0 + m * 32 < a.d) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<u32x4_t*>(o + 8 * h) =
-            u32x4_t{pack_bf16x2(v[8 * h], v[8 * h + 1]), pack_bf16x2(v[8 * h + 2], v[8 * h + 3]),
-                    pack_bf16x2(v[8 * h + 4], v[8 * h + 5]),
-                    pack_bf16x2(v[8 * h + 6], v[8 * h + 7])};
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<u32x4_t*>(o + 8 * i) =
+                u32x4_t{pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                        pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                        pack_bf16x2(v[8 * i + 6], v[8 * i + 7])};
+        }
+      }
     }
   }
 }
@@ -545,22 +593,60 @@ __global__ __launch_bounds__(kSumThreads) void router_grad_sum(SumArgs a) {
   }
 }
 
-int padded_experts(const Shape& s) { return (s.E + 31) / 32 * 32; }
+// Experts in a row of the planes: the steps that router_dx_bf16 is made for.
+int padded_experts(const Shape& s) { return s.E <= 32 ? 32 : (s.E + 63) / 64 * 64; }
 
-// Tile of the bf16 dW_r kernel for E experts.
-int dw_tile_e(const Shape& s) { return s.E <= 32 ? 32 : s.E <= 64 ? 64 : 128; }
-int dw_tile_c() { return 128; }
+// Plan of the bf16 dW_r kernel: its tile, and the parts of the token range.
+struct DwPlan {
+  int bc, be;
+  int splits;
+};
 
-// Parts of the token range: about two workgroups per compute unit, at least
-// 128 tokens each, and partial sums (written and read) no larger than x.
-int dw_splits(const Shape& s) {
-  const int be = s.act == kBF16 ? dw_tile_e(s) : 64;
-  const int bc = s.act == kBF16 ? dw_tile_c() : 64;
-  const long long tiles = (long long)(s.d / bc) * ((s.E + be - 1) / be);
-  long long n = (512 + tiles - 1) / tiles;
-  n = std::min<long long>(n, (s.T + 127) / 128);
-  n = std::min<long long>(n, std::max<long long>(s.T / (4LL * s.E), 4));
-  return (int)std::max<long long>(std::min<long long>(n, 64), 1);
+// One workgroup fits a compute unit.  A part costs the rounds of workgroups
+// over the 256 compute units times (start and end of a workgroup, 4 us, plus
+// its tokens: 44 ns each on the 256 x 128 tile, 25 ns on 128 x 128, 14 ns on
+// the narrow ones, as measured), plus its partial sums, written and read at
+// 4 TB/s.  The tall tile has the better rate (1139 against 976 TFLOP/s of
+// matrix instructions on 16384 tokens of 7168 x 256: 158 against 185 us) but
+// needs that many more parts to fill the chip: on 8192 tokens of 2048 x 128 it
+// takes 21.6 us and 32 parts, the square one 18.5 us and 16.
+double dw_cost(const Shape& s, int bc, int be, double ns_token, int splits) {
+  const double tiles = (double)((s.d + bc - 1) / bc) * ((s.E + be - 1) / be);
+  const double rounds = std::ceil(tiles * splits / 256.0);
+  const double tokens = std::ceil((double)s.T / splits / 64.0) * 64.0;
+  return rounds * (4000.0 + tokens * ns_token) +
+         (splits > 1 ? 2.0 * splits * s.d * s.E * 4 / 4000.0 : 0.0);
+}
+
+DwPlan dw_plan(const Shape& s) {
+  DwPlan best{128, 32, 1};
+  if (s.act != kBF16) {
+    best = DwPlan{64, 64, 1};
+    const long long tiles = (long long)(s.d / 64) * ((s.E + 63) / 64);
+    long long n = std::min<long long>((512 + tiles - 1) / tiles, (s.T + 127) / 128);
+    n = std::min<long long>(n, std::max<long long>(s.T / (4LL * s.E), 4));
+    best.splits = (int)std::max<long long>(std::min<long long>(n, 64), 1);
+    return best;
+  }
+  double cost = -1.0;
+  auto offer = [&](int bc, int be, double ns_token) {
+    for (int n = 1; n <= 64 && (n == 1 || (long long)n * 64 <= s.T + 63); ++n) {
+      const double c = dw_cost(s, bc, be, ns_token, n);
+      if (cost < 0 || c < cost) {
+        cost = c;
+        best = DwPlan{bc, be, n};
+      }
+    }
+  };
+  if (s.E <= 32) {
+    offer(128, 32, 14.0);
+  } else if (s.E <= 64) {
+    offer(128, 64, 14.0);
+  } else {
+    offer(128, 128, 25.0);
+    offer(256, 128, 44.0);
+  }
+  return best;
 }
 
 struct GradLayout {
@@ -579,24 +665,73 @@ GradLayout grad_layout(const Shape& s) {
   L.zero = take(kZeroLineBytes);
   if (s.act == kBF16) {
     L.planes = take((size_t)3 * s.T * Ep * 2);
-    L.wpad = take(Ep != s.E ? (size_t)s.d * Ep * 2 : 0);
+    L.wpad = take(s.E % 8 != 0 ? (size_t)s.d * Ep * 2 : 0);
   } else {
     L.dl = take((size_t)s.T * s.E * 4);
   }
   L.bias = take((size_t)gate_grad_blocks(s) * s.E * 4);
-  const int ns = dw_splits(s);
+  const int ns = dw_plan(s).splits;
   L.dw = take(ns > 1 ? (size_t)ns * s.d * s.E * 4 : 0);
   L.total = o;
   return L;
 }
 
-template <int BC, int BE, int WC, int WE>
-void launch_dw(const DwArgs& a, hipStream_t st) {
+template <class C>
+hipError_t launch_dw(DwArgs a, hipStream_t st) {
+  a.c_tiles = (a.d + C::BC - 1) / C::BC;
+  a.e_tiles = (a.E + C::BE - 1) / C::BE;
+  a.t_per_split = ((a.T + a.splits - 1) / a.splits + 63) / 64 * 64;
   const dim3 grid(xcd_grid(a.splits * a.e_tiles * a.c_tiles));
-  if (a.mask)
-    hipLaunchKernelGGL((router_dw_bf16<BC, BE, WC, WE, true>), grid, dim3(kThreads), 0, st, a);
-  else
-    hipLaunchKernelGGL((router_dw_bf16<BC, BE, WC, WE, false>), grid, dim3(kThreads), 0, st, a);
+  const int lds = C::kLds + (a.mask ? kSegment / 8 : 0);
+  if (a.mask) {
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(&router_dw_bf16<C, true>), lds, done);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((router_dw_bf16<C, true>), grid, dim3(C::kThreads), lds, st, a);
+  } else {
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(&router_dw_bf16<C, false>), lds, done);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((router_dw_bf16<C, false>), grid, dim3(C::kThreads), lds, st, a);
+  }
+  return hipGetLastError();
+}
+
+template <int MB, int KS, int NB, int NW, int kMinWaves>
+hipError_t launch_dx_as(DxArgs a, hipStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  constexpr int kTokens = 32 * NB;
+  constexpr int kLds = 2 * 2 * kTokens * KS * 32;
+  static_assert(kLds <= 160 * 1024, "LDS budget");
+  const void* kern = reinterpret_cast<const void*>(&router_dx_bf16<MB, KS, NB, NW, kMinWaves>);
+  const hipError_t e = set_lds_attr(kern, kLds, done);
+  if (e != hipSuccess) return e;
+  const int cols = MB * 32 * NW;
+  a.c_groups = (a.d + cols - 1) / cols;
+  // as many workgroups as fit the compute units at once
+  const long long steps = (a.T + kTokens - 1) / kTokens;
+  const int slots = std::max(256 * 4 * kMinWaves / NW / a.c_groups, 1);
+  a.steps_per_range = (int)std::max<long long>((steps + slots - 1) / slots, 1);
+  a.t_ranges = (int)((steps + a.steps_per_range - 1) / a.steps_per_range);
+  hipLaunchKernelGGL((router_dx_bf16<MB, KS, NB, NW, kMinWaves>),
+                     dim3(xcd_grid(a.c_groups * a.t_ranges)), dim3(NW * kWave), kLds, st, a);
+  return hipGetLastError();
+}
+
+// The variant by the experts of a row: a wave's share of the matrix takes
+// 4 MB KS registers, a stage 64 NB KS 32 bytes of LDS.
+hipError_t launch_dx(const DxArgs& a, int Ep, hipStream_t st) {
+  switch (Ep) {
+    case 32: return launch_dx_as<2, 2, 2, 4, 2>(a, st);
+    case 64: return launch_dx_as<2, 4, 2, 4, 2>(a, st);
+    case 128: return launch_dx_as<2, 8, 2, 4, 2>(a, st);
+    case 192: return launch_dx_as<2, 12, 2, 8, 2>(a, st);
+    case 256: return launch_dx_as<2, 16, 2, 8, 2>(a, st);
+    case 320: return launch_dx_as<2, 20, 1, 4, 1>(a, st);
+    case 384: return launch_dx_as<2, 24, 1, 4, 1>(a, st);
+    case 448: return launch_dx_as<2, 28, 1, 4, 1>(a, st);
+    default: return launch_dx_as<2, 32, 1, 4, 1>(a, st);
+  }
 }
 
 }  // namespace
@@ -607,7 +742,8 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
   unsigned char* base = static_cast<unsigned char*>(ws);
   const GradLayout lay = grad_layout(s);
   const int Ep = padded_experts(s);
-  const int ns = dw_splits(s);
+  const DwPlan plan = dw_plan(s);
+  const int ns = plan.splits;
   const bool bf16 = s.act == kBF16;
   float* bias_part = reinterpret_cast<float*>(base + lay.bias);
   uint16_t* planes = reinterpret_cast<uint16_t*>(base + lay.planes);
@@ -636,16 +772,17 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
     a.d = s.d;
     a.E = s.E;
     a.Ep = Ep;
-    a.c_tiles = s.d / dw_tile_c();
-    a.e_tiles = (s.E + dw_tile_e(s) - 1) / dw_tile_e(s);
     a.splits = ns;
-    a.t_per_split = ((s.T + ns - 1) / ns + kKT - 1) / kKT * kKT;
-    if (dw_tile_e(s) == 32)
-      launch_dw<128, 32, 4, 1>(a, st);
-    else if (dw_tile_e(s) == 64)
-      launch_dw<128, 64, 4, 1>(a, st);
+    hipError_t e;
+    if (plan.be == 32)
+      e = launch_dw<DwCfg<1, 1, 4, 1, 2, 64, 3>>(a, st);
+    else if (plan.be == 64)
+      e = launch_dw<DwCfg<2, 1, 2, 2, 2, 64, 2>>(a, st);
+    else if (plan.bc == 128)
+      e = launch_dw<DwCfg<2, 2, 2, 2, 2, 32, 4>>(a, st);
     else
-      launch_dw<128, 128, 2, 2>(a, st);
+      e = launch_dw<DwCfg<4, 2, 2, 2, 2, 32, 3>>(a, st);
+    if (e != hipSuccess) return e;
   }
   if (g.dw && s.T > 0 && !bf16) {
     F32Args a{};
@@ -678,23 +815,22 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
                        dim3(kSumThreads), 0, st, a);
   }
   if (g.dx && s.T > 0 && bf16) {
-    const uint16_t* w = static_cast<const uint16_t*>(g.w_router);
-    if (Ep != s.E) {
-      uint16_t* wp = reinterpret_cast<uint16_t*>(base + lay.wpad);
-      hipLaunchKernelGGL(router_pad_rows, dim3(s.d / 8), dim3(kThreads), 0, st, w, wp, s.E, Ep);
-      w = wp;
-    }
     DxArgs a{};
+    a.w = static_cast<const uint16_t*>(g.w_router);
+    a.w_pitch = s.E;
+    if (s.E % 8 != 0) {
+      uint16_t* wp = reinterpret_cast<uint16_t*>(base + lay.wpad);
+      hipLaunchKernelGGL(router_pad_rows, dim3(s.d / 8), dim3(kThreads), 0, st, a.w, wp, s.E, Ep);
+      a.w = wp;
+      a.w_pitch = Ep;
+    }
     a.planes = planes;
-    a.w = w;
     a.dx = static_cast<uint16_t*>(g.dx);
     a.T = s.T;
     a.d = s.d;
-    a.Ep = Ep;
-    a.c_tiles = s.d / kDxTile;
-    a.t_tiles = (s.T + kDxTile - 1) / kDxTile;
-    hipLaunchKernelGGL(router_dx_bf16, dim3(xcd_grid(a.c_tiles * a.t_tiles)), dim3(kThreads), 0, st,
-                       a);
+    a.E = a.w_pitch;
+    const hipError_t e = launch_dx(a, Ep, st);
+    if (e != hipSuccess) return e;
   }
   if (g.dx && s.T > 0 && !bf16) {
     F32Args a{};
