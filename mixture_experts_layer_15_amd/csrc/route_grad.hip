@@ -146,8 +146,9 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void route
   uint64_t* keep = reinterpret_cast<uint64_t*>(smem + C::kLds);  // kMask: kSegment bits
   const int item = xcd_item(a.splits * a.e_tiles * a.c_tiles);
   if (item < 0) return;  // the whole workgroup
-  const int ct = item % a.c_tiles;
-  const int et = item / a.c_tiles % a.e_tiles;
+  // the expert tiles of a column tile are neighbours: they share x
+  const int et = item % a.e_tiles;
+  const int ct = item / a.e_tiles % a.c_tiles;
   const int split = item / (a.c_tiles * a.e_tiles);
   const int c0 = ct * C::BC, e0 = et * C::BE;
   const long long t0 = split * a.t_per_split;
