@@ -372,6 +372,8 @@ struct GateGradKernelArgs {
   GateGradArgs a;
   long long T;
   int E, k, Ep;
+  int blocks;               // workgroups of the rows; those behind copy pad_src
+  int d, act_bytes;
   long long rows_per_block;
 };
 
@@ -401,6 +403,19 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
   __shared__ int wtot[kGradWaves];
   const GateGradArgs& a = ka.a;
   const int E = ka.E, k = ka.k;
+  if ((int)blockIdx.x >= ka.blocks) {
+    const int stride = ((int)gridDim.x - ka.blocks) * kGradThreads;
+    for (int i = ((int)blockIdx.x - ka.blocks) * kGradThreads + (int)threadIdx.x; i < ka.d * ka.Ep;
+         i += stride) {
+      const int r = i / ka.Ep, e = i % ka.Ep;
+      const size_t from = (size_t)r * E + e;
+      if (ka.act_bytes == 2)
+        static_cast<uint16_t*>(a.pad_dst)[i] = e < E ? static_cast<const uint16_t*>(a.pad_src)[from] : uint16_t(0);
+      else
+        static_cast<float*>(a.pad_dst)[i] = e < E ? static_cast<const float*>(a.pad_src)[from] : 0.0f;
+    }
+    return;
+  }
   const int tid = threadIdx.x;
   const int w = tid / kWave, l = tid % kWave;
   const int g = l % S::L, r = l / S::L;
@@ -513,6 +528,21 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
       } else {
         if (a.dlogits && e < E) a.dlogits[t * E + e] = v[c];
       }
+    }
+    if (a.dl_rows) {
+      float* row = a.dl_rows + t * ka.Ep;
+#pragma unroll
+      for (int c = 0; c < S::C; ++c) {
+        const int e = (c * S::L + g) * S::V;
+        if constexpr (S::V == 4) {
+          if (e < E)
+            *reinterpret_cast<f32x4_t*>(row + e) =
+                f32x4_t{v[c * 4], v[c * 4 + 1], v[c * 4 + 2], v[c * 4 + 3]};
+        } else {
+          if (e < E) row[e] = v[c];
+        }
+      }
+      for (int e = E + g; e < ka.Ep; e += S::L) row[e] = 0.0f;
     }
     for (int pl = 0; pl < a.nplanes; ++pl) {
       uint16_t* row = a.planes + ((size_t)pl * ka.T + t) * ka.Ep;
@@ -631,7 +661,12 @@ hipError_t gate_grad(const Shape& s, const GateGradArgs& a, int Ep, hipStream_t 
   ka.E = s.E;
   ka.k = s.k;
   ka.Ep = Ep;
-  const int nb = grad_blocks(s, &ka.rows_per_block);
+  ka.blocks = grad_blocks(s, &ka.rows_per_block);
+  ka.d = s.d;
+  ka.act_bytes = act_bytes(s);
+  // 4096 values of the copy per workgroup, at most 256 of them
+  const long long pad = a.pad_src ? (long long)s.d * Ep : 0;
+  const int nb = ka.blocks + (int)std::min<long long>((pad + 4095) / 4096, 256);
   with_row_shape(s.E, [&](auto sh) {
     using S = decltype(sh);
     hipLaunchKernelGGL((gate_grad_rows<S>), dim3(nb), dim3(kGradThreads), 0, st, ka);

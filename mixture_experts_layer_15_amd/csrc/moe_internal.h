@@ -117,6 +117,9 @@ struct GateGradArgs {
   float* dlogits;          // [T][E] or null
   uint16_t* planes;        // [nplanes][T][Ep] bfloat16 planes whose sum is the gradient
   int nplanes;
+  float* dl_rows;          // [T][Ep] the gradient, columns from E on zero, or null
+  const void* pad_src;     // a matrix [d][E] of act values that is copied to
+  void* pad_dst;           // [d][Ep] (zeros behind E), or null
   void* zero_line;         // kZeroLineBytes that the kernel clears
   float* bias_part;        // [gate_grad_blocks][E] column sums per workgroup, or null
 };

@@ -10,7 +10,8 @@
 // all three planes: the products with the bfloat16 tokens are exact and only
 // the float32 sums round.  The tokens' gradient is rounded to bfloat16 at the
 // end, so two planes (16 bits, 2^-17 off) do for it.
-// float32 activations: both products on the float32 matrix instructions.
+// float32 activations: the same kernels on the float32 matrix instructions,
+// with dL as it is.
 #include <algorithm>
 #include <cmath>
 
@@ -21,7 +22,6 @@ namespace moe {
 namespace {
 
 constexpr int kXcds = 8;
-constexpr int kThreads = 256;
 
 // Consecutive workgroups run on consecutive XCDs: gives each XCD one run of
 // consecutive items, so that items that share operands share an L2.
@@ -100,34 +100,38 @@ __device__ __forceinline__ u32x2_t read_tr(uint32_t lds) {
 // take every KG-th step of 16 tokens and are added at the end.
 constexpr int kSegment = 16384;  // tokens whose mask bits are held in LDS
 
-template <int kRowBytes>
+template <bool kF32, int kRowBytes>
 __device__ __forceinline__ int tr_swz(int t) {
+  if constexpr (kF32) return 0;  // plain reads: a lane a value, consecutive lanes
   constexpr int R = kRowBytes >= 256 ? 1 : 256 / kRowBytes;  // rows per bank sweep
   constexpr int N = kRowBytes >= 256 ? 4 : kRowBytes / 64;
   return (t / R) % N;
 }
 
 struct DwArgs {
-  const uint16_t* x;       // [T][d]
-  const uint16_t* planes;  // [3][T][Ep]
-  const uint8_t* mask;     // [T] or null
+  const unsigned char* x;       // [T][d]
+  const unsigned char* planes;  // bf16: [3][T][Ep]; float32: [T][Ep]
+  const uint8_t* mask;          // [T] or null
   const unsigned char* zero;
-  float* out;              // [splits][d][E]
+  float* out;                   // [splits][d][E]
   long long T;
   int d, E, Ep;
   int c_tiles, e_tiles, splits;
-  long long t_per_split;   // a multiple of 64
+  long long t_per_split;        // a multiple of 64
 };
 
-template <int MB_, int NB_, int WC_, int WE_, int KG_, int KT_, int NST_>
+template <bool kF32_, int MB_, int NB_, int WC_, int WE_, int KG_, int KT_, int NST_>
 struct DwCfg {
+  static constexpr bool kF32 = kF32_;
   static constexpr int MB = MB_, NB = NB_, WC = WC_, WE = WE_, KG = KG_, KT = KT_, NST = NST_;
+  static constexpr int kSize = kF32 ? 4 : 2;    // bytes of a value
+  static constexpr int kPlanes = kF32 ? 1 : 3;
   static constexpr int kWaves = WC * WE * KG;
   static constexpr int kThreads = kWaves * kWave;
   static constexpr int BC = 32 * MB * WC, BE = 32 * NB * WE;
-  static constexpr int kRowX = BC * 2, kRowP = BE * 2;
+  static constexpr int kRowX = BC * kSize, kRowP = BE * kSize;
   static constexpr int kStageX = KT * kRowX, kStageP = KT * kRowP;
-  static constexpr int kStage = kStageX + 3 * kStageP;
+  static constexpr int kStage = kStageX + kPlanes * kStageP;
   static constexpr int kInstr = kStage / 1024;  // 1 KB loads of a stage
   static constexpr int kPerWave = (kInstr + kWaves - 1) / kWaves;
   static constexpr int kSteps = KT / 16 / KG;   // steps of a wave per stage
@@ -135,12 +139,13 @@ struct DwCfg {
   static_assert(kStageX % 1024 == 0 && kStageP % 1024 == 0, "whole loads");
   static_assert(KT % (16 * KG) == 0 && 64 % KT == 0, "whole steps");
   static_assert((NST - 1) * kPerWave < 64, "vmcnt range");
+  static_assert(kLds + kSegment / 8 <= 160 * 1024, "LDS budget");
   // the sum over the K groups passes one block row of every wave through LDS
   static_assert(KG == 1 || WC * WE * NB * 4096 <= kLds, "room for the sums");
 };
 
 template <class C, bool kMask>
-__global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void router_dw_bf16(DwArgs a) {
+__global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void router_dw(DwArgs a) {
   constexpr int MB = C::MB, NB = C::NB;
   extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t* keep = reinterpret_cast<uint64_t*>(smem + C::kLds);  // kMask: kSegment bits
@@ -165,22 +170,21 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void route
 #pragma unroll
   for (int i = 0; i < C::kPerWave; ++i) {
     const int n = w + C::kWaves * i;
+    constexpr int kPer16 = 16 / C::kSize;  // values of a load
     if (n * 1024 < C::kStageX) {
       const int q = n * 64 + l;
       const int r = q / (C::kRowX / 16), pc = q % (C::kRowX / 16);
-      const int c = pc ^ (tr_swz<C::kRowX>(r) << 2);
+      const int c = c0 + (pc ^ (tr_swz<C::kF32, C::kRowX>(r) << 2)) * kPer16;
       row[i] = r;
-      src[i] = reinterpret_cast<const unsigned char*>(a.x + (t0 + r) * a.d + c0 + c * 8);
-      if (c0 + c * 8 >= a.d) src[i] = nullptr;
+      src[i] = c < a.d ? a.x + ((t0 + r) * a.d + c) * C::kSize : nullptr;
     } else {
       const int m = n * 1024 - C::kStageX;
       const int pl = m / C::kStageP;
       const int q = (m % C::kStageP) / 16 + l;
       const int r = q / (C::kRowP / 16), pc = q % (C::kRowP / 16);
-      const int c = pc ^ (tr_swz<C::kRowP>(r) << 2);
+      const int e = e0 + (pc ^ (tr_swz<C::kF32, C::kRowP>(r) << 2)) * kPer16;
       row[i] = r;
-      src[i] = reinterpret_cast<const unsigned char*>(a.planes + (pl * a.T + t0 + r) * a.Ep + e0 + c * 8);
-      if (e0 + c * 8 >= a.Ep) src[i] = nullptr;
+      src[i] = e < a.Ep ? a.planes + ((pl * a.T + t0 + r) * a.Ep + e) * C::kSize : nullptr;
     }
   }
   auto load_stage = [&](long long t, int b) {  // t: tokens from t0
@@ -189,7 +193,7 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void route
       const int n = w + C::kWaves * i;
       if (C::kInstr % C::kWaves != 0 && n >= C::kInstr) continue;
       const bool isx = n * 1024 < C::kStageX;
-      const unsigned char* p = src[i] + t * (isx ? a.d : a.Ep) * 2;
+      const unsigned char* p = src[i] + t * (isx ? a.d : a.Ep) * C::kSize;
       bool live = src[i] != nullptr && t0 + t + row[i] < t1;
       if (kMask && isx) {
         const int k = (int)((t + row[i]) % kSegment);
@@ -199,20 +203,22 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void route
     }
   };
 
-  // operand read offsets: lane l covers column l % 32 of a block, tokens
-  // 8 (l / 32) + 0 .. 7 of each 16-deep step (two reads of four)
+  // operand read offsets: lane l covers column l % 32 of a block; bf16: tokens
+  // 8 (l / 32) + 0 .. 7 of each 16-deep step (two reads of four), float32:
+  // token 2 i + l / 32 of the i-th of its eight products
   const int kg = w / (C::WC * C::WE), wc = w % C::WC, we = w / C::WC % C::WE;
   const int j = l % 16;
-  const int r0 = 8 * (l / 32) + j / 4 + 16 * kg;
-  const int in_block = ((l % 32) / 16) * 32 + (j % 4) * 8;
+  const int r0 = C::kF32 ? l / 32 + 16 * kg : 8 * (l / 32) + j / 4 + 16 * kg;
+  const int in_block = C::kF32 ? (l % 32) * 4 : ((l % 32) / 16) * 32 + (j % 4) * 8;
+  constexpr int kBlock = 32 * C::kSize;
   uint32_t offx[MB], offp[NB];
 #pragma unroll
   for (int m = 0; m < MB; ++m)
-    offx[m] = lds0 + r0 * C::kRowX + (((wc * MB + m) ^ tr_swz<C::kRowX>(j / 4)) * 64) + in_block;
+    offx[m] = r0 * C::kRowX + ((wc * MB + m) ^ tr_swz<C::kF32, C::kRowX>(j / 4)) * kBlock + in_block;
 #pragma unroll
   for (int n = 0; n < NB; ++n)
-    offp[n] = lds0 + C::kStageX + r0 * C::kRowP +
-              (((we * NB + n) ^ tr_swz<C::kRowP>(j / 4)) * 64) + in_block;
+    offp[n] = C::kStageX + r0 * C::kRowP +
+              ((we * NB + n) ^ tr_swz<C::kF32, C::kRowP>(j / 4)) * kBlock + in_block;
 
   f32x16_t acc[MB][NB];
 #pragma unroll
@@ -252,23 +258,41 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void route
       lds_barrier();  // ... for every wave, and nobody reads stage s - 1 any more
       if (s + C::NST - 1 < stages)
         load_stage(s0 + (long long)(s + C::NST - 1) * C::KT, b == 0 ? C::NST - 1 : b - 1);
-      const uint32_t st = b * C::kStage;
+      const unsigned char* st = smem + b * C::kStage;
+      const uint32_t sa = lds0 + b * C::kStage;
 #pragma unroll
       for (int ks = 0; ks < C::kSteps; ++ks) {
-        bf16x8_t xa[MB];
+        const int kx = ks * 16 * C::KG * C::kRowX, kp = ks * 16 * C::KG * C::kRowP;
+        if constexpr (C::kF32) {
 #pragma unroll
-        for (int m = 0; m < MB; ++m)
-          xa[m] = operand(offx[m] + st + ks * 16 * C::KG * C::kRowX, 4 * C::kRowX);
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl)
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            const bf16x8_t pb =
-                operand(offp[n] + st + pl * C::kStageP + ks * 16 * C::KG * C::kRowP, 4 * C::kRowP);
+          for (int i = 0; i < 8; ++i) {
+            float xa[MB], pb[NB];
 #pragma unroll
             for (int m = 0; m < MB; ++m)
-              acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[m], pb, acc[m][n], 0, 0, 0);
+              xa[m] = *reinterpret_cast<const float*>(st + offx[m] + kx + 2 * i * C::kRowX);
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+              pb[n] = *reinterpret_cast<const float*>(st + offp[n] + kp + 2 * i * C::kRowP);
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+              for (int n = 0; n < NB; ++n)
+                acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x2f32(xa[m], pb[n], acc[m][n], 0, 0, 0);
           }
+        } else {
+          bf16x8_t xa[MB];
+#pragma unroll
+          for (int m = 0; m < MB; ++m) xa[m] = operand(sa + offx[m] + kx, 4 * C::kRowX);
+#pragma unroll
+          for (int pl = 0; pl < 3; ++pl)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              const bf16x8_t pb = operand(sa + offp[n] + pl * C::kStageP + kp, 4 * C::kRowP);
+#pragma unroll
+              for (int m = 0; m < MB; ++m)
+                acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa[m], pb, acc[m][n], 0, 0, 0);
+            }
+        }
       }
       __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads of the stage have returned
       b = b + 1 == C::NST ? 0 : b + 1;
@@ -321,10 +345,11 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void route
     }
 }
 
-// ---- dx, bf16
+// ---- dx
 // The sum is short (the experts, at most 512), the output long: each wave
 // keeps its columns' share of the router matrix in registers as MFMA operands
-// (MB blocks of 32 columns, KS steps of 16 experts: 4 MB KS registers) and
+// (MB blocks of 32 columns, KS steps of 16 experts, in float32 of 8: 4 MB KS
+// registers) and
 // runs over the tokens, whose planes pass through LDS, 32 NB tokens a stage, in
 // two buffers.  The waves of a workgroup have neighbouring columns and share
 // the stage.  The matrix is the A operand, with its rows in an order that
@@ -334,13 +359,13 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void route
 // no multiple of 256, 128), so that 16 consecutive rows at one logical chunk
 // lie in different banks.
 struct DxArgs {
-  const uint16_t* planes;  // [2 of 3][T][Ep]
-  const uint16_t* w;       // [d][w_pitch], experts behind E not read
-  uint16_t* dx;            // [T][d]
+  const unsigned char* planes;  // bf16: [2 of 3][T][Ep]; float32: [T][Ep]
+  const unsigned char* w;       // [d][w_pitch], experts behind E not read
+  unsigned char* dx;            // [T][d]
   long long T;
   int d, E, w_pitch;
-  int c_groups, t_ranges;  // workgroups: column groups x token ranges
-  int steps_per_range;     // stages
+  int c_groups, t_ranges;       // workgroups: column groups x token ranges
+  int steps_per_range;          // stages
 };
 
 // Column 16 h + q of a 32-column block is register q of lane half h of the
@@ -354,15 +379,17 @@ __device__ __forceinline__ int dx_swz(int t) {
   return P % 256 == 0 ? t & 15 : P % 128 == 0 ? (t >> 1) & 7 : (t >> 2) & 3;
 }
 
-template <int MB, int KS, int NB, int NW, int kMinWaves>
-__global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx_bf16(DxArgs a) {
-  constexpr int kDxTokens = 32 * NB;
+template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
+__global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
+  constexpr int kSize = kF32 ? 4 : 2;        // bytes of a value
+  constexpr int kPlanes = kF32 ? 1 : 2;
+  constexpr int kTokens = 32 * NB;
   constexpr int P = KS * 32;                 // bytes of a staged row
-  constexpr int kPlane = kDxTokens * P;
-  constexpr int kStage = 2 * kPlane;
+  constexpr int kPlane = kTokens * P;
+  constexpr int kStage = kPlanes * kPlane;
   constexpr int kPerWave = kStage / 1024 / NW;
   static_assert(kStage % (1024 * NW) == 0, "whole loads per wave");
-  constexpr int kStores = MB * NB * 2;       // 16-byte stores of a lane per stage
+  constexpr int kStores = MB * NB * kSize;   // 16-byte stores of a lane per stage
   extern __shared__ __align__(1024) unsigned char smem[];
   const int item = xcd_item(a.c_groups * a.t_ranges);
   if (item < 0) return;  // the whole workgroup
@@ -374,7 +401,7 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx_bf16(DxArgs a)
   const int l = tid % kWave;
   const int h = l / 32;
   const int c0 = (cg * NW + w) * MB * 32;    // this wave's columns (may be behind d)
-  const long long steps = (a.T + kDxTokens - 1) / kDxTokens;
+  const long long steps = (a.T + kTokens - 1) / kTokens;
   const long long s0 = (long long)range * a.steps_per_range;
   const int ns = (int)min((long long)a.steps_per_range, steps - s0);
   if (ns <= 0) return;  // the whole workgroup
@@ -387,25 +414,26 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx_bf16(DxArgs a)
       const int n = w * kPerWave + i;
       const int q = n * 64 + l;               // 16-byte chunk of the stage
       const int row = q / (P / 16), pc = q % (P / 16);
-      const int pl = row / kDxTokens, r = row % kDxTokens;
+      const int pl = row / kTokens, r = row % kTokens;
       const int c = pc ^ dx_swz<KS>(r);
-      const long long t = min((s0 + s) * kDxTokens + r, a.T - 1);
-      dma16(a.planes + (pl * a.T + t) * (KS * 16) + c * 8, lds0 + b * kStage + n * 1024);
+      const long long t = min((s0 + s) * kTokens + r, a.T - 1);
+      dma16(a.planes + (pl * a.T + t) * P + c * 16, lds0 + b * kStage + n * 1024);
     }
   };
   load_stage(0, 0);
 
-  // lane l: matrix row dx_feat(l % 32) of a block, experts 16 ks + 8 h .. + 7
-  bf16x8_t wf[MB][KS];
+  // lane l: matrix row dx_feat(l % 32) of a block, the 16 bytes h of each
+  // step's 32 (float32: the step's product i takes value i of both halves)
+  u32x4_t wf[MB][KS];
 #pragma unroll
   for (int m = 0; m < MB; ++m) {
     const int c = min(c0 + m * 32 + dx_feat(l % 32), a.d - 1);
-    const uint16_t* row = a.w + (size_t)c * a.w_pitch + 8 * h;
+    const unsigned char* row = a.w + (size_t)c * a.w_pitch * kSize + 16 * h;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      u32x4_t v = {0, 0, 0, 0};
-      if (16 * ks + 8 * h < a.E) v = *reinterpret_cast<const u32x4_t*>(row + 16 * ks);
-      wf[m][ks] = __builtin_bit_cast(bf16x8_t, v);
+      wf[m][ks] = u32x4_t{0, 0, 0, 0};
+      if (32 * ks + 16 * h < a.E * kSize)
+        wf[m][ks] = *reinterpret_cast<const u32x4_t*>(row + 32 * ks);
     }
   }
   // operand read: lane l has token l % 32 of a block, chunk 2 ks + h
@@ -434,113 +462,54 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx_bf16(DxArgs a)
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int pl = 0; pl < 2; ++pl)
+      for (int pl = 0; pl < kPlanes; ++pl) {
+        u32x4_t pb[NB];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          const bf16x8_t pb = *reinterpret_cast<const bf16x8_t*>(
+        for (int n = 0; n < NB; ++n)
+          pb[n] = *reinterpret_cast<const u32x4_t*>(
               st + pl * kPlane + (base[n] ^ ((ks % kGroup) << 5)) + ks / kGroup * kGroup * 32);
+        if constexpr (kF32) {
 #pragma unroll
-          for (int m = 0; m < MB; ++m)
-            acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[m][ks], pb, acc[m][n], 0, 0, 0);
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+              for (int m = 0; m < MB; ++m)
+                acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                    __uint_as_float(wf[m][ks][i]), __uint_as_float(pb[n][i]), acc[m][n], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+              acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  __builtin_bit_cast(bf16x8_t, wf[m][ks]), __builtin_bit_cast(bf16x8_t, pb[n]),
+                  acc[m][n], 0, 0, 0);
         }
+      }
     __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads of the stage have returned
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      const long long t = (s0 + s) * kDxTokens + n * 32 + l % 32;
+      const long long t = (s0 + s) * kTokens + n * 32 + l % 32;
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
         const f32x16_t& v = acc[m][n];
-        uint16_t* o = a.dx + t * a.d + c0 + m * 32 + 16 * h;
+        u32x4_t* o = reinterpret_cast<u32x4_t*>(a.dx + (t * a.d + c0 + m * 32 + 16 * h) * kSize);
         if (t < a.T && c0 + m * 32 < a.d) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<u32x4_t*>(o + 8 * i) =
-                u32x4_t{pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                        pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
-                        pack_bf16x2(v[8 * i + 6], v[8 * i + 7])};
+          for (int i = 0; i < kSize; ++i) {
+            if constexpr (kF32)
+              o[i] = u32x4_t{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                             __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
+            else
+              o[i] = u32x4_t{pack_bf16x2(v[8 * i], v[8 * i + 1]),
+                             pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                             pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                             pack_bf16x2(v[8 * i + 6], v[8 * i + 7])};
+          }
         }
       }
     }
-  }
-}
-
-// The router matrix [d][E] with rows of Ep values (zeros behind E) for
-// router_dx_bf16, whose loads are 16-byte aligned; one workgroup per 8 rows.
-__global__ __launch_bounds__(kThreads) void router_pad_rows(const uint16_t* w, uint16_t* wp, int E,
-                                                            int Ep) {
-  const size_t r0 = (size_t)blockIdx.x * 8;
-  for (int i = threadIdx.x; i < 8 * Ep; i += kThreads) {
-    const int r = i / Ep, e = i % Ep;
-    wp[(r0 + r) * Ep + e] = e < E ? w[(r0 + r) * E + e] : uint16_t(0);
-  }
-}
-
-// ---- float32: 64 x 64 tiles, each wave a 32 x 32 block of
-// v_mfma_f32_32x32x2_f32, K-major LDS stages 32 deep.
-//   kDx:  rows = tokens, columns = x columns, sum over the experts
-//   else: rows = x columns, columns = experts, sum over a range of tokens
-struct F32Args {
-  const float* x;
-  const float* w;
-  const float* dl;
-  const uint8_t* mask;
-  float* out;
-  long long T;
-  int d, E;
-  int m_tiles, n_tiles;
-  long long t_per_split;
-};
-
-template <bool kDx>
-__global__ __launch_bounds__(kThreads) void router_grad_f32(F32Args a) {
-  constexpr int BK = 32, B = 64, P = B + 1;
-  __shared__ float As[BK][P], Bs[BK][P];
-  const int tid = threadIdx.x;
-  const int w = tid / kWave, l = tid % kWave;
-  const long long mt = blockIdx.x % a.m_tiles;
-  const int nt = blockIdx.x / a.m_tiles;
-  const long long m0 = mt * B;
-  const int n0 = nt * B;
-  const int split = blockIdx.y;
-  const long long k0 = kDx ? 0 : split * a.t_per_split;
-  const long long k1 = kDx ? a.E : min(k0 + a.t_per_split, a.T);
-  f32x16_t acc = f32x16_t{};
-  const int wm = (w % 2) * 32, wn = (w / 2) * 32;
-  for (long long kb = k0; kb < k1; kb += BK) {
-    __syncthreads();
-    if constexpr (kDx) {
-      // experts are consecutive in both operands: thread i on expert i % 32
-      const int k = tid % BK;
-      for (int r = tid / BK; r < B; r += kThreads / BK) {
-        const bool in = kb + k < k1;
-        As[k][r] = in && m0 + r < a.T ? a.dl[(m0 + r) * a.E + kb + k] : 0.0f;
-        Bs[k][r] = in ? a.w[(size_t)(n0 + r) * a.E + kb + k] : 0.0f;
-      }
-    } else {
-      const int c = tid % B;
-      for (int k = tid / B; k < BK; k += kThreads / B) {
-        const long long t = kb + k;
-        const bool in = t < k1;
-        const bool live = in && (!a.mask || a.mask[t] != 0);
-        As[k][c] = live ? a.x[t * a.d + m0 + c] : 0.0f;
-        Bs[k][c] = in && n0 + c < a.E ? a.dl[t * a.E + n0 + c] : 0.0f;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < BK; kk += 2)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(As[kk + l / 32][wm + l % 32],
-                                                 Bs[kk + l / 32][wn + l % 32], acc, 0, 0, 0);
-  }
-  const int n = n0 + wn + l % 32;
-  const int N = kDx ? a.d : a.E;
-  const long long M = kDx ? a.T : a.d;
-  float* out = a.out + (kDx ? 0 : (size_t)split * a.d * a.E);
-  if (n >= N) return;
-#pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const long long m = m0 + wm + 8 * (q / 4) + 4 * (l / 32) + q % 4;
-    if (m < M) out[m * N + n] = acc[q];
   }
 }
 
@@ -597,7 +566,7 @@ __global__ __launch_bounds__(kSumThreads) void router_grad_sum(SumArgs a) {
 // Experts in a row of the planes: the steps that router_dx_bf16 is made for.
 int padded_experts(const Shape& s) { return s.E <= 32 ? 32 : (s.E + 63) / 64 * 64; }
 
-// Plan of the bf16 dW_r kernel: its tile, and the parts of the token range.
+// Plan of the dW_r kernel: its tile, and the parts of the token range.
 struct DwPlan {
   int bc, be;
   int splits;
@@ -607,10 +576,10 @@ struct DwPlan {
 // over the 256 compute units times (start and end of a workgroup, 4 us, plus
 // its tokens: 44 ns each on the 256 x 128 tile, 25 ns on 128 x 128, 14 ns on
 // the narrow ones, as measured), plus its partial sums, written and read at
-// 4 TB/s.  The tall tile has the better rate (1139 against 976 TFLOP/s of
-// matrix instructions on 16384 tokens of 7168 x 256: 158 against 185 us) but
+// 4 TB/s.  The tall tile has the better rate (1075 against 913 TFLOP/s of
+// matrix instructions on 16384 tokens of 7168 x 256: 168 against 198 us) but
 // needs that many more parts to fill the chip: on 8192 tokens of 2048 x 128 it
-// takes 21.6 us and 32 parts, the square one 18.5 us and 16.
+// takes 22.0 us and 32 parts, the square one 18.8 us and 16.
 double dw_cost(const Shape& s, int bc, int be, double ns_token, int splits) {
   const double tiles = (double)((s.d + bc - 1) / bc) * ((s.E + be - 1) / be);
   const double rounds = std::ceil(tiles * splits / 256.0);
@@ -621,14 +590,6 @@ double dw_cost(const Shape& s, int bc, int be, double ns_token, int splits) {
 
 DwPlan dw_plan(const Shape& s) {
   DwPlan best{128, 32, 1};
-  if (s.act != kBF16) {
-    best = DwPlan{64, 64, 1};
-    const long long tiles = (long long)(s.d / 64) * ((s.E + 63) / 64);
-    long long n = std::min<long long>((512 + tiles - 1) / tiles, (s.T + 127) / 128);
-    n = std::min<long long>(n, std::max<long long>(s.T / (4LL * s.E), 4));
-    best.splits = (int)std::max<long long>(std::min<long long>(n, 64), 1);
-    return best;
-  }
   double cost = -1.0;
   auto offer = [&](int bc, int be, double ns_token) {
     for (int n = 1; n <= 64 && (n == 1 || (long long)n * 64 <= s.T + 63); ++n) {
@@ -639,19 +600,20 @@ DwPlan dw_plan(const Shape& s) {
       }
     }
   };
+  const bool bf16 = s.act == kBF16;
   if (s.E <= 32) {
-    offer(128, 32, 14.0);
+    offer(128, 32, bf16 ? 14.0 : 22.0);
   } else if (s.E <= 64) {
-    offer(128, 64, 14.0);
+    offer(128, 64, bf16 ? 14.0 : 30.0);
   } else {
-    offer(128, 128, 25.0);
-    offer(256, 128, 44.0);
+    offer(128, 128, bf16 ? 25.0 : 60.0);
+    if (bf16) offer(256, 128, 44.0);
   }
   return best;
 }
 
 struct GradLayout {
-  size_t zero, planes, wpad, dl, bias, dw, total;
+  size_t zero, planes, wpad, bias, dw, total;
 };
 
 GradLayout grad_layout(const Shape& s) {
@@ -668,7 +630,8 @@ GradLayout grad_layout(const Shape& s) {
     L.planes = take((size_t)3 * s.T * Ep * 2);
     L.wpad = take(s.E % 8 != 0 ? (size_t)s.d * Ep * 2 : 0);
   } else {
-    L.dl = take((size_t)s.T * s.E * 4);
+    L.planes = take((size_t)s.T * Ep * 4);
+    L.wpad = take(s.E % 4 != 0 ? (size_t)s.d * Ep * 4 : 0);
   }
   L.bias = take((size_t)gate_grad_blocks(s) * s.E * 4);
   const int ns = dw_plan(s).splits;
@@ -686,25 +649,25 @@ hipError_t launch_dw(DwArgs a, hipStream_t st) {
   const int lds = C::kLds + (a.mask ? kSegment / 8 : 0);
   if (a.mask) {
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(&router_dw_bf16<C, true>), lds, done);
+    const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(&router_dw<C, true>), lds, done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((router_dw_bf16<C, true>), grid, dim3(C::kThreads), lds, st, a);
+    hipLaunchKernelGGL((router_dw<C, true>), grid, dim3(C::kThreads), lds, st, a);
   } else {
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(&router_dw_bf16<C, false>), lds, done);
+    const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(&router_dw<C, false>), lds, done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((router_dw_bf16<C, false>), grid, dim3(C::kThreads), lds, st, a);
+    hipLaunchKernelGGL((router_dw<C, false>), grid, dim3(C::kThreads), lds, st, a);
   }
   return hipGetLastError();
 }
 
-template <int MB, int KS, int NB, int NW, int kMinWaves>
+template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
 hipError_t launch_dx_as(DxArgs a, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
   constexpr int kTokens = 32 * NB;
-  constexpr int kLds = 2 * 2 * kTokens * KS * 32;
+  constexpr int kLds = 2 * (kF32 ? 1 : 2) * kTokens * KS * 32;
   static_assert(kLds <= 160 * 1024, "LDS budget");
-  const void* kern = reinterpret_cast<const void*>(&router_dx_bf16<MB, KS, NB, NW, kMinWaves>);
+  const void* kern = reinterpret_cast<const void*>(&router_dx<kF32, MB, KS, NB, NW, kMinWaves>);
   const hipError_t e = set_lds_attr(kern, kLds, done);
   if (e != hipSuccess) return e;
   const int cols = MB * 32 * NW;
@@ -714,24 +677,35 @@ hipError_t launch_dx_as(DxArgs a, hipStream_t st) {
   const int slots = std::max(256 * 4 * kMinWaves / NW / a.c_groups, 1);
   a.steps_per_range = (int)std::max<long long>((steps + slots - 1) / slots, 1);
   a.t_ranges = (int)((steps + a.steps_per_range - 1) / a.steps_per_range);
-  hipLaunchKernelGGL((router_dx_bf16<MB, KS, NB, NW, kMinWaves>),
+  hipLaunchKernelGGL((router_dx<kF32, MB, KS, NB, NW, kMinWaves>),
                      dim3(xcd_grid(a.c_groups * a.t_ranges)), dim3(NW * kWave), kLds, st, a);
   return hipGetLastError();
 }
 
 // The variant by the experts of a row: a wave's share of the matrix takes
-// 4 MB KS registers, a stage 64 NB KS 32 bytes of LDS.
-hipError_t launch_dx(const DxArgs& a, int Ep, hipStream_t st) {
+// 4 MB KS registers, a stage 32 NB x 32 KS bytes of LDS a plane.
+hipError_t launch_dx(const DxArgs& a, int Ep, bool f32, hipStream_t st) {
+  if (f32) switch (Ep) {
+      case 32: return launch_dx_as<true, 2, 4, 2, 4, 2>(a, st);
+      case 64: return launch_dx_as<true, 2, 8, 2, 4, 2>(a, st);
+      case 128: return launch_dx_as<true, 2, 16, 2, 8, 2>(a, st);
+      case 192: return launch_dx_as<true, 2, 24, 2, 4, 1>(a, st);
+      case 256: return launch_dx_as<true, 2, 32, 2, 4, 1>(a, st);
+      case 320: return launch_dx_as<true, 1, 40, 1, 4, 1>(a, st);
+      case 384: return launch_dx_as<true, 1, 48, 1, 4, 1>(a, st);
+      case 448: return launch_dx_as<true, 1, 56, 1, 4, 1>(a, st);
+      default: return launch_dx_as<true, 1, 64, 1, 4, 1>(a, st);
+    }
   switch (Ep) {
-    case 32: return launch_dx_as<2, 2, 2, 4, 2>(a, st);
-    case 64: return launch_dx_as<2, 4, 2, 4, 2>(a, st);
-    case 128: return launch_dx_as<2, 8, 2, 4, 2>(a, st);
-    case 192: return launch_dx_as<2, 12, 2, 8, 2>(a, st);
-    case 256: return launch_dx_as<2, 16, 2, 8, 2>(a, st);
-    case 320: return launch_dx_as<2, 20, 1, 4, 1>(a, st);
-    case 384: return launch_dx_as<2, 24, 1, 4, 1>(a, st);
-    case 448: return launch_dx_as<2, 28, 1, 4, 1>(a, st);
-    default: return launch_dx_as<2, 32, 1, 4, 1>(a, st);
+    case 32: return launch_dx_as<false, 2, 2, 2, 4, 2>(a, st);
+    case 64: return launch_dx_as<false, 2, 4, 2, 4, 2>(a, st);
+    case 128: return launch_dx_as<false, 2, 8, 2, 4, 2>(a, st);
+    case 192: return launch_dx_as<false, 2, 12, 2, 8, 2>(a, st);
+    case 256: return launch_dx_as<false, 2, 16, 2, 8, 2>(a, st);
+    case 320: return launch_dx_as<false, 2, 20, 1, 4, 1>(a, st);
+    case 384: return launch_dx_as<false, 2, 24, 1, 4, 1>(a, st);
+    case 448: return launch_dx_as<false, 2, 28, 1, 4, 1>(a, st);
+    default: return launch_dx_as<false, 2, 32, 1, 4, 1>(a, st);
   }
 }
 
@@ -745,26 +719,38 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
   const int Ep = padded_experts(s);
   const DwPlan plan = dw_plan(s);
   const int ns = plan.splits;
-  const bool bf16 = s.act == kBF16;
+  const bool f32 = s.act != kBF16;
+  const bool products = s.T > 0 && (g.dw || g.dx);
   float* bias_part = reinterpret_cast<float*>(base + lay.bias);
-  uint16_t* planes = reinterpret_cast<uint16_t*>(base + lay.planes);
-  float* dl = g.dlogits;
-  if (!bf16 && !dl && (g.dw || g.dx)) dl = reinterpret_cast<float*>(base + lay.dl);
   float* part = ns > 1 ? reinterpret_cast<float*>(base + lay.dw) : g.dw;
+  // what the products read: the planes, or float32 rows of Ep values (the
+  // caller's, if they are as long)
+  unsigned char* planes = base + lay.planes;
+  if (f32 && g.dlogits && Ep == s.E) planes = reinterpret_cast<unsigned char*>(g.dlogits);
 
   if (s.T > 0) {
     GateGradArgs ga = g.gate;
-    ga.dlogits = dl;
-    ga.planes = planes;
-    ga.nplanes = !bf16 ? 0 : g.dw ? 3 : g.dx ? 2 : 0;
+    ga.dlogits = g.dlogits;
+    if (products && f32 && planes != reinterpret_cast<unsigned char*>(g.dlogits))
+      ga.dl_rows = reinterpret_cast<float*>(planes);
+    if (products && !f32) {
+      ga.planes = reinterpret_cast<uint16_t*>(planes);
+      ga.nplanes = g.dw ? 3 : 2;
+    }
     ga.zero_line = base + lay.zero;
     ga.bias_part = g.dbias ? bias_part : nullptr;
-    hipError_t e = gate_grad(s, ga, Ep, st);
+    // rows of the matrix that 16-byte loads cannot take are copied with Ep
+    // values each, by workgroups of the same launch
+    if (g.dx && s.E % (f32 ? 4 : 8) != 0) {
+      ga.pad_src = g.w_router;
+      ga.pad_dst = base + lay.wpad;
+    }
+    const hipError_t e = gate_grad(s, ga, Ep, st);
     if (e != hipSuccess) return e;
   }
-  if (g.dw && s.T > 0 && bf16) {
+  if (g.dw && s.T > 0) {
     DwArgs a{};
-    a.x = static_cast<const uint16_t*>(g.x);
+    a.x = static_cast<const unsigned char*>(g.x);
     a.planes = planes;
     a.mask = g.gate.mask;
     a.zero = base + lay.zero;
@@ -775,30 +761,17 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
     a.Ep = Ep;
     a.splits = ns;
     hipError_t e;
-    if (plan.be == 32)
-      e = launch_dw<DwCfg<1, 1, 4, 1, 2, 64, 3>>(a, st);
-    else if (plan.be == 64)
-      e = launch_dw<DwCfg<2, 1, 2, 2, 2, 64, 2>>(a, st);
-    else if (plan.bc == 128)
-      e = launch_dw<DwCfg<2, 2, 2, 2, 2, 32, 4>>(a, st);
+    if (f32)
+      e = plan.be == 32   ? launch_dw<DwCfg<true, 1, 1, 4, 1, 2, 64, 3>>(a, st)
+          : plan.be == 64 ? launch_dw<DwCfg<true, 2, 1, 2, 2, 2, 64, 2>>(a, st)
+                          : launch_dw<DwCfg<true, 2, 2, 2, 2, 2, 32, 4>>(a, st);
+    else if (plan.bc == 256)
+      e = launch_dw<DwCfg<false, 4, 2, 2, 2, 2, 32, 3>>(a, st);
     else
-      e = launch_dw<DwCfg<4, 2, 2, 2, 2, 32, 3>>(a, st);
+      e = plan.be == 32   ? launch_dw<DwCfg<false, 1, 1, 4, 1, 2, 64, 3>>(a, st)
+          : plan.be == 64 ? launch_dw<DwCfg<false, 2, 1, 2, 2, 2, 64, 2>>(a, st)
+                          : launch_dw<DwCfg<false, 2, 2, 2, 2, 2, 32, 4>>(a, st);
     if (e != hipSuccess) return e;
-  }
-  if (g.dw && s.T > 0 && !bf16) {
-    F32Args a{};
-    a.x = static_cast<const float*>(g.x);
-    a.dl = dl;
-    a.mask = g.gate.mask;
-    a.out = part;
-    a.T = s.T;
-    a.d = s.d;
-    a.E = s.E;
-    a.m_tiles = s.d / 64;
-    a.n_tiles = (s.E + 63) / 64;
-    a.t_per_split = ((s.T + ns - 1) / ns + 31) / 32 * 32;
-    hipLaunchKernelGGL(router_grad_f32<false>, dim3(a.m_tiles * a.n_tiles, ns), dim3(kThreads), 0,
-                       st, a);
   }
   const bool sum_w = g.dw && (ns > 1 || s.T == 0);
   if (sum_w || g.dbias) {
@@ -812,39 +785,22 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
     a.dbias = g.dbias;
     a.nb = s.T == 0 ? 0 : gate_grad_blocks(s);
     a.E = s.E;
-    hipLaunchKernelGGL(router_grad_sum, dim3(a.w_blocks + (g.dbias ? (s.E + kSumCols - 1) / kSumCols : 0)),
+    hipLaunchKernelGGL(router_grad_sum,
+                       dim3(a.w_blocks + (g.dbias ? (s.E + kSumCols - 1) / kSumCols : 0)),
                        dim3(kSumThreads), 0, st, a);
   }
-  if (g.dx && s.T > 0 && bf16) {
+  if (g.dx && s.T > 0) {
+    const bool padded = s.E % (f32 ? 4 : 8) != 0;
     DxArgs a{};
-    a.w = static_cast<const uint16_t*>(g.w_router);
-    a.w_pitch = s.E;
-    if (s.E % 8 != 0) {
-      uint16_t* wp = reinterpret_cast<uint16_t*>(base + lay.wpad);
-      hipLaunchKernelGGL(router_pad_rows, dim3(s.d / 8), dim3(kThreads), 0, st, a.w, wp, s.E, Ep);
-      a.w = wp;
-      a.w_pitch = Ep;
-    }
     a.planes = planes;
-    a.dx = static_cast<uint16_t*>(g.dx);
-    a.T = s.T;
-    a.d = s.d;
+    a.w = padded ? base + lay.wpad : static_cast<const unsigned char*>(g.w_router);
+    a.w_pitch = padded ? Ep : s.E;
     a.E = a.w_pitch;
-    const hipError_t e = launch_dx(a, Ep, st);
-    if (e != hipSuccess) return e;
-  }
-  if (g.dx && s.T > 0 && !bf16) {
-    F32Args a{};
-    a.w = static_cast<const float*>(g.w_router);
-    a.dl = dl;
-    a.out = static_cast<float*>(g.dx);
+    a.dx = static_cast<unsigned char*>(g.dx);
     a.T = s.T;
     a.d = s.d;
-    a.E = s.E;
-    a.m_tiles = (s.T + 63) / 64;
-    a.n_tiles = s.d / 64;
-    hipLaunchKernelGGL(router_grad_f32<true>, dim3(a.m_tiles * a.n_tiles), dim3(kThreads), 0, st,
-                       a);
+    const hipError_t e = launch_dx(a, Ep, f32, st);
+    if (e != hipSuccess) return e;
   }
   return hipGetLastError();
 }
