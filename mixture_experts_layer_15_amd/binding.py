@@ -8,6 +8,7 @@ used for device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import itertools
 import os
 import struct
 from typing import Optional
@@ -55,6 +56,7 @@ class RouteBackwardArgs(ctypes.Structure):
 
 
 _GRAD = "PPqi4x"   # moe_grad_t
+_GRAD_CODE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 _lib = None
 
@@ -366,22 +368,27 @@ class GradList:
         out = grads if out is None else list(out)
         if len(out) != len(grads):
             _refuse(c, f"{len(out)} outputs for {len(grads)} gradients")
-        kind = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
-        flat = []
-        self.device = grads[0].get_device() if grads else None
-        for g, o in zip(grads, out):
-            code = kind.get(g.dtype)
-            if code is None:
-                raise MoEError(c, MOE_ERR_UNSUPPORTED, f"a gradient is {g.dtype}, not float32 or bfloat16")
-            n, dev = g.numel(), g.get_device()
-            if not g.is_contiguous():
-                _refuse(c, "a gradient is not contiguous")
-            if dev != self.device:
-                _refuse(c, "the gradients are on more than one device")
-            if o is not g and (o.dtype is not g.dtype or o.numel() != n or not o.is_contiguous()
-                               or o.get_device() != dev):
+        T = torch.Tensor   # (maps over the methods: a list of 100 tensors takes 30 us)
+        codes = list(map(_GRAD_CODE.get, [g.dtype for g in grads]))
+        if None in codes:
+            raise MoEError(c, MOE_ERR_UNSUPPORTED,
+                           f"a gradient is {grads[codes.index(None)].dtype}, not float32 or bfloat16")
+        sizes = list(map(T.numel, grads))
+        devices = set(map(T.get_device, grads))
+        if not all(map(T.is_contiguous, grads)):
+            _refuse(c, "a gradient is not contiguous")
+        if len(devices) > 1:
+            _refuse(c, "the gradients are on more than one device")
+        self.device = devices.pop() if devices else None
+        at = list(map(T.data_ptr, grads))
+        to = at
+        if out is not grads:
+            if (list(map(_GRAD_CODE.get, [o.dtype for o in out])) != codes
+                    or list(map(T.numel, out)) != sizes or not all(map(T.is_contiguous, out))
+                    or any(d != self.device for d in map(T.get_device, out))):
                 _refuse(c, "an output has another type, size, layout or device than its gradient")
-            flat += (g.data_ptr(), o.data_ptr(), n, code)
+            to = list(map(T.data_ptr, out))
+        flat = itertools.chain.from_iterable(zip(at, to, sizes, codes))
         self.n = len(grads)
         self.tensors = (grads, out)
         self.array = struct.pack(_GRAD * self.n, *flat)

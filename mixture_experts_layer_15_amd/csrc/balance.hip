@@ -201,6 +201,16 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
   const float* logits = a.logits + t0 * a.E;
   const int32_t* idx = a.idx + t0 * a.k;
   const uint8_t* mask = a.mask ? a.mask + t0 : nullptr;
+  // a row's logits are loaded one row ahead, the first before the counting
+  // (masked rows too: what they hold is dropped)
+  float cur[S::Q];
+  bool keep = false;
+  auto load = [&](int t) {
+    keep = t < rows && (!mask || mask[t] != 0);
+    if (t < rows) load_row<S>(logits + (long long)t * a.E, a.E, g, cur);
+  };
+  int t = w * S::R + r;
+  load(t);
   for (int e = tid; e < a.E; e += kThreads) hist[e] = 0;
   if (!kSolo && blockIdx.x == 0 && tid == 0) *a.joined = 0;
   __syncthreads();
@@ -216,10 +226,13 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
   for (int q = 0; q < S::Q; ++q) acc[q] = 0.0f;
   double z = 0.0;
   int n = 0;
-  for (int t = w * S::R + r; t < rows; t += kWaves * S::R) {
-    if (mask && mask[t] == 0) continue;  // the same for the group's lanes
+  for (; t < rows; t += kWaves * S::R) {
     float v[S::Q], inv;
-    load_row<S>(logits + (long long)t * a.E, a.E, g, v);
+#pragma unroll
+    for (int q = 0; q < S::Q; ++q) v[q] = cur[q];
+    const bool live = keep;  // the same for the group's lanes
+    load(t + kWaves * S::R);
+    if (!live) continue;
     const float lse = row_exp<S>(v, inv);
 #pragma unroll
     for (int q = 0; q < S::Q; ++q) acc[q] = fmaf(v[q], inv, acc[q]);
@@ -373,7 +386,7 @@ struct GateGradKernelArgs {
   long long T;
   int E, k, Ep;
   int blocks;               // workgroups of the rows; those behind copy pad_src
-  int d, act_bytes;
+  int act_bytes;
   long long rows_per_block;
 };
 
@@ -400,54 +413,82 @@ template <class S>
 __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArgs ka) {
   __shared__ float red[kGradWaves * kMaxExperts];
   __shared__ __align__(16) float sparse[kGradWaves * kWave * S::Q];  // [wave][row][L Q >= E]
-  __shared__ int wtot[kGradWaves];
   const GateGradArgs& a = ka.a;
   const int E = ka.E, k = ka.k;
-  if ((int)blockIdx.x >= ka.blocks) {
-    const int stride = ((int)gridDim.x - ka.blocks) * kGradThreads;
-    for (int i = ((int)blockIdx.x - ka.blocks) * kGradThreads + (int)threadIdx.x; i < ka.d * ka.Ep;
-         i += stride) {
-      const int r = i / ka.Ep, e = i % ka.Ep;
-      const size_t from = (size_t)r * E + e;
-      if (ka.act_bytes == 2)
-        static_cast<uint16_t*>(a.pad_dst)[i] = e < E ? static_cast<const uint16_t*>(a.pad_src)[from] : uint16_t(0);
-      else
-        static_cast<float*>(a.pad_dst)[i] = e < E ? static_cast<const float*>(a.pad_src)[from] : 0.0f;
+  const int tid = threadIdx.x;
+  const int w = tid / kWave, l = tid % kWave;
+  if ((int)blockIdx.x >= ka.blocks) {  // a row of pad_src per wave
+    const int r = ((int)blockIdx.x - ka.blocks) * kGradWaves + w;
+    if (ka.act_bytes == 2) {
+      const uint16_t* from = static_cast<const uint16_t*>(a.pad_src) + (size_t)r * E;
+      uint16_t* to = static_cast<uint16_t*>(a.pad_dst) + (size_t)r * ka.Ep;
+#pragma unroll 4
+      for (int e = l; e < ka.Ep; e += kWave) to[e] = e < E ? from[e] : uint16_t(0);
+    } else {
+      const float* from = static_cast<const float*>(a.pad_src) + (size_t)r * E;
+      float* to = static_cast<float*>(a.pad_dst) + (size_t)r * ka.Ep;
+#pragma unroll 4
+      for (int e = l; e < ka.Ep; e += kWave) to[e] = e < E ? from[e] : 0.0f;
     }
     return;
   }
-  const int tid = threadIdx.x;
-  const int w = tid / kWave, l = tid % kWave;
   const int g = l % S::L, r = l / S::L;
   const bool losses = a.dlosses != nullptr;
+  const bool gates = a.dtopk_w != nullptr;
+  const long long t0 = blockIdx.x * ka.rows_per_block;
+  const long long t1 = min(t0 + ka.rows_per_block, ka.T);
+
+  // what a row's lanes read, loaded one row ahead
+  struct Row {
+    float v[S::Q];
+    int id;
+    float gw, dg;
+    bool live;
+  };
+  auto load = [&](long long t, Row& x) {
+    x.live = t < t1 && (!a.mask || a.mask[t] != 0);
+    x.id = -1;
+    x.gw = x.dg = 0.0f;
+#pragma unroll
+    for (int q = 0; q < S::Q; ++q) x.v[q] = 0.0f;
+    if (t >= t1) return;
+    if (losses) load_row<S>(a.logits + t * E, E, g, x.v);
+    if (gates && g < k) {
+      x.id = a.idx[t * k + g];
+      x.gw = a.topk_w[t * k + g];
+      x.dg = a.dtopk_w[t * k + g];
+    }
+  };
+  long long t = t0 + w * S::R + r;
+  Row cur;
+  load(t, cur);
+
   float* srow = sparse + (w * S::R + r) * (S::L * S::Q);
   float cen[S::Q];  // centred counts
   float ca = 0.0f, cz = 0.0f;
+  int cnt[S::Q];
 #pragma unroll
   for (int q = 0; q < S::Q; ++q) {
+    const int e = S::elem(g, q);
+    srow[e] = 0.0f;
+    cnt[q] = losses && e < E ? a.counts[e] : 0;
     cen[q] = 0.0f;
-    srow[S::elem(g, q)] = 0.0f;
   }
   if (losses) {
-    // the sum of the counts, in integers
-    int s = 0;
-    for (int e = tid; e < E; e += kGradThreads) s += a.counts[e];
     const int n = *a.n_tokens;
+    const double da = a.dlosses[0], dz = a.dlosses[1];
+    int mine = 0;  // (all counts: below 2^31 slots)
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, kWave);
-    if (l == 0) wtot[w] = s;
-    __syncthreads();
-    long long total = 0;
+    for (int q = 0; q < S::Q; ++q) mine += cnt[q];
 #pragma unroll
-    for (int i = 0; i < kGradWaves; ++i) total += wtot[i];
+    for (int o = S::L / 2; o >= 1; o >>= 1) mine += __shfl_xor(mine, o, kWave);
 #pragma unroll
-    for (int q = 0; q < S::Q; ++q) {
-      const int e = S::elem(g, q);
-      if (e < E) cen[q] = (float)((double)((long long)a.counts[e] * E - total) / E);
-    }
+    for (int q = 0; q < S::Q; ++q)
+      if (S::elem(g, q) < E)
+        cen[q] = (float)((double)((long long)cnt[q] * E - mine) / E);
     if (n > 0) {
-      ca = (float)((double)a.dlosses[0] * E / ((double)n * n * k));
-      cz = (float)((double)a.dlosses[1] * 2.0 / n);
+      ca = (float)(da * E / ((double)n * n * k));
+      cz = (float)(dz * 2.0 / n);
     }
   }
   if (blockIdx.x == 0 && tid < kZeroLineBytes / 4)
@@ -455,29 +496,19 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
   float colsum[S::Q];
 #pragma unroll
   for (int q = 0; q < S::Q; ++q) colsum[q] = 0.0f;
-  const long long t0 = blockIdx.x * ka.rows_per_block;
-  const long long t1 = min(t0 + ka.rows_per_block, ka.T);
-  for (long long t = t0 + w * S::R + r; t < t1; t += kGradWaves * S::R) {
-    float v[S::Q];
-#pragma unroll
-    for (int q = 0; q < S::Q; ++q) v[q] = 0.0f;
-    if (!a.mask || a.mask[t] != 0) {
-      // every load of the row first
-      if (losses) load_row<S>(a.logits + t * E, E, g, v);
-      int id = -1;
-      float gw = 0.0f, dg = 0.0f;
-      if (a.dtopk_w && g < k) {
-        id = a.idx[t * k + g];
-        gw = a.topk_w[t * k + g];
-        dg = a.dtopk_w[t * k + g];
-      }
-      if (a.dtopk_w) {
-        float gmean = (unsigned)id < (unsigned)E ? gw * dg : 0.0f;
+  for (; t < t1; t += kGradWaves * S::R) {
+    Row x = cur;
+    load(t + kGradWaves * S::R, cur);
+    float (&v)[S::Q] = x.v;
+    if (x.live) {
+      if (gates) {
+        const bool ok = (unsigned)x.id < (unsigned)E;
+        float gmean = ok ? x.gw * x.dg : 0.0f;
         for (int j = g + S::L; j < k; j += S::L)
           if ((unsigned)a.idx[t * k + j] < (unsigned)E)
             gmean = fmaf(a.topk_w[t * k + j], a.dtopk_w[t * k + j], gmean);
         gmean = group_sum<S::L>(gmean);
-        if ((unsigned)id < (unsigned)E) unsafeAtomicAdd(&srow[id], gw * (dg - gmean));
+        if (ok) unsafeAtomicAdd(&srow[x.id], x.gw * (x.dg - gmean));
         for (int j = g + S::L; j < k; j += S::L) {
           const int e = a.idx[t * k + j];
           if ((unsigned)e < (unsigned)E)
@@ -495,26 +526,29 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
 #pragma unroll
         for (int q = 0; q < S::Q; ++q) v[q] = v[q] * inv * fmaf(ca, cen[q] - mean, zl);
       }
-      if (a.dtopk_w) {
+      if (gates) {
         asm volatile("" ::: "memory");
 #pragma unroll
         for (int c = 0; c < S::C; ++c) {
           if constexpr (S::V == 4) {
-            const f32x4_t x = *reinterpret_cast<const f32x4_t*>(srow + (c * S::L + g) * 4);
+            const f32x4_t y = *reinterpret_cast<const f32x4_t*>(srow + (c * S::L + g) * 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[c * 4 + i] += x[i];
+            for (int i = 0; i < 4; ++i) v[c * 4 + i] += y[i];
           } else {
             v[c] += srow[c * S::L + g];
           }
         }
         asm volatile("" ::: "memory");
-        if ((unsigned)id < (unsigned)E) srow[id] = 0.0f;
+        if ((unsigned)x.id < (unsigned)E) srow[x.id] = 0.0f;
         for (int j = g + S::L; j < k; j += S::L) {
           const int e = a.idx[t * k + j];
           if ((unsigned)e < (unsigned)E) srow[e] = 0.0f;
         }
         asm volatile("" ::: "memory");
       }
+    } else {
+#pragma unroll
+      for (int q = 0; q < S::Q; ++q) v[q] = 0.0f;
     }
 #pragma unroll
     for (int q = 0; q < S::Q; ++q) colsum[q] += v[q];
@@ -662,11 +696,8 @@ hipError_t gate_grad(const Shape& s, const GateGradArgs& a, int Ep, hipStream_t 
   ka.k = s.k;
   ka.Ep = Ep;
   ka.blocks = grad_blocks(s, &ka.rows_per_block);
-  ka.d = s.d;
   ka.act_bytes = act_bytes(s);
-  // 4096 values of the copy per workgroup, at most 256 of them
-  const long long pad = a.pad_src ? (long long)s.d * Ep : 0;
-  const int nb = ka.blocks + (int)std::min<long long>((pad + 4095) / 4096, 256);
+  const int nb = ka.blocks + (a.pad_src ? s.d / kGradWaves : 0);
   with_row_shape(s.E, [&](auto sh) {
     using S = decltype(sh);
     hipLaunchKernelGGL((gate_grad_rows<S>), dim3(nb), dim3(kGradThreads), 0, st, ka);

@@ -133,7 +133,8 @@ __global__ __launch_bounds__(kThreads) void grad_scale(Table t, const float* nor
   const bool clip = nv > max_norm && nv < INFINITY;
   const float scale = clip ? max_norm / nv : 1.0f;
   const int tid = threadIdx.x;
-  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+  // from the end: the norm's pass has left the last chunks in the cache
+  for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
     const int i = find_tensor(t, c);
     if (!clip && t.src[i] == t.dst[i]) continue;  // in place and nothing to change
     const long long b = (long long)(c - (i ? t.chunk_end[i - 1] : 0)) * kChunk;

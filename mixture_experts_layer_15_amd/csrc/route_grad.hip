@@ -353,7 +353,7 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void route
 // runs over the tokens, whose planes pass through LDS, 32 NB tokens a stage, in
 // two buffers.  The waves of a workgroup have neighbouring columns and share
 // the stage.  The matrix is the A operand, with its rows in an order that
-// leaves a lane 16 consecutive columns of one token.
+// suits the stores.
 // A staged row (one token, one plane) of P bytes: 16-byte chunk c of row t
 // sits at c ^ swz(t) within its aligned group of 16 chunks (8, 4 where P is
 // no multiple of 256, 128), so that 16 consecutive rows at one logical chunk
@@ -368,10 +368,16 @@ struct DxArgs {
   int steps_per_range;          // stages
 };
 
-// Column 16 h + q of a 32-column block is register q of lane half h of the
-// MFMA result, row 8 (q / 4) + 4 h + q % 4: the row r operand is column
-// dx_feat(r).
-__device__ __forceinline__ int dx_feat(int r) { return ((r >> 2) & 1) * 16 + (r >> 3) * 4 + (r & 3); }
+// The MFMA result has row 8 (q / 4) + 4 h + q % 4 in register q of lane half
+// h.  Row r of the operand is column dx_feat(r), so that each 16-byte store
+// of the two halves covers 32 consecutive bytes: float32 the columns as they
+// come, bf16 column 16 (q / 8) + 8 h + q % 8.
+template <bool kF32>
+__device__ __forceinline__ int dx_feat(int r) {
+  if constexpr (kF32) return r;
+  const int h = (r >> 2) & 1, q = (r >> 3) * 4 + (r & 3);
+  return 16 * (q >> 3) + 8 * h + (q & 7);
+}
 
 template <int KS>
 __device__ __forceinline__ int dx_swz(int t) {
@@ -422,12 +428,12 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
   };
   load_stage(0, 0);
 
-  // lane l: matrix row dx_feat(l % 32) of a block, the 16 bytes h of each
+  // lane l: matrix row dx_feat<kF32>(l % 32) of a block, the 16 bytes h of each
   // step's 32 (float32: the step's product i takes value i of both halves)
   u32x4_t wf[MB][KS];
 #pragma unroll
   for (int m = 0; m < MB; ++m) {
-    const int c = min(c0 + m * 32 + dx_feat(l % 32), a.d - 1);
+    const int c = min(c0 + m * 32 + dx_feat<kF32>(l % 32), a.d - 1);
     const unsigned char* row = a.w + (size_t)c * a.w_pitch * kSize + 16 * h;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -494,15 +500,15 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
         const f32x16_t& v = acc[m][n];
-        u32x4_t* o = reinterpret_cast<u32x4_t*>(a.dx + (t * a.d + c0 + m * 32 + 16 * h) * kSize);
+        u32x4_t* o = reinterpret_cast<u32x4_t*>(a.dx + (t * a.d + c0 + m * 32) * kSize + 16 * h);
         if (t < a.T && c0 + m * 32 < a.d) {
 #pragma unroll
           for (int i = 0; i < kSize; ++i) {
             if constexpr (kF32)
-              o[i] = u32x4_t{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+              o[2 * i] = u32x4_t{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
                              __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
             else
-              o[i] = u32x4_t{pack_bf16x2(v[8 * i], v[8 * i + 1]),
+              o[2 * i] = u32x4_t{pack_bf16x2(v[8 * i], v[8 * i + 1]),
                              pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
                              pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
                              pack_bf16x2(v[8 * i + 6], v[8 * i + 7])};
@@ -682,30 +688,40 @@ hipError_t launch_dx_as(DxArgs a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// The variant by the experts of a row: a wave's share of the matrix takes
-// 4 MB KS registers, a stage 32 NB x 32 KS bytes of LDS a plane.
+// The variant for KS steps: a wave's share of the matrix takes 4 MB KS
+// registers, a stage 32 NB x 32 KS bytes of LDS a plane.  Where the wide one
+// has workgroups for less than half of the compute units, one of 128 columns
+// and 32 tokens (one token of 4096 x 128, float32: 23.8 us wide).
+template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
+hipError_t launch_dx_for(const DxArgs& a, hipStream_t st) {
+  const long long groups = (long long)((a.d + MB * 32 * NW - 1) / (MB * 32 * NW)) *
+                           ((a.T + 32 * NB - 1) / (32 * NB));
+  if (groups < 128) return launch_dx_as<kF32, 1, KS, 1, 4, 1>(a, st);
+  return launch_dx_as<kF32, MB, KS, NB, NW, kMinWaves>(a, st);
+}
+
 hipError_t launch_dx(const DxArgs& a, int Ep, bool f32, hipStream_t st) {
   if (f32) switch (Ep) {
-      case 32: return launch_dx_as<true, 2, 4, 2, 4, 2>(a, st);
-      case 64: return launch_dx_as<true, 2, 8, 2, 4, 2>(a, st);
-      case 128: return launch_dx_as<true, 2, 16, 2, 8, 2>(a, st);
-      case 192: return launch_dx_as<true, 2, 24, 2, 4, 1>(a, st);
-      case 256: return launch_dx_as<true, 2, 32, 2, 4, 1>(a, st);
+      case 32: return launch_dx_for<true, 2, 4, 2, 4, 2>(a, st);
+      case 64: return launch_dx_for<true, 2, 8, 2, 4, 2>(a, st);
+      case 128: return launch_dx_for<true, 2, 16, 2, 8, 2>(a, st);
+      case 192: return launch_dx_for<true, 2, 24, 2, 4, 1>(a, st);
+      case 256: return launch_dx_for<true, 2, 32, 2, 4, 1>(a, st);
       case 320: return launch_dx_as<true, 1, 40, 1, 4, 1>(a, st);
       case 384: return launch_dx_as<true, 1, 48, 1, 4, 1>(a, st);
       case 448: return launch_dx_as<true, 1, 56, 1, 4, 1>(a, st);
       default: return launch_dx_as<true, 1, 64, 1, 4, 1>(a, st);
     }
   switch (Ep) {
-    case 32: return launch_dx_as<false, 2, 2, 2, 4, 2>(a, st);
-    case 64: return launch_dx_as<false, 2, 4, 2, 4, 2>(a, st);
-    case 128: return launch_dx_as<false, 2, 8, 2, 4, 2>(a, st);
-    case 192: return launch_dx_as<false, 2, 12, 2, 8, 2>(a, st);
-    case 256: return launch_dx_as<false, 2, 16, 2, 8, 2>(a, st);
-    case 320: return launch_dx_as<false, 2, 20, 1, 4, 1>(a, st);
-    case 384: return launch_dx_as<false, 2, 24, 1, 4, 1>(a, st);
-    case 448: return launch_dx_as<false, 2, 28, 1, 4, 1>(a, st);
-    default: return launch_dx_as<false, 2, 32, 1, 4, 1>(a, st);
+    case 32: return launch_dx_for<false, 2, 2, 2, 4, 2>(a, st);
+    case 64: return launch_dx_for<false, 2, 4, 2, 4, 2>(a, st);
+    case 128: return launch_dx_for<false, 2, 8, 2, 4, 2>(a, st);
+    case 192: return launch_dx_for<false, 2, 12, 2, 8, 2>(a, st);
+    case 256: return launch_dx_for<false, 2, 16, 2, 8, 2>(a, st);
+    case 320: return launch_dx_for<false, 2, 20, 1, 4, 1>(a, st);
+    case 384: return launch_dx_for<false, 2, 24, 1, 4, 1>(a, st);
+    case 448: return launch_dx_for<false, 2, 28, 1, 4, 1>(a, st);
+    default: return launch_dx_for<false, 2, 32, 1, 4, 1>(a, st);
   }
 }
 
@@ -762,14 +778,14 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
     a.splits = ns;
     hipError_t e;
     if (f32)
-      e = plan.be == 32   ? launch_dw<DwCfg<true, 1, 1, 4, 1, 2, 64, 3>>(a, st)
-          : plan.be == 64 ? launch_dw<DwCfg<true, 2, 1, 2, 2, 2, 64, 2>>(a, st)
+      e = plan.be == 32   ? launch_dw<DwCfg<true, 1, 1, 4, 1, 2, 32, 7>>(a, st)
+          : plan.be == 64 ? launch_dw<DwCfg<true, 2, 1, 2, 2, 2, 32, 5>>(a, st)
                           : launch_dw<DwCfg<true, 2, 2, 2, 2, 2, 32, 4>>(a, st);
     else if (plan.bc == 256)
       e = launch_dw<DwCfg<false, 4, 2, 2, 2, 2, 32, 3>>(a, st);
     else
-      e = plan.be == 32   ? launch_dw<DwCfg<false, 1, 1, 4, 1, 2, 64, 3>>(a, st)
-          : plan.be == 64 ? launch_dw<DwCfg<false, 2, 1, 2, 2, 2, 64, 2>>(a, st)
+      e = plan.be == 32   ? launch_dw<DwCfg<false, 1, 1, 4, 1, 2, 64, 5>>(a, st)
+          : plan.be == 64 ? launch_dw<DwCfg<false, 2, 1, 2, 2, 2, 32, 6>>(a, st)
                           : launch_dw<DwCfg<false, 2, 2, 2, 2, 2, 32, 4>>(a, st);
     if (e != hipSuccess) return e;
   }
