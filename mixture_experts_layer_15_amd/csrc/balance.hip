@@ -36,7 +36,7 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kMaxRowBlocks = 512;
 constexpr int kGradThreads = 256;  // of the gradient
 constexpr int kGradWaves = kGradThreads / kWave;
-constexpr int kMaxGradBlocks = 1024;
+constexpr int kMaxGradBlocks = 512;
 
 // A row of E logits on L lanes: lane g holds elements (c L + g) V + v,
 // c < C, v < V (V = 4: 16-byte loads, E a multiple of 4).

@@ -506,12 +506,12 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
           for (int i = 0; i < kSize; ++i) {
             if constexpr (kF32)
               o[2 * i] = u32x4_t{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                             __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
+                                 __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
             else
               o[2 * i] = u32x4_t{pack_bf16x2(v[8 * i], v[8 * i + 1]),
-                             pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                             pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
-                             pack_bf16x2(v[8 * i + 6], v[8 * i + 7])};
+                                 pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                 pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                                 pack_bf16x2(v[8 * i + 6], v[8 * i + 7])};
           }
         }
       }
@@ -580,12 +580,13 @@ struct DwPlan {
 
 // One workgroup fits a compute unit.  A part costs the rounds of workgroups
 // over the 256 compute units times (start and end of a workgroup, 4 us, plus
-// its tokens: 44 ns each on the 256 x 128 tile, 25 ns on 128 x 128, 14 ns on
-// the narrow ones, as measured), plus its partial sums, written and read at
-// 4 TB/s.  The tall tile has the better rate (1075 against 913 TFLOP/s of
-// matrix instructions on 16384 tokens of 7168 x 256: 168 against 198 us) but
-// needs that many more parts to fill the chip: on 8192 tokens of 2048 x 128 it
-// takes 22.0 us and 32 parts, the square one 18.8 us and 16.
+// its tokens at the measured time each), plus its partial sums, written and
+// read at 4 TB/s.  The tall tiles have the better rate on many tokens of wide
+// rows but need that many more parts to fill the chip.  Measured, 16384
+// tokens of 7168: E = 256, 256 x 128 tiles 168 us, 128 x 128 198 us; E = 64,
+// 256 x 64 59 us, 128 x 64 67 us; E = 8, 256 x 32 44 us, 128 x 32 48 us
+// (5.3 TB/s of x).  8192 tokens of 2048, E = 128: 256 x 128 22.0 us with 32
+// parts, 128 x 128 18.8 us with 16.
 double dw_cost(const Shape& s, int bc, int be, double ns_token, int splits) {
   const double tiles = (double)((s.d + bc - 1) / bc) * ((s.E + be - 1) / be);
   const double rounds = std::ceil(tiles * splits / 256.0);
@@ -608,9 +609,11 @@ DwPlan dw_plan(const Shape& s) {
   };
   const bool bf16 = s.act == kBF16;
   if (s.E <= 32) {
-    offer(128, 32, bf16 ? 14.0 : 22.0);
+    offer(128, 32, bf16 ? 12.0 : 22.0);
+    if (bf16) offer(256, 32, 22.0);
   } else if (s.E <= 64) {
-    offer(128, 64, bf16 ? 14.0 : 30.0);
+    offer(128, 64, bf16 ? 17.0 : 30.0);
+    if (bf16) offer(256, 64, 30.0);
   } else {
     offer(128, 128, bf16 ? 25.0 : 60.0);
     if (bf16) offer(256, 128, 44.0);
@@ -778,13 +781,15 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
     a.splits = ns;
     hipError_t e;
     if (f32)
-      e = plan.be == 32   ? launch_dw<DwCfg<true, 1, 1, 4, 1, 2, 32, 7>>(a, st)
+      e = plan.be == 32   ? launch_dw<DwCfg<true, 1, 1, 4, 1, 2, 64, 3>>(a, st)
           : plan.be == 64 ? launch_dw<DwCfg<true, 2, 1, 2, 2, 2, 32, 5>>(a, st)
                           : launch_dw<DwCfg<true, 2, 2, 2, 2, 2, 32, 4>>(a, st);
     else if (plan.bc == 256)
-      e = launch_dw<DwCfg<false, 4, 2, 2, 2, 2, 32, 3>>(a, st);
+      e = plan.be == 32   ? launch_dw<DwCfg<false, 2, 1, 4, 1, 2, 64, 3>>(a, st)
+          : plan.be == 64 ? launch_dw<DwCfg<false, 2, 2, 4, 1, 2, 32, 4>>(a, st)
+                          : launch_dw<DwCfg<false, 4, 2, 2, 2, 2, 32, 3>>(a, st);
     else
-      e = plan.be == 32   ? launch_dw<DwCfg<false, 1, 1, 4, 1, 2, 64, 5>>(a, st)
+      e = plan.be == 32   ? launch_dw<DwCfg<false, 1, 1, 4, 1, 2, 64, 3>>(a, st)
           : plan.be == 64 ? launch_dw<DwCfg<false, 2, 1, 2, 2, 2, 32, 6>>(a, st)
                           : launch_dw<DwCfg<false, 2, 2, 2, 2, 2, 32, 4>>(a, st);
     if (e != hipSuccess) return e;
