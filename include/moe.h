@@ -410,8 +410,9 @@ typedef struct {
  * (the counts are constants of the gradient, and the selection is piecewise
  * constant: neither has one).  Rows of masked tokens are 0 in dlogits and dx.
  * Slots with an id outside [0, E) are left out of every sum.  N <= 0 leaves
- * the losses' terms out.  Sums are float32; with bf16 activations dx is
- * formed from dL rounded to 16 significant bits, dw_router from all 24.
+ * the losses' terms out.  Sums are float32; with bf16 activations dx
+ * (which is rounded to 8 bits) is formed from dL rounded to 11 significant
+ * bits (and to 2^-39 of the row's largest), dw_router from all 24.
  * T = 0 writes zeros to dw_router and dbias.
  *  The outputs are distinct from the inputs (no gradient is formed in place).
  *  ws, ws_bytes: scratch of moe_workspace_size(p, MOE_CALL_ROUTE_BACKWARD). */

@@ -5,11 +5,16 @@
 //   dx[t][c]   = sum_e dL[t][e] W_r[c][e]
 //   db[e]      = sum_t dL[t][e]
 //
-// bf16 activations: dL (float32) is split into bfloat16 planes whose sum is
-// the value (gate_grad).  The router matrix' gradient is float32, so it takes
-// all three planes: the products with the bfloat16 tokens are exact and only
-// the float32 sums round.  The tokens' gradient is rounded to bfloat16 at the
-// end, so two planes (16 bits, 2^-17 off) do for it.
+// bf16 activations: for the router matrix' gradient, which is float32, dL
+// (float32) is split into three bfloat16 planes whose sum is the value
+// (gate_grad): the products with the bfloat16 tokens are exact and only the
+// float32 sums round.  The tokens' gradient is rounded to bfloat16 at the end,
+// so dL goes into it with the 11 bits of a float16 (2^-11 off, an eighth of a
+// bfloat16's 2^-8): each token's row times the power of two that brings its
+// largest value to 2^14, and each row of the router matrix, exactly converted,
+// likewise; the result is scaled back (two bfloat16 planes took twice the
+// matrix instructions: 122 us against FP16_DX_US us on 16384 tokens of
+// 7168 x 256).
 // float32 activations: the same kernels on the float32 matrix instructions,
 // with dL as it is.
 #include <algorithm>
@@ -350,7 +355,7 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void route
 // keeps its columns' share of the router matrix in registers as MFMA operands
 // (MB blocks of 32 columns, KS steps of 16 experts, in float32 of 8: 4 MB KS
 // registers) and
-// runs over the tokens, whose planes pass through LDS, 32 NB tokens a stage, in
+// runs over the tokens, whose rows of dL pass through LDS, 32 NB tokens a stage, in
 // two buffers.  The waves of a workgroup have neighbouring columns and share
 // the stage.  The matrix is the A operand, with its rows in an order that
 // suits the stores.
@@ -359,7 +364,8 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void route
 // no multiple of 256, 128), so that 16 consecutive rows at one logical chunk
 // lie in different banks.
 struct DxArgs {
-  const unsigned char* planes;  // bf16: [2 of 3][T][Ep]; float32: [T][Ep]
+  const unsigned char* rows;    // [T][Ep] dL: float16 scaled by 2^exponent, or float32
+  const int* exponents;         // [T] (bf16)
   const unsigned char* w;       // [d][w_pitch], experts behind E not read
   unsigned char* dx;            // [T][d]
   long long T;
@@ -379,6 +385,8 @@ __device__ __forceinline__ int dx_feat(int r) {
   return 16 * (q >> 3) + 8 * h + (q & 7);
 }
 
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
 template <int KS>
 __device__ __forceinline__ int dx_swz(int t) {
   constexpr int P = KS * 32;
@@ -388,18 +396,17 @@ __device__ __forceinline__ int dx_swz(int t) {
 template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
 __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
   constexpr int kSize = kF32 ? 4 : 2;        // bytes of a value
-  constexpr int kPlanes = kF32 ? 1 : 2;
   constexpr int kTokens = 32 * NB;
   constexpr int P = KS * 32;                 // bytes of a staged row
-  constexpr int kPlane = kTokens * P;
-  constexpr int kStage = kPlanes * kPlane;
-  constexpr int kPerWave = kStage / 1024 / NW;
-  static_assert(kStage % (1024 * NW) == 0, "whole loads per wave");
+  constexpr int kStage = kTokens * P;
+  constexpr int kInstr = kStage / 1024;      // 1 KB loads of a stage
+  constexpr int kPerWave = (kInstr + NW - 1) / NW;
+  static_assert(kStage % 1024 == 0, "whole loads");
   constexpr int kStores = MB * NB * kSize;   // 16-byte stores of a lane per stage
   extern __shared__ __align__(1024) unsigned char smem[];
   const int item = xcd_item(a.c_groups * a.t_ranges);
   if (item < 0) return;  // the whole workgroup
-  // the column groups of a token range run on one XCD (they share the planes)
+  // the column groups of a token range run on one XCD (they share its rows)
   const int cg = item % a.c_groups;
   const int range = item / a.c_groups;
   const int tid = threadIdx.x;
@@ -418,12 +425,12 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
 #pragma unroll
     for (int i = 0; i < kPerWave; ++i) {
       const int n = w * kPerWave + i;
+      if (kInstr % NW != 0 && n >= kInstr) break;
       const int q = n * 64 + l;               // 16-byte chunk of the stage
-      const int row = q / (P / 16), pc = q % (P / 16);
-      const int pl = row / kTokens, r = row % kTokens;
+      const int r = q / (P / 16), pc = q % (P / 16);
       const int c = pc ^ dx_swz<KS>(r);
       const long long t = min((s0 + s) * kTokens + r, a.T - 1);
-      dma16(a.planes + (pl * a.T + t) * P + c * 16, lds0 + b * kStage + n * 1024);
+      dma16(a.rows + t * P + c * 16, lds0 + b * kStage + n * 1024);
     }
   };
   load_stage(0, 0);
@@ -442,6 +449,30 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
         wf[m][ks] = *reinterpret_cast<const u32x4_t*>(row + 32 * ks);
     }
   }
+  // float16: the rows scaled so that their largest value is at 2^14
+  int* wexp = reinterpret_cast<int*>(smem + 2 * kStage) + w * MB * 32;
+  if constexpr (!kF32) {
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      uint32_t big = 0;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          big = max(big, max(wf[m][ks][q] & 0x7fff, (wf[m][ks][q] >> 16) & 0x7fff));
+      big = max(big, (uint32_t)__shfl_xor((int)big, 32, kWave));  // the row's other half
+      const int up = scale_exponent(big << 16);
+      if (h == 0) wexp[m * 32 + dx_feat<kF32>(l % 32)] = up;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t v = wf[m][ks][q];
+          wf[m][ks][q] = scaled_half(__uint_as_float(v << 16), up) |
+                         (uint32_t)scaled_half(__uint_as_float(v & 0xffff0000u), up) << 16;
+        }
+    }
+  }
   // operand read: lane l has token l % 32 of a block, chunk 2 ks + h
   constexpr int kGroup = P % 256 == 0 ? 8 : P % 128 == 0 ? 4 : 2;  // steps of a swizzle group
   uint32_t base[NB];
@@ -458,6 +489,10 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
     if (s == 0 || !all_cols) wait_vm<0>();
     else wait_vm<kStores>();
     lds_barrier();            // ... of every wave, and nobody reads the other buffer any more
+    int texp[NB];  // (read at the end: the next stage's loads are behind it)
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+      texp[n] = kF32 ? 0 : a.exponents[min((s0 + s) * kTokens + n * 32 + l % 32, a.T - 1)];
     if (s + 1 < ns) load_stage(s + 1, b ^ 1);
     f32x16_t acc[MB][NB];
 #pragma unroll
@@ -466,41 +501,47 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
       for (int n = 0; n < NB; ++n) acc[m][n] = f32x16_t{};
     const unsigned char* st = smem + b * kStage;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
+    for (int ks = 0; ks < KS; ++ks) {
+      u32x4_t pb[NB];
 #pragma unroll
-      for (int pl = 0; pl < kPlanes; ++pl) {
-        u32x4_t pb[NB];
+      for (int n = 0; n < NB; ++n)
+        pb[n] = *reinterpret_cast<const u32x4_t*>(st + (base[n] ^ ((ks % kGroup) << 5)) +
+                                                  ks / kGroup * kGroup * 32);
+      if constexpr (kF32) {
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
-          pb[n] = *reinterpret_cast<const u32x4_t*>(
-              st + pl * kPlane + (base[n] ^ ((ks % kGroup) << 5)) + ks / kGroup * kGroup * 32);
-        if constexpr (kF32) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-              for (int m = 0; m < MB; ++m)
-                acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                    __uint_as_float(wf[m][ks][i]), __uint_as_float(pb[n][i]), acc[m][n], 0, 0, 0);
-        } else {
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int m = 0; m < MB; ++m)
-              acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                  __builtin_bit_cast(bf16x8_t, wf[m][ks]), __builtin_bit_cast(bf16x8_t, pb[n]),
-                  acc[m][n], 0, 0, 0);
-        }
+              acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                  __uint_as_float(wf[m][ks][i]), __uint_as_float(pb[n][i]), acc[m][n], 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int m = 0; m < MB; ++m)
+            acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                __builtin_bit_cast(f16x8_t, wf[m][ks]), __builtin_bit_cast(f16x8_t, pb[n]),
+                acc[m][n], 0, 0, 0);
       }
+    }
     __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads of the stage have returned
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const long long t = (s0 + s) * kTokens + n * 32 + l % 32;
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
-        const f32x16_t& v = acc[m][n];
+        f32x16_t v = acc[m][n];
         u32x4_t* o = reinterpret_cast<u32x4_t*>(a.dx + (t * a.d + c0 + m * 32) * kSize + 16 * h);
+        if constexpr (!kF32) {
+          // register 8 i + q is column 16 i + 8 h + q
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              v[8 * i + q] = ldexpf(v[8 * i + q], -(wexp[m * 32 + 16 * i + 8 * h + q] + texp[n]));
+        }
         if (t < a.T && c0 + m * 32 < a.d) {
 #pragma unroll
           for (int i = 0; i < kSize; ++i) {
@@ -622,7 +663,7 @@ DwPlan dw_plan(const Shape& s) {
 }
 
 struct GradLayout {
-  size_t zero, planes, wpad, bias, dw, total;
+  size_t zero, planes, half, exps, wpad, bias, dw, total;
 };
 
 GradLayout grad_layout(const Shape& s) {
@@ -637,6 +678,8 @@ GradLayout grad_layout(const Shape& s) {
   L.zero = take(kZeroLineBytes);
   if (s.act == kBF16) {
     L.planes = take((size_t)3 * s.T * Ep * 2);
+    L.half = take((size_t)s.T * Ep * 2);
+    L.exps = take((size_t)s.T * 4);
     L.wpad = take(s.E % 8 != 0 ? (size_t)s.d * Ep * 2 : 0);
   } else {
     L.planes = take((size_t)s.T * Ep * 4);
@@ -674,7 +717,7 @@ template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
 hipError_t launch_dx_as(DxArgs a, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
   constexpr int kTokens = 32 * NB;
-  constexpr int kLds = 2 * (kF32 ? 1 : 2) * kTokens * KS * 32;
+  constexpr int kLds = 2 * kTokens * KS * 32 + (kF32 ? 0 : NW * MB * 32 * 4);
   static_assert(kLds <= 160 * 1024, "LDS budget");
   const void* kern = reinterpret_cast<const void*>(&router_dx<kF32, MB, KS, NB, NW, kMinWaves>);
   const hipError_t e = set_lds_attr(kern, kLds, done);
@@ -692,7 +735,7 @@ hipError_t launch_dx_as(DxArgs a, hipStream_t st) {
 }
 
 // The variant for KS steps: a wave's share of the matrix takes 4 MB KS
-// registers, a stage 32 NB x 32 KS bytes of LDS a plane.  Where the wide one
+// registers, a stage 32 NB x 32 KS bytes of LDS.  Where the wide one
 // has workgroups for less than half of the compute units, one of 128 columns
 // and 32 tokens (one token of 4096 x 128, float32: 23.8 us wide).
 template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
@@ -721,10 +764,10 @@ hipError_t launch_dx(const DxArgs& a, int Ep, bool f32, hipStream_t st) {
     case 128: return launch_dx_for<false, 2, 8, 2, 4, 2>(a, st);
     case 192: return launch_dx_for<false, 2, 12, 2, 8, 2>(a, st);
     case 256: return launch_dx_for<false, 2, 16, 2, 8, 2>(a, st);
-    case 320: return launch_dx_for<false, 2, 20, 1, 4, 1>(a, st);
-    case 384: return launch_dx_for<false, 2, 24, 1, 4, 1>(a, st);
-    case 448: return launch_dx_for<false, 2, 28, 1, 4, 1>(a, st);
-    default: return launch_dx_for<false, 2, 32, 1, 4, 1>(a, st);
+    case 320: return launch_dx_for<false, 2, 20, 2, 4, 1>(a, st);
+    case 384: return launch_dx_for<false, 2, 24, 2, 4, 1>(a, st);
+    case 448: return launch_dx_for<false, 2, 28, 2, 4, 1>(a, st);
+    default: return launch_dx_for<false, 2, 32, 2, 4, 1>(a, st);
   }
 }
 
@@ -740,10 +783,12 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
   const int ns = plan.splits;
   const bool f32 = s.act != kBF16;
   const bool products = s.T > 0 && (g.dw || g.dx);
-  float* bias_part = reinterpret_cast<float*>(base + lay.bias);
+  // one row block's column sums are the bias' gradient
+  const bool sum_b = g.dbias && (s.T == 0 || gate_grad_blocks(s) > 1);
+  float* bias_part = sum_b ? reinterpret_cast<float*>(base + lay.bias) : g.dbias;
   float* part = ns > 1 ? reinterpret_cast<float*>(base + lay.dw) : g.dw;
-  // what the products read: the planes, or float32 rows of Ep values (the
-  // caller's, if they are as long)
+  // what the products read, bf16: the planes and the float16 rows; float32:
+  // rows of Ep values (the caller's, if they are as long)
   unsigned char* planes = base + lay.planes;
   if (f32 && g.dlogits && Ep == s.E) planes = reinterpret_cast<unsigned char*>(g.dlogits);
 
@@ -752,12 +797,13 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
     ga.dlogits = g.dlogits;
     if (products && f32 && planes != reinterpret_cast<unsigned char*>(g.dlogits))
       ga.dl_rows = reinterpret_cast<float*>(planes);
-    if (products && !f32) {
-      ga.planes = reinterpret_cast<uint16_t*>(planes);
-      ga.nplanes = g.dw ? 3 : 2;
+    if (!f32 && g.dw) ga.planes = reinterpret_cast<uint16_t*>(planes);
+    if (!f32 && g.dx) {
+      ga.half = reinterpret_cast<uint16_t*>(base + lay.half);
+      ga.exponents = reinterpret_cast<int*>(base + lay.exps);
     }
     ga.zero_line = base + lay.zero;
-    ga.bias_part = g.dbias ? bias_part : nullptr;
+    ga.bias_part = bias_part;
     // rows of the matrix that 16-byte loads cannot take are copied with Ep
     // values each, by workgroups of the same launch
     if (g.dx && s.E % (f32 ? 4 : 8) != 0) {
@@ -795,7 +841,7 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
     if (e != hipSuccess) return e;
   }
   const bool sum_w = g.dw && (ns > 1 || s.T == 0);
-  if (sum_w || g.dbias) {
+  if (sum_w || sum_b) {
     SumArgs a{};
     a.part = part;
     a.dw = g.dw;
@@ -807,13 +853,14 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
     a.nb = s.T == 0 ? 0 : gate_grad_blocks(s);
     a.E = s.E;
     hipLaunchKernelGGL(router_grad_sum,
-                       dim3(a.w_blocks + (g.dbias ? (s.E + kSumCols - 1) / kSumCols : 0)),
+                       dim3(a.w_blocks + (sum_b ? (s.E + kSumCols - 1) / kSumCols : 0)),
                        dim3(kSumThreads), 0, st, a);
   }
   if (g.dx && s.T > 0) {
     const bool padded = s.E % (f32 ? 4 : 8) != 0;
     DxArgs a{};
-    a.planes = planes;
+    a.rows = f32 ? planes : base + lay.half;
+    a.exponents = reinterpret_cast<const int*>(base + lay.exps);
     a.w = padded ? base + lay.wpad : static_cast<const unsigned char*>(g.w_router);
     a.w_pitch = padded ? Ep : s.E;
     a.E = a.w_pitch;

@@ -310,8 +310,14 @@ class Router:
             ref = dl @ w.t()
             mag = dl.abs() @ w.abs().t()
             bf = self.act == "bf16"
-            planes = 2.0 ** -17 if bf else 0.0
-            tol = b @ w.abs().t() + (planes + (2 * E + 8) * U) * mag + (BF16 * ref.abs() if bf else 0.0)
+            tol = b @ w.abs().t() + (2 * E + 8) * U * mag + (BF16 * ref.abs() if bf else 0.0)
+            if bf:
+                # dL in a float16 of 11 bits (half a step, eps / 2, is 2^-11 relative), each row scaled to a largest value
+                # of at least 2^14: below the normal numbers half a step of 2^-24, 2^-39 of the largest; the
+                # rows of the matrix (8 bits, exact) likewise
+                tol += 2.0 ** -11 * mag
+                tol += 2.0 ** -39 * dl.abs().amax(dim=1, keepdim=True) * w.abs().sum(dim=1)
+                tol += 2.0 ** -39 * dl.abs().sum(dim=1, keepdim=True) * w.abs().amax(dim=1)
             assert torch.all((got["dx"].double() - ref).abs() <= tol * (1 + BF16) + 1e-37)
             assert torch.all(got["dx"][~keep] == 0)
 
