@@ -91,6 +91,22 @@ __device__ __forceinline__ u32x2_t read_tr(uint32_t lds) {
 #endif
 }
 
+// 4 bytes per lane, global -> LDS: lane i's land at lds + 4 i.
+__device__ __forceinline__ void dma4(const void* src, uint32_t lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile(
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %0, off"
+      :
+      : "v"(src), "s"(lds)
+      : "memory", "m0");
+#else
+  (void)src;
+  (void)lds;
+#endif
+}
+
 // ---- dW_r, bf16
 // Tile: BC columns of x by BE experts, the sum over a range of tokens.  Both
 // operands have the summed index (the token) as their slow dimension, so they
@@ -432,6 +448,11 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
       const long long t = min((s0 + s) * kTokens + r, a.T - 1);
       dma16(a.rows + t * P + c * 16, lds0 + b * kStage + n * 1024);
     }
+    // the tokens' exponents go the same way: a load into registers would be
+    // waited for with every store before it
+    if (!kF32 && w == 0 && l < kTokens)
+      dma4(a.exponents + min((s0 + s) * kTokens + l, a.T - 1),
+           lds0 + 2 * kStage + b * kTokens * 4);
   };
   load_stage(0, 0);
 
@@ -450,7 +471,7 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
     }
   }
   // float16: the rows scaled so that their largest value is at 2^14
-  int* wexp = reinterpret_cast<int*>(smem + 2 * kStage) + w * MB * 32;
+  int* wexp = reinterpret_cast<int*>(smem + 2 * kStage) + 2 * kTokens + w * MB * 32;
   if constexpr (!kF32) {
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
@@ -489,10 +510,6 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
     if (s == 0 || !all_cols) wait_vm<0>();
     else wait_vm<kStores>();
     lds_barrier();            // ... of every wave, and nobody reads the other buffer any more
-    int texp[NB];  // (read at the end: the next stage's loads are behind it)
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-      texp[n] = kF32 ? 0 : a.exponents[min((s0 + s) * kTokens + n * 32 + l % 32, a.T - 1)];
     if (s + 1 < ns) load_stage(s + 1, b ^ 1);
     f32x16_t acc[MB][NB];
 #pragma unroll
@@ -526,6 +543,10 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
                 acc[m][n], 0, 0, 0);
       }
     }
+    int texp[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+      texp[n] = kF32 ? 0 : reinterpret_cast<const int*>(smem + 2 * kStage)[b * kTokens + n * 32 + l % 32];
     __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads of the stage have returned
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
@@ -717,7 +738,7 @@ template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
 hipError_t launch_dx_as(DxArgs a, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
   constexpr int kTokens = 32 * NB;
-  constexpr int kLds = 2 * kTokens * KS * 32 + (kF32 ? 0 : NW * MB * 32 * 4);
+  constexpr int kLds = 2 * kTokens * KS * 32 + (kF32 ? 0 : (2 * kTokens + NW * MB * 32) * 4);
   static_assert(kLds <= 160 * 1024, "LDS budget");
   const void* kern = reinterpret_cast<const void*>(&router_dx<kF32, MB, KS, NB, NW, kMinWaves>);
   const hipError_t e = set_lds_attr(kern, kLds, done);
