@@ -382,7 +382,8 @@ moe_status_t moe_balance_loss(const moe_problem_t* p, const float* logits, const
                               void* stream);
 
 /* Arguments of moe_route_backward.  At least one of dtopk_w and dlosses, and
- * at least one output, is given; each input is read only where noted. */
+ * at least one output, is given (T = 0: arrays of no tokens may be NULL);
+ * each input is read only where noted. */
 typedef struct {
   const void* x;             /* [T][d] act: with dw_router */
   const void* w_router;      /* [d][E] act: with dx */
@@ -413,6 +414,8 @@ typedef struct {
  * the losses' terms out.  Sums are float32; with bf16 activations dx
  * (which is rounded to 8 bits) is formed from dL rounded to 11 significant
  * bits (and to 2^-39 of the row's largest), dw_router from all 24.
+ * Where an infinity or NaN enters a sum, the sum is not finite (an infinity
+ * may come out as NaN).
  * T = 0 writes zeros to dw_router and dbias.
  *  The outputs are distinct from the inputs (no gradient is formed in place).
  *  ws, ws_bytes: scratch of moe_workspace_size(p, MOE_CALL_ROUTE_BACKWARD). */

@@ -385,7 +385,7 @@ class GradList:
         if out is not grads:
             if (list(map(_GRAD_CODE.get, [o.dtype for o in out])) != codes
                     or list(map(T.numel, out)) != sizes or not all(map(T.is_contiguous, out))
-                    or any(d != self.device for d in map(T.get_device, out))):
+                    or not set(map(T.get_device, out)) <= {self.device}):
                 _refuse(c, "an output has another type, size, layout or device than its gradient")
             to = list(map(T.data_ptr, out))
         flat = itertools.chain.from_iterable(zip(at, to, sizes, codes))

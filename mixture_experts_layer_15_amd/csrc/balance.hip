@@ -204,13 +204,14 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
   // a row's logits are loaded one row ahead, the first before the counting
   // (masked rows too: what they hold is dropped)
   float cur[S::Q];
-  bool keep = false;
+  int keep = 0;
   auto load = [&](int t) {
-    keep = t < rows && (!mask || mask[t] != 0);
-    if (t < rows) load_row<S>(logits + (long long)t * a.E, a.E, g, cur);
+    t = min(t, rows - 1);
+    load_row<S>(logits + (long long)t * a.E, a.E, g, cur);
+    keep = mask ? mask[t] : 1;
   };
   int t = w * S::R + r;
-  load(t);
+  if (rows > 0) load(t);  // (0: the only workgroup, of no tokens)
   for (int e = tid; e < a.E; e += kThreads) hist[e] = 0;
   if (!kSolo && blockIdx.x == 0 && tid == 0) *a.joined = 0;
   __syncthreads();
@@ -230,7 +231,7 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
     float v[S::Q], inv;
 #pragma unroll
     for (int q = 0; q < S::Q; ++q) v[q] = cur[q];
-    const bool live = keep;  // the same for the group's lanes
+    const int live = keep;  // the same for the group's lanes
     load(t + kWaves * S::R);
     if (!live) continue;
     const float lse = row_exp<S>(v, inv);
@@ -444,28 +445,31 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
     float v[S::Q];
     int id;
     float gw, dg;
-    bool live;
+    int keep;
   };
+  // (no value is looked at here, so that the loads are all in flight at once;
+  // behind the last row it is read again)
   auto load = [&](long long t, Row& x) {
-    x.live = t < t1 && (!a.mask || a.mask[t] != 0);
+    t = min(t, t1 - 1);
     x.id = -1;
     x.gw = x.dg = 0.0f;
+    x.keep = 1;
 #pragma unroll
     for (int q = 0; q < S::Q; ++q) x.v[q] = 0.0f;
-    if (t >= t1) return;
     if (losses) load_row<S>(a.logits + t * E, E, g, x.v);
     if (gates && g < k) {
       x.id = a.idx[t * k + g];
       x.gw = a.topk_w[t * k + g];
       x.dg = a.dtopk_w[t * k + g];
     }
+    if (a.mask) x.keep = a.mask[t];
   };
   long long t = t0 + w * S::R + r;
   Row cur;
   load(t, cur);
 
   float* srow = sparse + (w * S::R + r) * (S::L * S::Q);
-  float cen[S::Q];  // centred counts
+  float cen[S::Q];  // centred counts, times E
   float ca = 0.0f, cz = 0.0f;
   int cnt[S::Q];
 #pragma unroll
@@ -478,17 +482,18 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
   if (losses) {
     const int n = *a.n_tokens;
     const double da = a.dlosses[0], dz = a.dlosses[1];
-    int mine = 0;  // (all counts: below 2^31 slots)
+    // integers in float64 (exact): the counts of many ranks' tokens may pass
+    // 2^31 in sum
+    double mine = 0.0;
 #pragma unroll
     for (int q = 0; q < S::Q; ++q) mine += cnt[q];
 #pragma unroll
     for (int o = S::L / 2; o >= 1; o >>= 1) mine += __shfl_xor(mine, o, kWave);
 #pragma unroll
     for (int q = 0; q < S::Q; ++q)
-      if (S::elem(g, q) < E)
-        cen[q] = (float)((double)((long long)cnt[q] * E - mine) / E);
+      if (S::elem(g, q) < E) cen[q] = (float)((double)cnt[q] * E - mine);  // (an integer below 2^40)
     if (n > 0) {
-      ca = (float)(da * E / ((double)n * n * k));
+      ca = (float)(da / ((double)n * n * k));
       cz = (float)(dz * 2.0 / n);
     }
   }
@@ -501,7 +506,7 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
     Row x = cur;
     load(t + kGradWaves * S::R, cur);
     float (&v)[S::Q] = x.v;
-    if (x.live) {
+    if (x.keep) {
       if (gates) {
         const bool ok = (unsigned)x.id < (unsigned)E;
         float gmean = ok ? x.gw * x.dg : 0.0f;

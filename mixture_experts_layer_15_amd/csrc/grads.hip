@@ -214,35 +214,45 @@ int blocks_of(const Table& t) { return std::min(t.chunks, kMaxBlocks); }
 
 }  // namespace
 
-size_t grad_ws_bytes(const moe_grad_t* g, int n) {
-  // as for_tables cuts the list, without the table
-  long long blocks = 0, chunks = 0;
+// Launches and workgroups of a list, as for_tables cuts it.
+struct Totals {
+  int launches = 0;
+  long long blocks = 0;
+};
+
+static Totals totals_of(const moe_grad_t* g, int n) {
+  Totals r;
+  long long chunks = 0;
   int in = 0;
+  auto close = [&] {
+    if (in == 0) return;
+    ++r.launches;
+    r.blocks += std::min<long long>(chunks, kMaxBlocks);
+  };
   for (int i = 0; i < n; ++i) {
     if (g[i].numel == 0) continue;
     const long long c = chunks_of(g[i]);
     if (in == kTable || chunks + c > (1LL << 30)) {
-      blocks += std::min<long long>(chunks, kMaxBlocks);
+      close();
       in = 0;
       chunks = 0;
     }
     ++in;
     chunks += c;
   }
-  blocks += std::min<long long>(chunks, kMaxBlocks);
-  return align_up((size_t)std::max<long long>(blocks, 1) * sizeof(double));
+  close();
+  return r;
+}
+
+size_t grad_ws_bytes(const moe_grad_t* g, int n) {
+  return align_up((size_t)std::max<long long>(totals_of(g, n).blocks, 1) * sizeof(double));
 }
 
 hipError_t grad_norm(const moe_grad_t* g, int n, float* norm, void* ws, hipStream_t st) {
   double* part = static_cast<double*>(ws);
   int used = 0;
-  bool solo = false;
-  int tables = 0, total_chunks = 0;
-  for_tables(g, n, [&](const Table& t) {
-    ++tables;
-    total_chunks += t.chunks;
-  });
-  solo = tables == 1 && total_chunks == 1;
+  const Totals total = totals_of(g, n);
+  const bool solo = total.launches == 1 && total.blocks == 1;
   for_tables(g, n, [&](const Table& t) {
     const int nb = blocks_of(t);
     hipLaunchKernelGGL(grad_squares, dim3(nb), dim3(kThreads), 0, st, t, part + used,

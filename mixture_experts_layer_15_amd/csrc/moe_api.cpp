@@ -321,8 +321,10 @@ moe_status_t moe_route_backward(const moe_problem_t* p, const moe_route_backward
   moe_status_t st = check_problem(p, &s);
   if (st != MOE_OK) return st;
   if (a == nullptr) return MOE_ERR_INVALID_ARGUMENT;
-  if (a->dtopk_w == nullptr && a->dlosses == nullptr) return MOE_ERR_INVALID_ARGUMENT;
-  if (a->dlogits == nullptr && a->dx == nullptr && a->dw_router == nullptr && a->dbias == nullptr)
+  // (arrays of no tokens may be null)
+  if (s.T > 0 && a->dtopk_w == nullptr && a->dlosses == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (s.T > 0 && a->dlogits == nullptr && a->dx == nullptr && a->dw_router == nullptr &&
+      a->dbias == nullptr)
     return MOE_ERR_INVALID_ARGUMENT;
   if (a->dlogits != nullptr && a->dlogits == a->logits) return MOE_ERR_INVALID_ARGUMENT;
   if (a->dx != nullptr && a->dx == a->x) return MOE_ERR_INVALID_ARGUMENT;
@@ -365,12 +367,12 @@ moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dout, cons
   Shape s;
   moe_status_t st = check_problem(p, &s);
   if (st != MOE_OK) return st;
+  if (s.T == 0) return MOE_OK;
   if (dout == nullptr || slot_pos == nullptr) return MOE_ERR_INVALID_ARGUMENT;
   if (dy == nullptr && dtopk_w == nullptr) return MOE_ERR_INVALID_ARGUMENT;
   if (dtopk_w != nullptr && y == nullptr) return MOE_ERR_INVALID_ARGUMENT;
   if (dy != nullptr && (dy == y || dy == dout)) return MOE_ERR_INVALID_ARGUMENT;
   if (!all_aligned16(dout, y, slot_pos, topk_w, dy, dtopk_w)) return MOE_ERR_INVALID_ARGUMENT;
-  if (s.T == 0) return MOE_OK;
   return from_hip(moe::combine_backward(s, dout, y, slot_pos, topk_w, dy, dtopk_w,
                                         static_cast<hipStream_t>(stream)));
 }

@@ -63,13 +63,16 @@ __device__ __forceinline__ uint32_t lds_addr(const unsigned char* p) {
 // waits by wait_vm and a barrier before it reads what arrives.
 __device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
+  uint32_t m0;  // (the instruction takes its LDS address from M0, which is put back)
   asm volatile(
-      "s_mov_b32 m0, %1\n\t"
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
       "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %0, off"
-      :
+      "global_load_lds_dwordx4 %1, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(m0)
       : "v"(src), "s"(lds)
-      : "memory", "m0");
+      : "memory");
 #else
   (void)src;
   (void)lds;
@@ -94,13 +97,16 @@ __device__ __forceinline__ u32x2_t read_tr(uint32_t lds) {
 // 4 bytes per lane, global -> LDS: lane i's land at lds + 4 i.
 __device__ __forceinline__ void dma4(const void* src, uint32_t lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
+  uint32_t m0;  // (the instruction takes its LDS address from M0, which is put back)
   asm volatile(
-      "s_mov_b32 m0, %1\n\t"
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
       "s_nop 0\n\t"
-      "global_load_lds_dword %0, off"
-      :
+      "global_load_lds_dword %1, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(m0)
       : "v"(src), "s"(lds)
-      : "memory", "m0");
+      : "memory");
 #else
   (void)src;
   (void)lds;
@@ -661,7 +667,9 @@ DwPlan dw_plan(const Shape& s) {
   DwPlan best{128, 32, 1};
   double cost = -1.0;
   auto offer = [&](int bc, int be, double ns_token) {
-    for (int n = 1; n <= 64 && (n == 1 || (long long)n * 64 <= s.T + 63); ++n) {
+    // (the plan is made several times a call: few candidates)
+    for (const int n : {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 18, 20, 24, 28, 32, 40, 48, 64}) {
+      if (n > 1 && (long long)n * 64 > s.T + 63) break;
       const double c = dw_cost(s, bc, be, ns_token, n);
       if (cost < 0 || c < cost) {
         cost = c;

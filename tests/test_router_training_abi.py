@@ -107,6 +107,7 @@ def test_combine_backward_refusals(lib):
         assert call(**{name: 5 * FAKE + 8}) == B.MOE_ERR_INVALID_ARGUMENT
     assert call(p=_p(T=-1)) == B.MOE_ERR_INVALID_ARGUMENT
     assert call(p=_p(T=0)) == B.MOE_OK                            # nothing to do, nothing enqueued
+    assert call(dout=None, y=None, pos=None, w=None, dy=None, dw=None, p=_p(T=0)) == B.MOE_OK
 
 
 def _grads(*rows):

@@ -426,6 +426,32 @@ def test_route_backward_zero_tokens(act):
     assert torch.all(dw == 0) and torch.all(db == 0)
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_zero_tokens_through_empty_tensors(act):
+    """A rank without tokens: empty tensors (null addresses), gradients of zeros."""
+    E, d, k = 12, 256, 2
+    p = B.problem(0, d, E, k, 128, 0, E, act, act)
+    e = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device=DEV)  # noqa: E731
+    dw, db = torch.full((d, E), 3.0, device=DEV), torch.full((E,), 3.0, device=DEV)
+    ws = B.workspace(p, B.MOE_CALL_ROUTE_BACKWARD, DEV)
+    ids, a = e(0, k, t=torch.int32), ACT[act]
+    B.moe_route_backward(p, x=e(0, d, t=a), topk_idx=ids, topk_w=e(0, k), dtopk_w=e(0, k), dw_router=dw, dbias=db, ws=ws)
+    B.moe_route_backward(p, topk_idx=ids, topk_w=e(0, k), dtopk_w=e(0, k), dlogits=e(0, E), ws=ws)
+    B.moe_combine_backward(p, e(0, d, t=a), e(0, d, t=a), ids, e(0, k), e(0, d, t=a), e(0, k))
+    torch.cuda.synchronize()
+    assert torch.all(dw == 0) and torch.all(db == 0)
+
+
+def test_route_backward_counts_of_many_ranks():
+    """Counts and tokens of a batch on many ranks: their sum passes 2^31."""
+    r = Router(300, 128, 20, 4, "bf16", "random", gates=False)
+    r.counts = torch.randint(1 << 29, (1 << 31) - 1, (20,), generator=gen(1), dtype=torch.int64)
+    r.n = (r.counts.sum(dtype=torch.int64) // 20).clamp(max=2 ** 31 - 1).reshape(1)
+    r.counts, r.n = r.counts.to(torch.int32), r.n.to(torch.int32)
+    r.dl = torch.tensor([1e4, 0.0])
+    r.check(r.run())
+
+
 def test_gradients_against_differences_of_the_losses():
     """The kernel's dL against central differences of its own definition in 64 bits along random directions
     (h = 1e-5: the h^2 term is below 1e-9 of the slope's scale); the kernel's float32 error is the element bound."""
