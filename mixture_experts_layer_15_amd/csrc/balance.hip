@@ -37,6 +37,7 @@ constexpr int kMaxRowBlocks = 512;
 constexpr int kGradThreads = 256;  // of the gradient
 constexpr int kGradWaves = kGradThreads / kWave;
 constexpr int kMaxGradBlocks = 512;
+constexpr int kSoloPasses = 4;
 
 // A row of E logits on L lanes: lane g holds elements (c L + g) V + v,
 // c < C, v < V (V = 4: 16-byte loads, E a multiple of 4).
@@ -67,6 +68,26 @@ void with_row_shape(int E, F f) {
   if (E <= 128) return f(RowShape<1, 16, 8>{});
   if (E <= 256) return f(RowShape<1, 16, 16>{});
   return f(RowShape<1, 32, 16>{});
+}
+
+// The gradient's row shapes for few rows: more lanes a row, so that the rows
+// spread over more compute units and a lane stores less.
+template <class F>
+void with_wide_row_shape(int E, F f) {
+  if (E % 4 == 0) {
+    if (E <= 16) return with_row_shape(E, f);
+    if (E <= 32) return f(RowShape<4, 8, 1>{});
+    if (E <= 64) return f(RowShape<4, 16, 1>{});
+    if (E <= 128) return f(RowShape<4, 32, 1>{});
+    if (E <= 256) return f(RowShape<4, 64, 1>{});
+    return f(RowShape<4, 64, 2>{});
+  }
+  if (E <= 16) return with_row_shape(E, f);
+  if (E <= 32) return f(RowShape<1, 32, 1>{});
+  if (E <= 64) return f(RowShape<1, 64, 1>{});
+  if (E <= 128) return f(RowShape<1, 64, 2>{});
+  if (E <= 256) return f(RowShape<1, 64, 4>{});
+  return f(RowShape<1, 64, 8>{});
 }
 
 template <class S>
@@ -101,6 +122,7 @@ __device__ __forceinline__ float group_reduce(float v, F f) {
   if constexpr (L >= 8) v = f(v, dpp<0x141>(v));
   if constexpr (L >= 16) v = f(v, dpp<0x140>(v));
   if constexpr (L >= 32) v = f(v, __shfl_xor(v, 16, kWave));
+  if constexpr (L >= 64) v = f(v, __shfl_xor(v, 32, kWave));
   return v;
 }
 template <int L>
@@ -391,6 +413,17 @@ struct GateGradKernelArgs {
   long long rows_per_block;
 };
 
+// Zeros from value E to Ep (a multiple of 32) of a row whose start is 16-byte
+// aligned, by the L lanes of its group.
+template <int L, class T>
+__device__ __forceinline__ void clear_tail(T* row, int E, int Ep, int g) {
+  constexpr int V = 16 / sizeof(T);
+  const int up = (E + V - 1) / V * V;
+  for (int e = E + g; e < up; e += L) row[e] = T(0);
+  for (int e = up + g * V; e < Ep; e += L * V)
+    *reinterpret_cast<u32x4_t*>(row + e) = u32x4_t{0, 0, 0, 0};
+}
+
 // float32 -> bfloat16 rounding and what it leaves (none of an infinite or
 // NaN value, so that it is not turned into another one).
 __device__ __forceinline__ uint16_t split_bf16(float& v) {
@@ -582,7 +615,7 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
           if (e < E) row[e] = v[c];
         }
       }
-      for (int e = E + g; e < ka.Ep; e += S::L) row[e] = 0.0f;
+      clear_tail<S::L>(row, E, ka.Ep, g);
     }
     if (a.half) {
       uint32_t big = 0;  // the row's largest magnitude, as bits
@@ -607,7 +640,7 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
           if (e < E) row[e] = scaled_half(v[c], up);
         }
       }
-      for (int e = E + g; e < ka.Ep; e += S::L) row[e] = 0;
+      clear_tail<S::L>(row, E, ka.Ep, g);
     }
     if (!a.planes) continue;
 #pragma unroll
@@ -628,7 +661,7 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
           if (e < E) row[e] = h;
         }
       }
-      for (int e = E + g; e < ka.Ep; e += S::L) row[e] = 0;
+      clear_tail<S::L>(row, E, ka.Ep, g);
     }
   }
   if (!a.bias_part) return;
@@ -638,21 +671,56 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
     a.bias_part[(size_t)blockIdx.x * E + e] = (float)col_total<kGradWaves>(red, E, e);
 }
 
-// Workgroups of a row kernel of `waves` waves: whole passes of them, as many
-// workgroups as there are passes up to `most`.
-int row_blocks(long long T, int E, int waves, int most, long long* rows_per_block) {
-  long long pass = 0;
-  with_row_shape(E, [&](auto sh) { pass = waves * decltype(sh)::R; });
+// Workgroups of a row kernel that passes over `pass` rows at a time: whole
+// passes, as many workgroups as there are passes up to `most`.
+int row_blocks(long long T, long long pass, int most, long long* rows_per_block) {
   const long long passes = std::max<long long>((T + pass - 1) / pass, 1);
   const long long each = (passes + most - 1) / most;
   *rows_per_block = each * pass;
   return (int)((passes + each - 1) / each);
 }
+
+// The balance loss: up to four passes one workgroup makes them all, in one
+// launch (256 tokens of 128, a call among others: 8.4 us, in two kernels
+// 11.5 us; at eight passes, 1000 tokens of 64, 12.8 against 11.6 us).  Below
+// 64 passes the wide shape spreads the rows (the two kernels together: 1000
+// tokens of 64, 10.5 us, wide 7.8 us; 2048 of 128, 10.3 and 8.9 us; 8192 of
+// 128, which are 128 passes, 10.8 and 11.1 us).
+long long balance_pass(const Shape& s) {
+  long long pass = 0;
+  with_row_shape(s.E, [&](auto sh) { pass = kWaves * decltype(sh)::R; });
+  return pass;
+}
+template <class F>
+void with_balance_shape(const Shape& s, F f) {
+  const long long pass = balance_pass(s);
+  if (s.T > kSoloPasses * pass && s.T < 64 * pass) return with_wide_row_shape(s.E, f);
+  return with_row_shape(s.E, f);
+}
 int balance_blocks(const Shape& s, long long* rows) {
-  return row_blocks(s.T, s.E, kWaves, kMaxRowBlocks, rows);
+  long long pass = balance_pass(s);
+  if (s.T <= kSoloPasses * pass) {
+    *rows = kSoloPasses * pass;
+    return 1;
+  }
+  with_balance_shape(s, [&](auto sh) { pass = kWaves * decltype(sh)::R; });
+  return row_blocks(s.T, pass, kMaxRowBlocks, rows);
+}
+
+// Calls f with the gradient's row shape: the wide one up to 512 passes of the
+// other (2048 tokens, E = 64: 7.6 us, wide 4.8 us; 8192, E = 128: 10.7 and
+// 9.6 us; 16384, E = 256, 1024 passes: 16.8 and 21.2 us).
+template <class F>
+void with_grad_shape(const Shape& s, F f) {
+  long long pass = 0;
+  with_row_shape(s.E, [&](auto sh) { pass = kGradWaves * decltype(sh)::R; });
+  if (s.T < 512 * pass) return with_wide_row_shape(s.E, f);
+  return with_row_shape(s.E, f);
 }
 int grad_blocks(const Shape& s, long long* rows) {
-  return row_blocks(s.T, s.E, kGradWaves, kMaxGradBlocks, rows);
+  long long pass = 0;
+  with_grad_shape(s, [&](auto sh) { pass = kGradWaves * decltype(sh)::R; });
+  return row_blocks(s.T, pass, kMaxGradBlocks, rows);
 }
 
 struct BalanceLayout {
@@ -702,7 +770,7 @@ hipError_t balance_loss(const Shape& s, const float* logits, const int32_t* topk
   a.n_tokens = n_tokens;
   a.prob_mean = prob_mean;
   a.losses = losses;
-  with_row_shape(s.E, [&](auto sh) {
+  with_balance_shape(s, [&](auto sh) {
     using S = decltype(sh);
     if (a.nb == 1)
       hipLaunchKernelGGL((balance_rows<S, true>), dim3(1), dim3(kThreads), 0, st, a);
@@ -731,7 +799,7 @@ hipError_t gate_grad(const Shape& s, const GateGradArgs& a, int Ep, hipStream_t 
   ka.blocks = grad_blocks(s, &ka.rows_per_block);
   ka.act_bytes = act_bytes(s);
   const int nb = ka.blocks + (a.pad_src ? s.d / kGradWaves : 0);
-  with_row_shape(s.E, [&](auto sh) {
+  with_grad_shape(s, [&](auto sh) {
     using S = decltype(sh);
     hipLaunchKernelGGL((gate_grad_rows<S>), dim3(nb), dim3(kGradThreads), 0, st, ka);
   });
