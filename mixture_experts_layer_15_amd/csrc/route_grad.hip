@@ -29,12 +29,12 @@ namespace {
 constexpr int kXcds = 8;
 
 // Consecutive workgroups run on consecutive XCDs: gives each XCD one run of
-// consecutive items, so that items that share operands share an L2.
-// Launched with xcd_grid(items) workgroups; -1: nothing to do.
-__device__ __forceinline__ int xcd_item(int items) {
+// consecutive items, so that items that share operands share an L2.  Launched
+// with xcd_grid(items) workgroups, of which `block` is one; -1: nothing to do.
+__device__ __forceinline__ int xcd_item(int items, int block) {
   const int per = (items + kXcds - 1) / kXcds;
-  const int i = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
-  return (int)(blockIdx.x / kXcds) < per && i < items ? i : -1;
+  const int i = block % kXcds * per + block / kXcds;
+  return block / kXcds < per && i < items ? i : -1;
 }
 int xcd_grid(int items) { return (items + kXcds - 1) / kXcds * kXcds; }
 
@@ -172,11 +172,10 @@ struct DwCfg {
 };
 
 template <class C, bool kMask>
-__global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void router_dw(DwArgs a) {
+__device__ __forceinline__ void dw_tile(const DwArgs& a, int block, unsigned char* smem) {
   constexpr int MB = C::MB, NB = C::NB;
-  extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t* keep = reinterpret_cast<uint64_t*>(smem + C::kLds);  // kMask: kSegment bits
-  const int item = xcd_item(a.splits * a.e_tiles * a.c_tiles);
+  const int item = xcd_item(a.splits * a.e_tiles * a.c_tiles, block);
   if (item < 0) return;  // the whole workgroup
   // the expert tiles of a column tile are neighbours: they share x
   const int et = item % a.e_tiles;
@@ -372,6 +371,12 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 2 : 1) void route
     }
 }
 
+template <class C, bool kMask>
+__global__ __launch_bounds__(C::kThreads, 2) void router_dw(DwArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  dw_tile<C, kMask>(a, blockIdx.x, smem);
+}
+
 // ---- dx
 // The sum is short (the experts, at most 512), the output long: each wave
 // keeps its columns' share of the router matrix in registers as MFMA operands
@@ -415,8 +420,8 @@ __device__ __forceinline__ int dx_swz(int t) {
   return P % 256 == 0 ? t & 15 : P % 128 == 0 ? (t >> 1) & 7 : (t >> 2) & 3;
 }
 
-template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
-__global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
+template <bool kF32, int MB, int KS, int NB, int NW>
+__device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned char* smem) {
   constexpr int kSize = kF32 ? 4 : 2;        // bytes of a value
   constexpr int kTokens = 32 * NB;
   constexpr int P = KS * 32;                 // bytes of a staged row
@@ -425,8 +430,7 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
   constexpr int kPerWave = (kInstr + NW - 1) / NW;
   static_assert(kStage % 1024 == 0, "whole loads");
   constexpr int kStores = MB * NB * kSize;   // 16-byte stores of a lane per stage
-  extern __shared__ __align__(1024) unsigned char smem[];
-  const int item = xcd_item(a.c_groups * a.t_ranges);
+  const int item = xcd_item(a.c_groups * a.t_ranges, block);
   if (item < 0) return;  // the whole workgroup
   // the column groups of a token range run on one XCD (they share its rows)
   const int cg = item % a.c_groups;
@@ -587,6 +591,24 @@ __global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
   }
 }
 
+template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
+__global__ __launch_bounds__(NW* kWave, kMinWaves) void router_dx(DxArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  dx_tile<kF32, MB, KS, NB, NW>(a, blockIdx.x, smem);
+}
+
+// Both products of few tokens in one launch: the first dw_blocks workgroups
+// (a multiple of the XCDs) are those of dW_r, the others of dx.
+template <class C, bool kMask, int KS>
+__global__ __launch_bounds__(512, 2) void router_products(DwArgs w, DxArgs x, int dw_blocks) {
+  static_assert(C::kThreads == 512, "both have eight waves");
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if ((int)blockIdx.x < dw_blocks)
+    dw_tile<C, kMask>(w, blockIdx.x, smem);
+  else
+    dx_tile<C::kF32, 1, KS, 1, 8>(x, (int)blockIdx.x - dw_blocks, smem);
+}
+
 // ---- sums of the partial results, in order: the splits of dW_r (d E values,
 // a multiple of four) by the first w_blocks workgroups, the row blocks' column
 // sums by the others.
@@ -722,82 +744,148 @@ GradLayout grad_layout(const Shape& s) {
 }
 
 template <class C>
-hipError_t launch_dw(DwArgs a, hipStream_t st) {
+void place_dw(DwArgs& a) {
   a.c_tiles = (a.d + C::BC - 1) / C::BC;
   a.e_tiles = (a.E + C::BE - 1) / C::BE;
   a.t_per_split = ((a.T + a.splits - 1) / a.splits + 63) / 64 * 64;
-  const dim3 grid(xcd_grid(a.splits * a.e_tiles * a.c_tiles));
-  const int lds = C::kLds + (a.mask ? kSegment / 8 : 0);
-  if (a.mask) {
-    static std::atomic<uint64_t> done{0};
-    const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(&router_dw<C, true>), lds, done);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((router_dw<C, true>), grid, dim3(C::kThreads), lds, st, a);
-  } else {
-    static std::atomic<uint64_t> done{0};
-    const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(&router_dw<C, false>), lds, done);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((router_dw<C, false>), grid, dim3(C::kThreads), lds, st, a);
-  }
+}
+template <class C>
+int dw_lds(const DwArgs& a) {
+  return C::kLds + (a.mask ? kSegment / 8 : 0);
+}
+
+template <class C, bool kMask>
+hipError_t launch_dw_as(const DwArgs& a, hipStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  const int lds = dw_lds<C>(a);
+  const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(&router_dw<C, kMask>), lds, done);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((router_dw<C, kMask>), dim3(xcd_grid(a.splits * a.e_tiles * a.c_tiles)),
+                     dim3(C::kThreads), lds, st, a);
   return hipGetLastError();
+}
+template <class C>
+hipError_t launch_dw(DwArgs a, hipStream_t st) {
+  place_dw<C>(a);
+  return a.mask ? launch_dw_as<C, true>(a, st) : launch_dw_as<C, false>(a, st);
+}
+
+// Column groups and token ranges of dx, for `slots` workgroups at once.
+void place_dx(DxArgs& a, int cols, int tokens, int slots) {
+  a.c_groups = (a.d + cols - 1) / cols;
+  const long long steps = (a.T + tokens - 1) / tokens;
+  const int ranges = std::max(slots / a.c_groups, 1);
+  a.steps_per_range = (int)std::max<long long>((steps + ranges - 1) / ranges, 1);
+  a.t_ranges = (int)((steps + a.steps_per_range - 1) / a.steps_per_range);
+}
+constexpr int dx_lds(bool f32, int MB, int KS, int NB, int NW) {
+  return 2 * 32 * NB * KS * 32 + (f32 ? 0 : (2 * 32 * NB + NW * MB * 32) * 4);
 }
 
 template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
 hipError_t launch_dx_as(DxArgs a, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
-  constexpr int kTokens = 32 * NB;
-  constexpr int kLds = 2 * kTokens * KS * 32 + (kF32 ? 0 : (2 * kTokens + NW * MB * 32) * 4);
+  constexpr int kLds = dx_lds(kF32, MB, KS, NB, NW);
   static_assert(kLds <= 160 * 1024, "LDS budget");
   const void* kern = reinterpret_cast<const void*>(&router_dx<kF32, MB, KS, NB, NW, kMinWaves>);
   const hipError_t e = set_lds_attr(kern, kLds, done);
   if (e != hipSuccess) return e;
-  const int cols = MB * 32 * NW;
-  a.c_groups = (a.d + cols - 1) / cols;
   // as many workgroups as fit the compute units at once
-  const long long steps = (a.T + kTokens - 1) / kTokens;
-  const int slots = std::max(256 * 4 * kMinWaves / NW / a.c_groups, 1);
-  a.steps_per_range = (int)std::max<long long>((steps + slots - 1) / slots, 1);
-  a.t_ranges = (int)((steps + a.steps_per_range - 1) / a.steps_per_range);
+  place_dx(a, MB * 32 * NW, 32 * NB, 256 * 4 * kMinWaves / NW);
   hipLaunchKernelGGL((router_dx<kF32, MB, KS, NB, NW, kMinWaves>),
                      dim3(xcd_grid(a.c_groups * a.t_ranges)), dim3(NW * kWave), kLds, st, a);
   return hipGetLastError();
 }
 
 // The variant for KS steps: a wave's share of the matrix takes 4 MB KS
-// registers, a stage 32 NB x 32 KS bytes of LDS.  Where the wide one
-// has workgroups for less than half of the compute units, one of 128 columns
-// and 32 tokens (one token of 4096 x 128, float32: 23.8 us wide).
+// registers, a stage 32 NB x 32 KS bytes of LDS.  For few tokens one of 128
+// columns and 32 tokens a workgroup (one token of 4096 x 128, float32: 6.2 us,
+// 23.8 us wide).
+bool few_tokens(const Shape& s) {
+  // workgroups of 512 columns and 64 tokens for less than half of the compute
+  // units
+  return (long long)((s.d + 511) / 512) * ((s.T + 63) / 64) < 128;
+}
+
 template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
-hipError_t launch_dx_for(const DxArgs& a, hipStream_t st) {
-  const long long groups = (long long)((a.d + MB * 32 * NW - 1) / (MB * 32 * NW)) *
-                           ((a.T + 32 * NB - 1) / (32 * NB));
-  if (groups < 128) return launch_dx_as<kF32, 1, KS, 1, 4, 1>(a, st);
+hipError_t launch_dx_for(const DxArgs& a, bool few, hipStream_t st) {
+  if (few) return launch_dx_as<kF32, 1, KS, 1, 4, 1>(a, st);
   return launch_dx_as<kF32, MB, KS, NB, NW, kMinWaves>(a, st);
 }
 
-hipError_t launch_dx(const DxArgs& a, int Ep, bool f32, hipStream_t st) {
+hipError_t launch_dx(const DxArgs& a, int Ep, bool f32, bool few, hipStream_t st) {
   if (f32) switch (Ep) {
-      case 32: return launch_dx_for<true, 2, 4, 2, 4, 2>(a, st);
-      case 64: return launch_dx_for<true, 2, 8, 2, 4, 2>(a, st);
-      case 128: return launch_dx_for<true, 2, 16, 2, 8, 2>(a, st);
-      case 192: return launch_dx_for<true, 2, 24, 2, 4, 1>(a, st);
-      case 256: return launch_dx_for<true, 2, 32, 2, 4, 1>(a, st);
+      case 32: return launch_dx_for<true, 2, 4, 2, 4, 2>(a, few, st);
+      case 64: return launch_dx_for<true, 2, 8, 2, 4, 2>(a, few, st);
+      case 128: return launch_dx_for<true, 2, 16, 2, 8, 2>(a, few, st);
+      case 192: return launch_dx_for<true, 2, 24, 2, 4, 1>(a, few, st);
+      case 256: return launch_dx_for<true, 2, 32, 2, 4, 1>(a, few, st);
       case 320: return launch_dx_as<true, 1, 40, 1, 4, 1>(a, st);
       case 384: return launch_dx_as<true, 1, 48, 1, 4, 1>(a, st);
       case 448: return launch_dx_as<true, 1, 56, 1, 4, 1>(a, st);
       default: return launch_dx_as<true, 1, 64, 1, 4, 1>(a, st);
     }
   switch (Ep) {
-    case 32: return launch_dx_for<false, 2, 2, 2, 4, 2>(a, st);
-    case 64: return launch_dx_for<false, 2, 4, 2, 4, 2>(a, st);
-    case 128: return launch_dx_for<false, 2, 8, 2, 4, 2>(a, st);
-    case 192: return launch_dx_for<false, 2, 12, 2, 8, 2>(a, st);
-    case 256: return launch_dx_for<false, 2, 16, 2, 8, 2>(a, st);
-    case 320: return launch_dx_for<false, 2, 20, 2, 4, 1>(a, st);
-    case 384: return launch_dx_for<false, 2, 24, 2, 4, 1>(a, st);
-    case 448: return launch_dx_for<false, 2, 28, 2, 4, 1>(a, st);
-    default: return launch_dx_for<false, 2, 32, 2, 4, 1>(a, st);
+    case 32: return launch_dx_for<false, 2, 2, 2, 4, 2>(a, few, st);
+    case 64: return launch_dx_for<false, 2, 4, 2, 4, 2>(a, few, st);
+    case 128: return launch_dx_for<false, 2, 8, 2, 4, 2>(a, few, st);
+    case 192: return launch_dx_for<false, 2, 12, 2, 8, 2>(a, few, st);
+    case 256: return launch_dx_for<false, 2, 16, 2, 8, 2>(a, few, st);
+    case 320: return launch_dx_for<false, 2, 20, 2, 4, 1>(a, few, st);
+    case 384: return launch_dx_for<false, 2, 24, 2, 4, 1>(a, few, st);
+    case 448: return launch_dx_for<false, 2, 28, 2, 4, 1>(a, few, st);
+    default: return launch_dx_for<false, 2, 32, 2, 4, 1>(a, few, st);
   }
+}
+
+// dW_r and dx of few tokens in one launch.
+template <class C, int KS, bool kMask>
+hipError_t launch_products_as(const DwArgs& w, DxArgs x, hipStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  constexpr int kDx = dx_lds(C::kF32, 1, KS, 1, 8);
+  const int lds = std::max(dw_lds<C>(w), kDx);
+  const void* kern = reinterpret_cast<const void*>(&router_products<C, kMask, KS>);
+  const hipError_t e = set_lds_attr(kern, lds, done);
+  if (e != hipSuccess) return e;
+  place_dx(x, 256, 32, 256);
+  const int dw_blocks = xcd_grid(w.splits * w.e_tiles * w.c_tiles);
+  hipLaunchKernelGGL((router_products<C, kMask, KS>),
+                     dim3(dw_blocks + xcd_grid(x.c_groups * x.t_ranges)), dim3(512), lds, st, w, x,
+                     dw_blocks);
+  return hipGetLastError();
+}
+template <class C, int KS>
+hipError_t launch_products_for(DwArgs w, const DxArgs& x, hipStream_t st) {
+  place_dw<C>(w);
+  return w.mask ? launch_products_as<C, KS, true>(w, x, st)
+                : launch_products_as<C, KS, false>(w, x, st);
+}
+
+template <bool kF32>
+using Dw32 = DwCfg<kF32, 1, 1, 4, 1, 2, 64, 3>;
+template <bool kF32>
+using Dw64 = DwCfg<kF32, 2, 1, 2, 2, 2, 32, kF32 ? 5 : 6>;
+template <bool kF32>
+using Dw128 = DwCfg<kF32, 2, 2, 2, 2, 2, 32, 4>;
+
+// (the tile of dW_r follows from the experts, as in dw_plan; kB: steps of 64
+// experts)
+template <bool kF32, int kB>
+hipError_t launch_products(const DwArgs& w, const DxArgs& x, int Ep, hipStream_t st) {
+  switch (Ep) {
+    case 32: return launch_products_for<Dw32<kF32>, kB / 2>(w, x, st);
+    case 64: return launch_products_for<Dw64<kF32>, kB>(w, x, st);
+    case 128: return launch_products_for<Dw128<kF32>, 2 * kB>(w, x, st);
+    case 192: return launch_products_for<Dw128<kF32>, 3 * kB>(w, x, st);
+    case 256: return launch_products_for<Dw128<kF32>, 4 * kB>(w, x, st);
+  }
+  if constexpr (!kF32) switch (Ep) {
+      case 320: return launch_products_for<Dw128<kF32>, 5 * kB>(w, x, st);
+      case 384: return launch_products_for<Dw128<kF32>, 6 * kB>(w, x, st);
+      case 448: return launch_products_for<Dw128<kF32>, 7 * kB>(w, x, st);
+      case 512: return launch_products_for<Dw128<kF32>, 8 * kB>(w, x, st);
+    }
+  return hipErrorInvalidValue;  // (not reached: see route_backward)
 }
 
 }  // namespace
@@ -842,33 +930,54 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
     const hipError_t e = gate_grad(s, ga, Ep, st);
     if (e != hipSuccess) return e;
   }
+  DwArgs wa{};
   if (g.dw && s.T > 0) {
-    DwArgs a{};
-    a.x = static_cast<const unsigned char*>(g.x);
-    a.planes = planes;
-    a.mask = g.gate.mask;
-    a.zero = base + lay.zero;
-    a.out = part;
-    a.T = s.T;
-    a.d = s.d;
-    a.E = s.E;
-    a.Ep = Ep;
-    a.splits = ns;
-    hipError_t e;
-    if (f32)
-      e = plan.be == 32   ? launch_dw<DwCfg<true, 1, 1, 4, 1, 2, 64, 3>>(a, st)
-          : plan.be == 64 ? launch_dw<DwCfg<true, 2, 1, 2, 2, 2, 32, 5>>(a, st)
-                          : launch_dw<DwCfg<true, 2, 2, 2, 2, 2, 32, 4>>(a, st);
-    else if (plan.bc == 256)
-      e = plan.be == 32   ? launch_dw<DwCfg<false, 2, 1, 4, 1, 2, 64, 3>>(a, st)
-          : plan.be == 64 ? launch_dw<DwCfg<false, 2, 2, 4, 1, 2, 32, 4>>(a, st)
-                          : launch_dw<DwCfg<false, 4, 2, 2, 2, 2, 32, 3>>(a, st);
-    else
-      e = plan.be == 32   ? launch_dw<DwCfg<false, 1, 1, 4, 1, 2, 64, 3>>(a, st)
-          : plan.be == 64 ? launch_dw<DwCfg<false, 2, 1, 2, 2, 2, 32, 6>>(a, st)
-                          : launch_dw<DwCfg<false, 2, 2, 2, 2, 2, 32, 4>>(a, st);
-    if (e != hipSuccess) return e;
+    wa.x = static_cast<const unsigned char*>(g.x);
+    wa.planes = planes;
+    wa.mask = g.gate.mask;
+    wa.zero = base + lay.zero;
+    wa.out = part;
+    wa.T = s.T;
+    wa.d = s.d;
+    wa.E = s.E;
+    wa.Ep = Ep;
+    wa.splits = ns;
   }
+  DxArgs xa{};
+  if (g.dx && s.T > 0) {
+    const bool padded = s.E % (f32 ? 4 : 8) != 0;
+    xa.rows = f32 ? planes : base + lay.half;
+    xa.exponents = reinterpret_cast<const int*>(base + lay.exps);
+    xa.w = padded ? base + lay.wpad : static_cast<const unsigned char*>(g.w_router);
+    xa.w_pitch = padded ? Ep : s.E;
+    xa.E = xa.w_pitch;
+    xa.dx = static_cast<unsigned char*>(g.dx);
+    xa.T = s.T;
+    xa.d = s.d;
+  }
+  // few tokens: both products in one launch (a launch less, and the narrow
+  // grids side by side)
+  const bool few = few_tokens(s);
+  // (float32 rows of more than 256 experts leave eight waves no registers)
+  const bool both = products && g.dw && g.dx && few && plan.bc == 128 && (!f32 || Ep <= 256);
+  hipError_t e = hipSuccess;
+  if (both) {
+    e = f32 ? launch_products<true, 8>(wa, xa, Ep, st) : launch_products<false, 4>(wa, xa, Ep, st);
+  } else if (g.dw && s.T > 0) {
+    if (f32)
+      e = plan.be == 32   ? launch_dw<Dw32<true>>(wa, st)
+          : plan.be == 64 ? launch_dw<Dw64<true>>(wa, st)
+                          : launch_dw<Dw128<true>>(wa, st);
+    else if (plan.bc == 256)
+      e = plan.be == 32   ? launch_dw<DwCfg<false, 2, 1, 4, 1, 2, 64, 3>>(wa, st)
+          : plan.be == 64 ? launch_dw<DwCfg<false, 2, 2, 4, 1, 2, 32, 4>>(wa, st)
+                          : launch_dw<DwCfg<false, 4, 2, 2, 2, 2, 32, 3>>(wa, st);
+    else
+      e = plan.be == 32   ? launch_dw<Dw32<false>>(wa, st)
+          : plan.be == 64 ? launch_dw<Dw64<false>>(wa, st)
+                          : launch_dw<Dw128<false>>(wa, st);
+  }
+  if (e != hipSuccess) return e;
   const bool sum_w = g.dw && (ns > 1 || s.T == 0);
   if (sum_w || sum_b) {
     SumArgs a{};
@@ -884,22 +993,11 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
     hipLaunchKernelGGL(router_grad_sum,
                        dim3(a.w_blocks + (sum_b ? (s.E + kSumCols - 1) / kSumCols : 0)),
                        dim3(kSumThreads), 0, st, a);
-  }
-  if (g.dx && s.T > 0) {
-    const bool padded = s.E % (f32 ? 4 : 8) != 0;
-    DxArgs a{};
-    a.rows = f32 ? planes : base + lay.half;
-    a.exponents = reinterpret_cast<const int*>(base + lay.exps);
-    a.w = padded ? base + lay.wpad : static_cast<const unsigned char*>(g.w_router);
-    a.w_pitch = padded ? Ep : s.E;
-    a.E = a.w_pitch;
-    a.dx = static_cast<unsigned char*>(g.dx);
-    a.T = s.T;
-    a.d = s.d;
-    const hipError_t e = launch_dx(a, Ep, f32, st);
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  return hipGetLastError();
+  if (g.dx && s.T > 0 && !both) e = launch_dx(xa, Ep, f32, few, st);
+  return e;
 }
 
 }  // namespace moe
