@@ -704,7 +704,11 @@ int balance_blocks(const Shape& s, long long* rows) {
     return 1;
   }
   with_balance_shape(s, [&](auto sh) { pass = kWaves * decltype(sh)::R; });
-  return row_blocks(s.T, pass, kMaxRowBlocks, rows);
+  // Rows of 16-byte loads: one workgroup a compute unit, with half the partial
+  // sums to add (32768 tokens of 128: both kernels 13.4 us, 16.5 us with 512
+  // workgroups; 131072 of 256: 34.8 and 35.4 us); of 4-byte loads two (65536
+  // tokens of 511: 35.6 us, 39.2 us with 256).
+  return row_blocks(s.T, pass, s.E % 4 == 0 ? 256 : kMaxRowBlocks, rows);
 }
 
 // Calls f with the gradient's row shape: the wide one up to 512 passes of the
