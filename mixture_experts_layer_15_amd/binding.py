@@ -1,7 +1,8 @@
 """Thin ctypes binding of the C ABI in ``include/moe.h``.
 
-Argument marshalling only: tensors become device pointers, the stream becomes
-the current HIP stream, status codes become exceptions.  Every step of the
+Argument marshalling: tensors become device pointers, the stream becomes the
+current HIP stream, status codes become exceptions (the router-training calls
+check their tensors too).  Every step of the
 layer runs in the HIP library; there is no fallback of any kind.  PyTorch is
 used for device memory and streams.
 """

@@ -38,10 +38,22 @@ __device__ __forceinline__ int xcd_item(int items, int block) {
 }
 int xcd_grid(int items) { return (items + kXcds - 1) / kXcds * kXcds; }
 
+// At most N vector-memory operations of this wave (loads to LDS and stores,
+// counted in order) still in flight.  The empty statements keep the compiler
+// from moving a store or an LDS read across the count that assumes it done.
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
+
+// This wave's LDS reads have returned.
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  asm volatile("" ::: "memory");
 }
 
 // Barrier that orders LDS accesses of the wave's own instruction stream only:
@@ -113,11 +125,11 @@ __device__ __forceinline__ void dma4(const void* src, uint32_t lds) {
 #endif
 }
 
-// ---- dW_r, bf16
+// ---- dW_r
 // Tile: BC columns of x by BE experts, the sum over a range of tokens.  Both
 // operands have the summed index (the token) as their slow dimension, so they
 // are staged as they lie and the transposing read forms the operands.  A
-// staged row is cut into blocks of 64 bytes (32 columns, one MFMA block);
+// staged bf16 row is cut into blocks of 64 bytes (32 columns, one MFMA block);
 // block b of row t sits at b ^ swz(t), so that the four rows which a group of
 // 16 lanes reads together lie in different banks (256 bytes a sweep).
 //
@@ -320,7 +332,7 @@ __device__ __forceinline__ void dw_tile(const DwArgs& a, int block, unsigned cha
             }
         }
       }
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads of the stage have returned
+      wait_lds();
       b = b + 1 == C::NST ? 0 : b + 1;
     }
     lds_barrier();
@@ -381,12 +393,11 @@ __global__ __launch_bounds__(C::kThreads, 2) void router_dw(DwArgs a) {
 // The sum is short (the experts, at most 512), the output long: each wave
 // keeps its columns' share of the router matrix in registers as MFMA operands
 // (MB blocks of 32 columns, KS steps of 16 experts, in float32 of 8: 4 MB KS
-// registers) and
-// runs over the tokens, whose rows of dL pass through LDS, 32 NB tokens a stage, in
-// two buffers.  The waves of a workgroup have neighbouring columns and share
-// the stage.  The matrix is the A operand, with its rows in an order that
-// suits the stores.
-// A staged row (one token, one plane) of P bytes: 16-byte chunk c of row t
+// registers) and runs over the tokens, whose rows of dL pass through LDS,
+// 32 NB tokens a stage, in two buffers.  The waves of a workgroup have
+// neighbouring columns and share the stage.  The matrix is the A operand, with
+// its rows in an order that suits the stores.
+// A staged row (one token) of P bytes: 16-byte chunk c of row t
 // sits at c ^ swz(t) within its aligned group of 16 chunks (8, 4 where P is
 // no multiple of 256, 128), so that 16 consecutive rows at one logical chunk
 // lie in different banks.
@@ -557,7 +568,7 @@ __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned cha
 #pragma unroll
     for (int n = 0; n < NB; ++n)
       texp[n] = kF32 ? 0 : reinterpret_cast<const int*>(smem + 2 * kStage)[b * kTokens + n * 32 + l % 32];
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // this wave's reads of the stage have returned
+    wait_lds();
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const long long t = (s0 + s) * kTokens + n * 32 + l % 32;

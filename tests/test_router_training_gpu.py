@@ -404,6 +404,21 @@ def test_route_backward_experts_switched_off():
     assert torch.all(got["dlogits"][:, 1::3] == 0) and torch.all(got["dlogits"][17] == 0)
 
 
+def test_token_gradient_keeps_values_far_below_a_rows_largest():
+    """The float16 form of a row of dL: a value 2^-30 of the largest, which meets the only nonzero row of the
+    matrix, comes out within the row's 2^-39 and the formats' roundings."""
+    T, d, E = 40, 128, 2
+    r = Router(T, d, E, 2, "bf16", losses=False)
+    r.idx[:] = torch.tensor([0, 1])
+    r.w[:] = torch.tensor([0.5, 2.0 ** -31])
+    r.g[:] = torch.tensor([1.0, -1.0])
+    r.w_router[:, 0] = 0
+    got = r.run(("dx",))
+    r.check(got)
+    ref = -1.5 * 2.0 ** -31 * r.w_router[:, 1].double()   # w (g - mean), mean = 0.5 to 2^-31
+    assert torch.all((got["dx"].double() - ref).abs() <= ref.abs() * (BF16 + 2.0 ** -7))
+
+
 def test_route_backward_infinite_gradient_stays_infinite():
     """A slot whose gate gradient overflows reaches the matrix' gradient as inf or NaN of its own experts only."""
     r = Router(70, 128, 40, 2, "bf16", losses=False)
