@@ -19,6 +19,7 @@
 // with dL as it is.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "moe_device.h"
 #include "moe_internal.h"
@@ -413,14 +414,40 @@ struct DxArgs {
 };
 
 // The MFMA result has row 8 (q / 4) + 4 h + q % 4 in register q of lane half
-// h.  Row r of the operand is column dx_feat(r), so that each 16-byte store
-// of the two halves covers 32 consecutive bytes: float32 the columns as they
-// come, bf16 column 16 (q / 8) + 8 h + q % 8.
-template <bool kF32>
-__device__ __forceinline__ int dx_feat(int r) {
-  if constexpr (kF32) return r;
+// h.  Row r of block m of a wave's MB is column dx_feat(m, r) of them.  kQuad:
+// half h has the columns 16 MB h + 16 m + q, so that a lane's registers are
+// 16 MB consecutive columns of its token.  Else each 16-byte store of the two
+// halves covers 32 consecutive bytes: float32 the columns as they come, bf16
+// column 16 (q / 8) + 8 h + q % 8 of the block.
+template <bool kF32, int MB, bool kQuad>
+__device__ __forceinline__ int dx_feat(int m, int r) {
   const int h = (r >> 2) & 1, q = (r >> 3) * 4 + (r & 3);
-  return 16 * (q >> 3) + 8 * h + (q & 7);
+  if constexpr (kQuad) return 16 * MB * h + 16 * m + q;
+  if constexpr (kF32) return 32 * m + r;
+  return 32 * m + 16 * (q >> 3) + 8 * h + (q & 7);
+}
+
+// 4 x 4 transposition of 16-byte values within every four lanes: value r of
+// lane i goes to value i of lane r.
+__device__ __forceinline__ void quad_transpose(u32x4_t (&v)[4], int l) {
+  auto step = [&](auto ctrl, int bit) {
+    constexpr int kCtrl = decltype(ctrl)::value;
+    const bool up = l & bit;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (r & bit) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t x = v[r][q], y = v[r | bit][q];
+        const uint32_t fx = __builtin_amdgcn_update_dpp(0u, x, kCtrl, 0xF, 0xF, false);
+        const uint32_t fy = __builtin_amdgcn_update_dpp(0u, y, kCtrl, 0xF, 0xF, false);
+        v[r][q] = up ? fy : x;
+        v[r | bit][q] = up ? y : fx;
+      }
+    }
+  };
+  step(std::integral_constant<int, 0xB1>{}, 1);  // lane ^ 1
+  step(std::integral_constant<int, 0x4E>{}, 2);  // lane ^ 2
 }
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -441,6 +468,9 @@ __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned cha
   constexpr int kPerWave = (kInstr + NW - 1) / NW;
   static_assert(kStage % 1024 == 0, "whole loads");
   constexpr int kStores = MB * NB * kSize;   // 16-byte stores of a lane per stage
+  // Four 16-byte values at a time are transposed within four lanes before
+  // the store, where there are as many.
+  constexpr bool kQuad = MB * kSize % 4 == 0;
   const int item = xcd_item(a.c_groups * a.t_ranges, block);
   if (item < 0) return;  // the whole workgroup
   // the column groups of a token range run on one XCD (they share its rows)
@@ -477,12 +507,12 @@ __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned cha
   };
   load_stage(0, 0);
 
-  // lane l: matrix row dx_feat<kF32>(l % 32) of a block, the 16 bytes h of each
+  // lane l: matrix row dx_feat(m, l % 32), the 16 bytes h of each
   // step's 32 (float32: the step's product i takes value i of both halves)
   u32x4_t wf[MB][KS];
 #pragma unroll
   for (int m = 0; m < MB; ++m) {
-    const int c = min(c0 + m * 32 + dx_feat<kF32>(l % 32), a.d - 1);
+    const int c = min(c0 + dx_feat<kF32, MB, kQuad>(m, l % 32), a.d - 1);
     const unsigned char* row = a.w + (size_t)c * a.w_pitch * kSize + 16 * h;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -504,7 +534,7 @@ __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned cha
           big = max(big, max(wf[m][ks][q] & 0x7fff, (wf[m][ks][q] >> 16) & 0x7fff));
       big = max(big, (uint32_t)__shfl_xor((int)big, 32, kWave));  // the row's other half
       const int up = scale_exponent(big << 16);
-      if (h == 0) wexp[m * 32 + dx_feat<kF32>(l % 32)] = up;
+      if (h == 0) wexp[dx_feat<kF32, MB, kQuad>(m, l % 32)] = up;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -569,33 +599,59 @@ __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned cha
     for (int n = 0; n < NB; ++n)
       texp[n] = kF32 ? 0 : reinterpret_cast<const int*>(smem + 2 * kStage)[b * kTokens + n * 32 + l % 32];
     wait_lds();
+    // kQuad: lane l has 16 MB columns of token l % 32, from column 16 MB h, as
+    // kVals 16-byte values.  Transposed within four lanes, these store 64
+    // consecutive bytes of one token, in four stores of the lanes' four
+    // tokens: whole pieces of a line, which may stream past the caches (16384
+    // tokens of 7168 x 8: the whole call 134 us, with 32-byte pieces, 128 us
+    // with 64-byte ones, 108 us streaming; 32-byte pieces streaming are five
+    // times slower).
+    constexpr int kVals = MB * kSize;
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      const long long t = (s0 + s) * kTokens + n * 32 + l % 32;
+      u32x4_t o[kVals];
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
-        f32x16_t v = acc[m][n];
-        u32x4_t* o = reinterpret_cast<u32x4_t*>(a.dx + (t * a.d + c0 + m * 32) * kSize + 16 * h);
-        if constexpr (!kF32) {
-          // register 8 i + q is column 16 i + 8 h + q
+        const f32x16_t& v = acc[m][n];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < kSize; ++i) {
+          if constexpr (kF32) {
+            o[m * kSize + i] = u32x4_t{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                       __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
+          } else {
+            // the columns of registers 8 i .. 8 i + 7
+            const int* we = wexp + (kQuad ? 16 * MB * h + 16 * m + 8 * i : 32 * m + 16 * i + 8 * h);
+            float f[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              v[8 * i + q] = ldexpf(v[8 * i + q], -(wexp[m * 32 + 16 * i + 8 * h + q] + texp[n]));
-        }
-        if (t < a.T && c0 + m * 32 < a.d) {
-#pragma unroll
-          for (int i = 0; i < kSize; ++i) {
-            if constexpr (kF32)
-              o[2 * i] = u32x4_t{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                 __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
-            else
-              o[2 * i] = u32x4_t{pack_bf16x2(v[8 * i], v[8 * i + 1]),
-                                 pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                                 pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
-                                 pack_bf16x2(v[8 * i + 6], v[8 * i + 7])};
+            for (int q = 0; q < 8; ++q) f[q] = ldexpf(v[8 * i + q], -(we[q] + texp[n]));
+            o[m * kSize + i] = u32x4_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                       pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
           }
+        }
+      }
+      const long long tb = (s0 + s) * kTokens + n * 32;
+      if constexpr (kQuad) {
+        const long long t = tb + (l % 32 & ~3);
+#pragma unroll
+        for (int c = 0; c < kVals; c += 4) {
+          u32x4_t q4[4] = {o[c], o[c + 1], o[c + 2], o[c + 3]};
+          quad_transpose(q4, l);
+          unsigned char* to = a.dx + (t * a.d + c0 + 16 * MB * h) * kSize + (c + l % 4) * 16;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (t + r < a.T && c0 < a.d)
+              __builtin_nontemporal_store(
+                  q4[r], reinterpret_cast<u32x4_t*>(to + (long long)r * a.d * kSize));
+        }
+      } else {
+        const long long t = tb + l % 32;
+        if (t < a.T && c0 < a.d) {
+          unsigned char* to = a.dx + (t * a.d + c0) * kSize + 16 * h;
+#pragma unroll
+          for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int i = 0; i < kSize; ++i)
+              *reinterpret_cast<u32x4_t*>(to + 32 * m * kSize + 32 * i) = o[m * kSize + i];
         }
       }
     }
@@ -809,7 +865,9 @@ hipError_t launch_dx_as(DxArgs a, hipStream_t st) {
 }
 
 // The variant for KS steps: a wave's share of the matrix takes 4 MB KS
-// registers, a stage 32 NB x 32 KS bytes of LDS.  For few tokens one of 128
+// registers, a stage 32 NB x 32 KS bytes of LDS.  (With 256 experts, 64 tokens
+// a stage leave no registers for the transposition of the stores: 294 us a
+// call without it, 318 with spills, 272 with 32 tokens.)  For few tokens one of 128
 // columns and 32 tokens a workgroup (one token of 4096 x 128, float32: 6.2 us,
 // 23.8 us wide).
 bool few_tokens(const Shape& s) {
@@ -828,7 +886,7 @@ hipError_t launch_dx(const DxArgs& a, int Ep, bool f32, bool few, hipStream_t st
   if (f32) switch (Ep) {
       case 32: return launch_dx_for<true, 2, 4, 2, 4, 2>(a, few, st);
       case 64: return launch_dx_for<true, 2, 8, 2, 4, 2>(a, few, st);
-      case 128: return launch_dx_for<true, 2, 16, 2, 8, 2>(a, few, st);
+      case 128: return launch_dx_for<true, 2, 16, 1, 8, 2>(a, few, st);
       case 192: return launch_dx_for<true, 2, 24, 2, 4, 1>(a, few, st);
       case 256: return launch_dx_for<true, 2, 32, 2, 4, 1>(a, few, st);
       case 320: return launch_dx_as<true, 1, 40, 1, 4, 1>(a, st);
@@ -841,7 +899,7 @@ hipError_t launch_dx(const DxArgs& a, int Ep, bool f32, bool few, hipStream_t st
     case 64: return launch_dx_for<false, 2, 4, 2, 4, 2>(a, few, st);
     case 128: return launch_dx_for<false, 2, 8, 2, 4, 2>(a, few, st);
     case 192: return launch_dx_for<false, 2, 12, 2, 8, 2>(a, few, st);
-    case 256: return launch_dx_for<false, 2, 16, 2, 8, 2>(a, few, st);
+    case 256: return launch_dx_for<false, 2, 16, 1, 8, 2>(a, few, st);
     case 320: return launch_dx_for<false, 2, 20, 2, 4, 1>(a, few, st);
     case 384: return launch_dx_for<false, 2, 24, 2, 4, 1>(a, few, st);
     case 448: return launch_dx_for<false, 2, 28, 2, 4, 1>(a, few, st);
