@@ -14,6 +14,8 @@
 // only writes zeros.  The pass is HBM-bound; bf16 rows are read and written
 // with nontemporal accesses (each byte is touched once: measured 55 -> 48 us
 // on the Qwen3 prefill's 268 MB of expert outputs).
+#include <algorithm>
+
 #include "moe_device.h"
 #include "moe_internal.h"
 
@@ -142,7 +144,8 @@ __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(CombineGr
   constexpr int V = 16 / kSize;  // values of a chunk
   constexpr int U = 4;           // chunks of a lane in flight
   const int g = threadIdx.x % L;
-  const long long s = (long long)blockIdx.x * (kMaxThreads / L) + threadIdx.x / L;
+  const long long block = (long long)blockIdx.y * gridDim.x + blockIdx.x;
+  const long long s = block * (kMaxThreads / L) + threadIdx.x / L;
   if (s >= a.S) return;  // whole groups
   const int p = a.pos[s];
   if (p < 0 || p >= a.S) {
@@ -197,7 +200,10 @@ __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(CombineGr
 template <bool kBF16, int L>
 void launch_combine_backward(const CombineGradArgs& a, hipStream_t st) {
   constexpr int per = kMaxThreads / L;
-  hipLaunchKernelGGL((combine_backward_kernel<kBF16, L>), dim3((unsigned)((a.S + per - 1) / per)),
+  const long long blocks = (a.S + per - 1) / per;
+  // one dimension of a launch has fewer than 2^32 threads, 2^31 slots need more
+  const long long nx = std::min(blocks, 1LL << 22), ny = (blocks + nx - 1) / nx;
+  hipLaunchKernelGGL((combine_backward_kernel<kBF16, L>), dim3((unsigned)nx, (unsigned)ny),
                      dim3(kMaxThreads), 0, st, a);
 }
 

@@ -486,6 +486,43 @@ def test_gradients_against_differences_of_the_losses():
         assert abs((float(up) - float(down)) / (2 * h) - slope) <= tol
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_offsets_past_32_bits(act):
+    """Logits, their gradient and its planes of more than 2^32 bytes: a few tokens at both ends are kept, the
+    rows between hold NaN.  The results are those of the kept tokens alone."""
+    n, d, E, k = 300, 128, 512, 4
+    T = 2 ** 21 + 77
+    r = Router(n, d, E, k, act)
+    rows = torch.cat([torch.arange(100), torch.arange(T - 200, T)]).to(DEV)
+
+    def spread(t, fill):
+        out = torch.full((T,) + t.shape[1:], fill, dtype=t.dtype, device=DEV)
+        out[rows] = t.to(DEV)
+        return out
+
+    p = B.problem(T, d, E, k, 128, 0, E, act, act)
+    nan = float("nan")
+    L, idx = spread(r.L, nan), spread(r.idx, 0)
+    mask = spread(torch.ones(n, dtype=torch.uint8), 0)
+    o = dict(counts=torch.full((E,), -5, dtype=torch.int32, device=DEV),
+             n_tokens=torch.full((1,), -5, dtype=torch.int32, device=DEV),
+             prob_mean=torch.full((E,), 7.0, device=DEV), losses=torch.full((2,), 7.0, device=DEV))
+    B.moe_balance_loss(p, L, idx, mask, o["counts"], o["n_tokens"], o["prob_mean"], o["losses"],
+                       B.workspace(p, B.MOE_CALL_BALANCE_LOSS, DEV))
+    got = dict(dlogits=torch.full((T, E), 7.0, device=DEV), dx=torch.full((T, d), 7.0, dtype=ACT[act], device=DEV),
+               dw_router=torch.full((d, E), 7.0, device=DEV), dbias=torch.full((E,), 7.0, device=DEV))
+    B.moe_route_backward(p, x=spread(r.x, nan), w_router=dev(r.w_router), logits=L, topk_idx=idx,
+                         topk_w=spread(r.w, nan), dtopk_w=spread(r.g, nan), token_mask=mask, counts=o["counts"],
+                         n_tokens=o["n_tokens"], dlosses=dev(r.dl), **got,
+                         ws=B.workspace(p, B.MOE_CALL_ROUTE_BACKWARD, DEV))
+    torch.cuda.synchronize()
+    check_balance({m: t.cpu() for m, t in o.items()}, r.L, r.idx, None, E, k)
+    r.check({m: (t[rows] if len(t) == T else t).cpu() for m, t in got.items()})
+    for m in ("dlogits", "dx"):
+        got[m][rows] = 0
+        assert int(torch.count_nonzero(got[m])) == 0
+
+
 # ---- the combine's backward pass
 
 def run_combine(T, d, E, local, k, act, gates=True, want=("dy", "dtopk_w"), seed=0):
@@ -553,6 +590,31 @@ def test_combine_backward_positions_outside_are_not_kept():
     torch.cuda.synchronize()
     assert dw.cpu().reshape(-1).tolist() == [128.0, 0, 0, 128.0, 0, 0, 128.0, 128.0]
     assert torch.all(dy[:4] == 1) and torch.all(dy[4:] == 7)
+
+
+def test_combine_backward_of_more_slots_than_one_grid_dimension_holds():
+    # a wave a slot, 71 million slots: more than 2^32 threads; slots at both ends and in between are kept
+    T, d, k = 2 ** 22 - 8, 512, 17
+    p = B.problem(T, d, 17, k, 128, 0, 17, "bf16", "bf16")
+    S = T * k
+    at = torch.tensor([0, 1, 5 * k + 3, S // 2, 2 ** 26 - 1, 2 ** 26, 2 ** 26 + 1, S - k, S - 1])
+    n = len(at)
+    pos = torch.full((S,), -1, dtype=torch.int32, device=DEV)
+    pos[at.to(DEV)] = torch.arange(n, dtype=torch.int32, device=DEV)
+    dout = torch.full((T, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    g = gen(5)
+    rows = torch.randint(-3, 4, (n, d), generator=g).to(torch.bfloat16)
+    dout[(at // k).to(DEV)] = rows.to(DEV)   # (a token of two kept slots has one of its rows)
+    y = torch.randint(-3, 4, (n, d), generator=g).to(torch.bfloat16).to(DEV)
+    dy, dw = torch.full_like(y, 7.0), torch.full((S,), 7.0, device=DEV)
+    # no position names a row behind the n that are there: addresses, since the whole arrays have 73 GB
+    B.moe_combine_backward(p, dout, y.data_ptr(), pos, None, dy.data_ptr(), dw)
+    torch.cuda.synchronize()
+    mine = dout[(at // k).to(DEV)]
+    assert torch.equal(dy, mine)   # small integers: exact
+    assert torch.equal(dw[at.to(DEV)].cpu(), (mine.cpu().double() * y.cpu().double()).sum(dim=1).float())
+    dw[at.to(DEV)] = 0
+    assert int(torch.count_nonzero(dw)) == 0
 
 
 # ---- gradient norm and clipping
