@@ -369,7 +369,7 @@ class GradList:
         out = grads if out is None else list(out)
         if len(out) != len(grads):
             _refuse(c, f"{len(out)} outputs for {len(grads)} gradients")
-        T = torch.Tensor   # (maps over the methods: a list of 100 tensors takes 30 us)
+        T = torch.Tensor   # (maps over the methods: a list of 100 tensors takes 50 us)
         codes = list(map(_GRAD_CODE.get, [g.dtype for g in grads]))
         if None in codes:
             raise MoEError(c, MOE_ERR_UNSUPPORTED,

@@ -13,8 +13,8 @@
 // bfloat16's 2^-8): each token's row times the power of two that brings its
 // largest value to 2^14, and each row of the router matrix, exactly converted,
 // likewise; the result is scaled back.  (Two bfloat16 planes of dL took twice
-// the matrix instructions: 145 us against 104 us on 16384 tokens of
-// 7168 x 256.)
+// the matrix instructions: 145 us against 104 us, which are 94 us with today's
+// stores, on 16384 tokens of 7168 x 256.)
 // float32 activations: the same kernels on the float32 matrix instructions,
 // with dL as it is.
 #include <algorithm>
