@@ -412,8 +412,8 @@ typedef struct {
  * constant: neither has one).  Rows of masked tokens are 0 in dlogits and dx.
  * Slots with an id outside [0, E) are left out of every sum.  N <= 0 leaves
  * the losses' terms out.  Sums are float32; with bf16 activations dx
- * (which is rounded to 8 bits) is formed from dL rounded to 11 significant
- * bits (and to 2^-39 of the row's largest), dw_router from all 24.
+ * (which is rounded to 8 bits) is formed from dL rounded to 16 significant
+ * bits, dw_router from all 24 (values of dL below 2^-102 may have fewer).
  * Where an infinity or NaN enters a sum, the sum is not finite (an infinity
  * may come out as NaN).
  * T = 0 writes zeros to dw_router and dbias.

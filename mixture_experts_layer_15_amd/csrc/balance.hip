@@ -434,9 +434,9 @@ __device__ __forceinline__ uint16_t split_bf16(float& v) {
 }
 
 // Workgroup b: consecutive rows.  Writes the float32 gradient, what the
-// products read (three bfloat16 planes whose sum is the value, and the row in
-// float16 with its scale, or the float32 row; columns E .. Ep - 1 are zero),
-// and the workgroup's column sums.
+// products read (bfloat16 planes whose sum is the value: three hold all 24
+// bits, two 16; or the float32 row; columns E .. Ep - 1 are zero), and the
+// workgroup's column sums.
 //
 // The gates' gradient has k values of a row's E.  Lane j of the row's group
 // forms that of slot j (then j + L, ...) and adds it to a row of zeros in LDS
@@ -617,34 +617,10 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
       }
       clear_tail<S::L>(row, E, ka.Ep, g);
     }
-    if (a.half) {
-      uint32_t big = 0;  // the row's largest magnitude, as bits
-#pragma unroll
-      for (int q = 0; q < S::Q; ++q) big = max(big, __float_as_uint(v[q]) & 0x7fffffffu);
-      big = __float_as_uint(group_reduce<S::L>(__uint_as_float(big), [](float p, float q) {
-        return __uint_as_float(max(__float_as_uint(p), __float_as_uint(q)));
-      }));
-      const int up = scale_exponent(big);
-      if (g == 0) a.exponents[t] = up;
-      uint16_t* row = a.half + t * ka.Ep;
-#pragma unroll
-      for (int c = 0; c < S::C; ++c) {
-        const int e = (c * S::L + g) * S::V;
-        if constexpr (S::V == 4) {
-          uint32_t x4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x4[i] = scaled_half(v[c * 4 + i], up);
-          if (e < E)
-            *reinterpret_cast<u32x2_t*>(row + e) = u32x2_t{x4[0] | x4[1] << 16, x4[2] | x4[3] << 16};
-        } else {
-          if (e < E) row[e] = scaled_half(v[c], up);
-        }
-      }
-      clear_tail<S::L>(row, E, ka.Ep, g);
-    }
     if (!a.planes) continue;
 #pragma unroll
     for (int pl = 0; pl < 3; ++pl) {
+      if (pl >= a.nplanes) break;
       uint16_t* row = a.planes + ((size_t)pl * ka.T + t) * ka.Ep;
 #pragma unroll
       for (int c = 0; c < S::C; ++c) {

@@ -61,20 +61,6 @@ __device__ __forceinline__ bf16x8_t e2m1x8_to_bf16x8(uint32_t q, float scale) {
                                               __builtin_bit_cast(uint32_t, b3)});
 }
 
-// The power of two that brings a row whose largest magnitude has the float32
-// bits `big` to [2^14, 2^15), so that its float16 has all 11 bits down to
-// 2^-28 of it; 0 for a row with an infinity or NaN.
-__device__ __forceinline__ int scale_exponent(uint32_t big) {
-  const int e = (int)(big >> 23) & 0xff;
-  return e == 0xff ? 0 : 14 + 127 - e;
-}
-
-// v times 2^up as a float16's bits, rounded to nearest even.
-__device__ __forceinline__ uint16_t scaled_half(float v, int up) {
-  const _Float16 h = (_Float16)ldexpf(v, up);
-  return __builtin_bit_cast(uint16_t, h);
-}
-
 __device__ __forceinline__ int lane_id() { return __lane_id(); }
 
 // Wave-wide sum with a fixed butterfly order (deterministic).

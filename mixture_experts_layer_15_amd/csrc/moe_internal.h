@@ -115,9 +115,8 @@ struct GateGradArgs {
   const int32_t* n_tokens;
   const float* dlosses;    // [2] or null
   float* dlogits;          // [T][E] or null
-  uint16_t* planes;        // [3][T][Ep] bfloat16 planes whose sum is the gradient, or null
-  uint16_t* half;          // [T][Ep] float16: the gradient times 2^exponents[t], or null
-  int* exponents;          // [T]
+  uint16_t* planes;        // [nplanes][T][Ep] bfloat16 planes whose sum is the gradient, or null
+  int nplanes;             // 2 or 3
   float* dl_rows;          // [T][Ep] the gradient, columns from E on zero, or null
   const void* pad_src;     // a matrix [d][E] of act values that is copied to
   void* pad_dst;           // [d][Ep] (zeros behind E), or null

@@ -9,12 +9,11 @@
 // (float32) is split into three bfloat16 planes whose sum is the value
 // (gate_grad): the products with the bfloat16 tokens are exact and only the
 // float32 sums round.  The tokens' gradient is rounded to bfloat16 at the end,
-// so dL goes into it with the 11 bits of a float16 (2^-11 off, an eighth of a
-// bfloat16's 2^-8): each token's row times the power of two that brings its
-// largest value to 2^14, and each row of the router matrix, exactly converted,
-// likewise; the result is scaled back.  (Two bfloat16 planes of dL took twice
-// the matrix instructions: 145 us against 104 us, which are 94 us with today's
-// stores, on 16384 tokens of 7168 x 256.)
+// so two planes do for it: every value of dL with 16 bits (2^-17 off, where the
+// result is rounded by up to 2^-8), whatever else is in its row, and the router
+// matrix as it is.  (One product in float16, of rows of both scaled by powers of
+// two, took 279 us a call against 301 us on 16384 tokens of 7168 x 256, but lost
+// what lies far below a row's largest value, in dL and in the matrix.)
 // float32 activations: the same kernels on the float32 matrix instructions,
 // with dL as it is.
 #include <algorithm>
@@ -104,25 +103,6 @@ __device__ __forceinline__ u32x2_t read_tr(uint32_t lds) {
 #else
   (void)lds;
   return u32x2_t{};
-#endif
-}
-
-// 4 bytes per lane, global -> LDS: lane i's land at lds + 4 i.
-__device__ __forceinline__ void dma4(const void* src, uint32_t lds) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  uint32_t m0;  // (the instruction takes its LDS address from M0, which is put back)
-  asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %2\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dword %1, off\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(m0)
-      : "v"(src), "s"(lds)
-      : "memory");
-#else
-  (void)src;
-  (void)lds;
 #endif
 }
 
@@ -403,8 +383,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void router_dw(DwArgs a) {
 // no multiple of 256, 128), so that 16 consecutive rows at one logical chunk
 // lie in different banks.
 struct DxArgs {
-  const unsigned char* rows;    // [T][Ep] dL: float16 scaled by 2^exponent, or float32
-  const int* exponents;         // [T] (bf16)
+  const unsigned char* rows;    // dL: bf16 the first two planes of [3][T][Ep], float32 [T][Ep]
   const unsigned char* w;       // [d][w_pitch], experts behind E not read
   unsigned char* dx;            // [T][d]
   long long T;
@@ -450,8 +429,6 @@ __device__ __forceinline__ void quad_transpose(u32x4_t (&v)[4], int l) {
   step(std::integral_constant<int, 0x4E>{}, 2);  // lane ^ 2
 }
 
-typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
-
 template <int KS>
 __device__ __forceinline__ int dx_swz(int t) {
   constexpr int P = KS * 32;
@@ -461,9 +438,11 @@ __device__ __forceinline__ int dx_swz(int t) {
 template <bool kF32, int MB, int KS, int NB, int NW>
 __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned char* smem) {
   constexpr int kSize = kF32 ? 4 : 2;        // bytes of a value
+  constexpr int kPlanes = kF32 ? 1 : 2;
   constexpr int kTokens = 32 * NB;
   constexpr int P = KS * 32;                 // bytes of a staged row
-  constexpr int kStage = kTokens * P;
+  constexpr int kPlane = kTokens * P;
+  constexpr int kStage = kPlanes * kPlane;
   constexpr int kInstr = kStage / 1024;      // 1 KB loads of a stage
   constexpr int kPerWave = (kInstr + NW - 1) / NW;
   static_assert(kStage % 1024 == 0, "whole loads");
@@ -494,16 +473,12 @@ __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned cha
       const int n = w * kPerWave + i;
       if (kInstr % NW != 0 && n >= kInstr) break;
       const int q = n * 64 + l;               // 16-byte chunk of the stage
-      const int r = q / (P / 16), pc = q % (P / 16);
+      const int row = q / (P / 16), pc = q % (P / 16);
+      const int pl = row / kTokens, r = row % kTokens;
       const int c = pc ^ dx_swz<KS>(r);
       const long long t = min((s0 + s) * kTokens + r, a.T - 1);
-      dma16(a.rows + t * P + c * 16, lds0 + b * kStage + n * 1024);
+      dma16(a.rows + (pl * a.T + t) * P + c * 16, lds0 + b * kStage + n * 1024);
     }
-    // the tokens' exponents go the same way: a load into registers would be
-    // waited for with every store before it
-    if (!kF32 && w == 0 && l < kTokens)
-      dma4(a.exponents + min((s0 + s) * kTokens + l, a.T - 1),
-           lds0 + 2 * kStage + b * kTokens * 4);
   };
   load_stage(0, 0);
 
@@ -519,30 +494,6 @@ __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned cha
       wf[m][ks] = u32x4_t{0, 0, 0, 0};
       if (32 * ks + 16 * h < a.E * kSize)
         wf[m][ks] = *reinterpret_cast<const u32x4_t*>(row + 32 * ks);
-    }
-  }
-  // float16: the rows scaled so that their largest value is at 2^14
-  int* wexp = reinterpret_cast<int*>(smem + 2 * kStage) + 2 * kTokens + w * MB * 32;
-  if constexpr (!kF32) {
-#pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      uint32_t big = 0;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          big = max(big, max(wf[m][ks][q] & 0x7fff, (wf[m][ks][q] >> 16) & 0x7fff));
-      big = max(big, (uint32_t)__shfl_xor((int)big, 32, kWave));  // the row's other half
-      const int up = scale_exponent(big << 16);
-      if (h == 0) wexp[dx_feat<kF32, MB, kQuad>(m, l % 32)] = up;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t v = wf[m][ks][q];
-          wf[m][ks][q] = scaled_half(__uint_as_float(v << 16), up) |
-                         (uint32_t)scaled_half(__uint_as_float(v & 0xffff0000u), up) << 16;
-        }
     }
   }
   // operand read: lane l has token l % 32 of a block, chunk 2 ks + h
@@ -569,35 +520,33 @@ __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned cha
       for (int n = 0; n < NB; ++n) acc[m][n] = f32x16_t{};
     const unsigned char* st = smem + b * kStage;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      u32x4_t pb[NB];
+    for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
-        pb[n] = *reinterpret_cast<const u32x4_t*>(st + (base[n] ^ ((ks % kGroup) << 5)) +
-                                                  ks / kGroup * kGroup * 32);
-      if constexpr (kF32) {
+      for (int pl = 0; pl < kPlanes; ++pl) {
+        u32x4_t pb[NB];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int n = 0; n < NB; ++n)
+          pb[n] = *reinterpret_cast<const u32x4_t*>(
+              st + pl * kPlane + (base[n] ^ ((ks % kGroup) << 5)) + ks / kGroup * kGroup * 32);
+        if constexpr (kF32) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+              for (int m = 0; m < MB; ++m)
+                acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                    __uint_as_float(wf[m][ks][i]), __uint_as_float(pb[n][i]), acc[m][n], 0, 0, 0);
+        } else {
 #pragma unroll
           for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int m = 0; m < MB; ++m)
-              acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                  __uint_as_float(wf[m][ks][i]), __uint_as_float(pb[n][i]), acc[m][n], 0, 0, 0);
-      } else {
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int m = 0; m < MB; ++m)
-            acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                __builtin_bit_cast(f16x8_t, wf[m][ks]), __builtin_bit_cast(f16x8_t, pb[n]),
-                acc[m][n], 0, 0, 0);
+              acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  __builtin_bit_cast(bf16x8_t, wf[m][ks]), __builtin_bit_cast(bf16x8_t, pb[n]),
+                  acc[m][n], 0, 0, 0);
+        }
       }
-    }
-    int texp[NB];
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-      texp[n] = kF32 ? 0 : reinterpret_cast<const int*>(smem + 2 * kStage)[b * kTokens + n * 32 + l % 32];
     wait_lds();
     // kQuad: lane l has 16 MB columns of token l % 32, from column 16 MB h, as
     // kVals 16-byte values.  Transposed within four lanes, these store 64
@@ -619,13 +568,9 @@ __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned cha
             o[m * kSize + i] = u32x4_t{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
                                        __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
           } else {
-            // the columns of registers 8 i .. 8 i + 7
-            const int* we = wexp + (kQuad ? 16 * MB * h + 16 * m + 8 * i : 32 * m + 16 * i + 8 * h);
-            float f[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) f[q] = ldexpf(v[8 * i + q], -(we[q] + texp[n]));
-            o[m * kSize + i] = u32x4_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                       pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+            o[m * kSize + i] =
+                u32x4_t{pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                        pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7])};
           }
         }
       }
@@ -781,7 +726,7 @@ DwPlan dw_plan(const Shape& s) {
 }
 
 struct GradLayout {
-  size_t zero, planes, half, exps, wpad, bias, dw, total;
+  size_t zero, planes, wpad, bias, dw, total;
 };
 
 GradLayout grad_layout(const Shape& s) {
@@ -796,8 +741,6 @@ GradLayout grad_layout(const Shape& s) {
   L.zero = take(kZeroLineBytes);
   if (s.act == kBF16) {
     L.planes = take((size_t)3 * s.T * Ep * 2);
-    L.half = take((size_t)s.T * Ep * 2);
-    L.exps = take((size_t)s.T * 4);
     L.wpad = take(s.E % 8 != 0 ? (size_t)s.d * Ep * 2 : 0);
   } else {
     L.planes = take((size_t)s.T * Ep * 4);
@@ -845,14 +788,14 @@ void place_dx(DxArgs& a, int cols, int tokens, int slots) {
   a.steps_per_range = (int)std::max<long long>((steps + ranges - 1) / ranges, 1);
   a.t_ranges = (int)((steps + a.steps_per_range - 1) / a.steps_per_range);
 }
-constexpr int dx_lds(bool f32, int MB, int KS, int NB, int NW) {
-  return 2 * 32 * NB * KS * 32 + (f32 ? 0 : (2 * 32 * NB + NW * MB * 32) * 4);
+constexpr int dx_lds(bool f32, int KS, int NB) {
+  return 2 * (f32 ? 1 : 2) * 32 * NB * KS * 32;
 }
 
 template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
 hipError_t launch_dx_as(DxArgs a, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
-  constexpr int kLds = dx_lds(kF32, MB, KS, NB, NW);
+  constexpr int kLds = dx_lds(kF32, KS, NB);
   static_assert(kLds <= 160 * 1024, "LDS budget");
   const void* kern = reinterpret_cast<const void*>(&router_dx<kF32, MB, KS, NB, NW, kMinWaves>);
   const hipError_t e = set_lds_attr(kern, kLds, done);
@@ -865,9 +808,9 @@ hipError_t launch_dx_as(DxArgs a, hipStream_t st) {
 }
 
 // The variant for KS steps: a wave's share of the matrix takes 4 MB KS
-// registers, a stage 32 NB x 32 KS bytes of LDS.  (With 256 experts, 64 tokens
-// a stage leave no registers for the transposition of the stores: 294 us a
-// call without it, 318 with spills, 272 with 32 tokens.)  For few tokens one of 128
+// registers, a stage 32 NB x 32 KS bytes of LDS a plane.  (With 256 experts, 64 tokens
+// a stage leave no registers for the transposition of the stores, with more no
+// LDS.)  For few tokens one of 128
 // columns and 32 tokens a workgroup (one token of 4096 x 128, float32: 6.2 us,
 // 23.8 us wide).
 bool few_tokens(const Shape& s) {
@@ -900,10 +843,10 @@ hipError_t launch_dx(const DxArgs& a, int Ep, bool f32, bool few, hipStream_t st
     case 128: return launch_dx_for<false, 2, 8, 2, 4, 2>(a, few, st);
     case 192: return launch_dx_for<false, 2, 12, 2, 8, 2>(a, few, st);
     case 256: return launch_dx_for<false, 2, 16, 1, 8, 2>(a, few, st);
-    case 320: return launch_dx_for<false, 2, 20, 2, 4, 1>(a, few, st);
-    case 384: return launch_dx_for<false, 2, 24, 2, 4, 1>(a, few, st);
-    case 448: return launch_dx_for<false, 2, 28, 2, 4, 1>(a, few, st);
-    default: return launch_dx_for<false, 2, 32, 2, 4, 1>(a, few, st);
+    case 320: return launch_dx_for<false, 2, 20, 1, 4, 1>(a, few, st);
+    case 384: return launch_dx_for<false, 2, 24, 1, 4, 1>(a, few, st);
+    case 448: return launch_dx_for<false, 2, 28, 1, 4, 1>(a, few, st);
+    default: return launch_dx_for<false, 2, 32, 1, 4, 1>(a, few, st);
   }
 }
 
@@ -911,7 +854,7 @@ hipError_t launch_dx(const DxArgs& a, int Ep, bool f32, bool few, hipStream_t st
 template <class C, int KS, bool kMask>
 hipError_t launch_products_as(const DwArgs& w, DxArgs x, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
-  constexpr int kDx = dx_lds(C::kF32, 1, KS, 1, 8);
+  constexpr int kDx = dx_lds(C::kF32, KS, 1);
   const int lds = std::max(dw_lds<C>(w), kDx);
   const void* kern = reinterpret_cast<const void*>(&router_products<C, kMask, KS>);
   const hipError_t e = set_lds_attr(kern, lds, done);
@@ -973,8 +916,8 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
   const bool sum_b = g.dbias && (s.T == 0 || gate_grad_blocks(s) > 1);
   float* bias_part = sum_b ? reinterpret_cast<float*>(base + lay.bias) : g.dbias;
   float* part = ns > 1 ? reinterpret_cast<float*>(base + lay.dw) : g.dw;
-  // what the products read, bf16: the planes and the float16 rows; float32:
-  // rows of Ep values (the caller's, if they are as long)
+  // what the products read, bf16: the planes; float32: rows of Ep values (the
+  // caller's, if they are as long)
   unsigned char* planes = base + lay.planes;
   if (f32 && g.dlogits && Ep == s.E) planes = reinterpret_cast<unsigned char*>(g.dlogits);
 
@@ -983,10 +926,9 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
     ga.dlogits = g.dlogits;
     if (products && f32 && planes != reinterpret_cast<unsigned char*>(g.dlogits))
       ga.dl_rows = reinterpret_cast<float*>(planes);
-    if (!f32 && g.dw) ga.planes = reinterpret_cast<uint16_t*>(planes);
-    if (!f32 && g.dx) {
-      ga.half = reinterpret_cast<uint16_t*>(base + lay.half);
-      ga.exponents = reinterpret_cast<int*>(base + lay.exps);
+    if (products && !f32) {
+      ga.planes = reinterpret_cast<uint16_t*>(planes);
+      ga.nplanes = g.dw ? 3 : 2;
     }
     ga.zero_line = base + lay.zero;
     ga.bias_part = bias_part;
@@ -1015,8 +957,7 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
   DxArgs xa{};
   if (g.dx && s.T > 0) {
     const bool padded = s.E % (f32 ? 4 : 8) != 0;
-    xa.rows = f32 ? planes : base + lay.half;
-    xa.exponents = reinterpret_cast<const int*>(base + lay.exps);
+    xa.rows = planes;
     xa.w = padded ? base + lay.wpad : static_cast<const unsigned char*>(g.w_router);
     xa.w_pitch = padded ? Ep : s.E;
     xa.E = xa.w_pitch;

@@ -1,0 +1,102 @@
+"""How many bits of dL and of the router matrix reach the router's gradients.
+
+The inputs are made so that no sum rounds: the gates' gradient gives dL exactly
+(pairs of slots w = 1/2^n whose weighted gradients cancel in the mean), and
+every output has one product that is not zero.  What comes out is then known
+bit for bit, and no tolerance is needed.
+"""
+import pytest
+import torch
+
+from mixture_experts_layer_15_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+# experts of every width of a padded row; few tokens (the narrow kernels) and enough for the wide ones
+EXPERTS = [4, 20, 60, 128, 150, 250, 256, 300, 380, 440, 512]
+TOKENS = [1, 45, 8207]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.load_library()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def bf16_randn(*shape, seed):
+    return torch.randn(*shape, generator=gen(seed)).to(torch.bfloat16)
+
+
+def backward(T, d, E, k, idx, w, g, w_router=None, x=None, mask=None, want=("dx",), act=torch.bfloat16):
+    """The outputs of a call with the gates' gradient alone, on the host."""
+    name = "bf16" if act is torch.bfloat16 else "f32"
+    p = B.problem(T, d, E, k, 128, 0, E, name, name)
+    shapes = dict(dlogits=((T, E), torch.float32), dx=((T, d), act), dw_router=((d, E), torch.float32),
+                  dbias=((E,), torch.float32))
+    o = {n: torch.full(shapes[n][0], 7.0, dtype=shapes[n][1], device=DEV) for n in want}
+    dev = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    ws = B.workspace(p, B.MOE_CALL_ROUTE_BACKWARD, DEV)
+    ws.fill_(0xFF)
+    B.moe_route_backward(p, x=dev(x), w_router=dev(w_router), topk_idx=dev(idx), topk_w=dev(w), dtopk_w=dev(g),
+                         token_mask=dev(mask), ws=ws, **o)
+    torch.cuda.synchronize()
+    return {n: t.cpu() for n, t in o.items()}
+
+
+def slots(T, ids, weight):
+    return (torch.tensor(ids, dtype=torch.int32).repeat(T, 1), torch.full((T, len(ids)), weight))
+
+
+@pytest.mark.parametrize("E", EXPERTS)
+@pytest.mark.parametrize("T", TOKENS)
+def test_token_gradient_takes_the_matrix_as_it_is(T, E):
+    """A weight far below its row's largest, which the token's gradient does not meet: dL = (0, 1/2, -1/2, 0 ..),
+    the row (1, 2^-40 m, 0, ..): exactly 2^-41 m, a bfloat16."""
+    d = 128
+    idx, w = slots(T, [1, 2], 0.5)
+    g = torch.tensor([1.0, -1.0]).repeat(T, 1)
+    w_router = bf16_randn(d, E, seed=E)
+    w_router[:, 0] = 1.0
+    w_router[:, 1] = (w_router[:, 1].float() * 2.0 ** -40).to(torch.bfloat16)
+    w_router[:, 2] = 0.0
+    got = backward(T, d, E, 2, idx, w, g, w_router)["dx"]
+    assert torch.equal(got, (w_router[:, 1].float() * 0.5).to(torch.bfloat16).repeat(T, 1))
+
+
+@pytest.mark.parametrize("E", EXPERTS)
+@pytest.mark.parametrize("T", TOKENS)
+def test_token_gradient_keeps_a_small_gradient_beside_a_large_one(T, E):
+    """dL = (2^28, -2^28, 2^-22, -2^-22, 0 ..) on a matrix whose first two and fourth columns are zero."""
+    d = 128
+    idx, w = slots(T, [0, 1, 2, 3], 0.25)
+    g = torch.tensor([2.0 ** 30, -2.0 ** 30, 2.0 ** -20, -2.0 ** -20]).repeat(T, 1)
+    w_router = bf16_randn(d, E, seed=E)
+    w_router[:, [0, 1, 3]] = 0.0
+    got = backward(T, d, E, 4, idx, w, g, w_router)["dx"]
+    assert torch.equal(got, (w_router[:, 2].float() * 2.0 ** -22).to(torch.bfloat16).repeat(T, 1))
+
+
+@pytest.mark.parametrize("E", EXPERTS)
+@pytest.mark.parametrize("T", TOKENS)
+def test_token_gradient_takes_16_bits_of_dl(T, E):
+    """dL values of 16 significant bits times powers of two: each result is the exact product rounded once to
+    bfloat16, so one just behind a tie of bfloat16 goes to its own side."""
+    d = 128
+    idx, w = slots(T, [E - 1, E // 2], 0.5)
+    m = 2 ** 15 + 2 * torch.randint(0, 2 ** 14, (T,), generator=gen(T + E)) + 1
+    m[::3] = 2 ** 15 + 2 ** 7 + 1          # 1 + 2^-8 + 2^-15: up from the tie
+    m[1::3] = 2 ** 15 + 3 * 2 ** 7 - 1     # 1 + 3 2^-8 - 2^-15: down from it
+    v = m.float() * 2.0 ** -15 * 2.0 ** torch.randint(-20, 20, (T,), generator=gen(E)).float()
+    g = torch.stack([2 * v, -2 * v], dim=1)
+    w_router = bf16_randn(d, E, seed=E)
+    w_router[:, E // 2] = 0.0
+    w_router[:, E - 1] = (2.0 ** torch.randint(-9, 9, (d,), generator=gen(d)).float()).to(torch.bfloat16)
+    got = backward(T, d, E, 2, idx, w, g, w_router)["dx"]
+    exact = v.double()[:, None] * w_router[:, E - 1].double()     # 16 bits: a float32
+    assert torch.equal(got, exact.float().to(torch.bfloat16))
