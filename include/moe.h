@@ -409,7 +409,8 @@ typedef struct {
  *    dx[t][c] = sum_e dL[t][e] W_r[c][e],  dw_router[c][e] = sum_t x[t][c] dL[t][e],
  *    dbias[e] = sum_t dL[t][e]
  * (the counts are constants of the gradient, and the selection is piecewise
- * constant: neither has one).  Rows of masked tokens are 0 in dlogits and dx.
+ * constant: neither has one).  Rows of masked tokens are 0 in dlogits and dx
+ * (whatever w_router holds).
  * Slots with an id outside [0, E) are left out of every sum.  N <= 0 leaves
  * the losses' terms out.  Sums are float32; with bf16 activations dx
  * (which is rounded to 8 bits) is formed from dL rounded to 16 significant

@@ -617,6 +617,7 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
       }
       clear_tail<S::L>(row, E, ka.Ep, g);
     }
+    if (a.live && g == 0) a.live[t] = x.keep;
     if (!a.planes) continue;
 #pragma unroll
     for (int pl = 0; pl < 3; ++pl) {

@@ -118,6 +118,7 @@ struct GateGradArgs {
   uint16_t* planes;        // [nplanes][T][Ep] bfloat16 planes whose sum is the gradient, or null
   int nplanes;             // 2 or 3
   float* dl_rows;          // [T][Ep] the gradient, columns from E on zero, or null
+  int* live;               // [T] the mask as integers, or null (without a mask)
   const void* pad_src;     // a matrix [d][E] of act values that is copied to
   void* pad_dst;           // [d][Ep] (zeros behind E), or null
   void* zero_line;         // kZeroLineBytes that the kernel clears

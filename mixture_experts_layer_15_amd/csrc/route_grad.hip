@@ -106,6 +106,25 @@ __device__ __forceinline__ u32x2_t read_tr(uint32_t lds) {
 #endif
 }
 
+// 4 bytes per lane, global -> LDS: lane i's land at lds + 4 i.
+__device__ __forceinline__ void dma4(const void* src, uint32_t lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  uint32_t m0;  // (the instruction takes its LDS address from M0, which is put back)
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "v"(src), "s"(lds)
+      : "memory");
+#else
+  (void)src;
+  (void)lds;
+#endif
+}
+
 // ---- dW_r
 // Tile: BC columns of x by BE experts, the sum over a range of tokens.  Both
 // operands have the summed index (the token) as their slow dimension, so they
@@ -384,6 +403,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void router_dw(DwArgs a) {
 // lie in different banks.
 struct DxArgs {
   const unsigned char* rows;    // dL: bf16 the first two planes of [3][T][Ep], float32 [T][Ep]
+  const int* live;              // [T], 0: a masked token, whose row of dx is zeros; or null
   const unsigned char* w;       // [d][w_pitch], experts behind E not read
   unsigned char* dx;            // [T][d]
   long long T;
@@ -479,6 +499,10 @@ __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned cha
       const long long t = min((s0 + s) * kTokens + r, a.T - 1);
       dma16(a.rows + (pl * a.T + t) * P + c * 16, lds0 + b * kStage + n * 1024);
     }
+    // the tokens' marks go the same way: a load into registers would be waited
+    // for with every store before it
+    if (a.live && w == 0 && l < kTokens)
+      dma4(a.live + min((s0 + s) * kTokens + l, a.T - 1), lds0 + 2 * kStage + b * kTokens * 4);
   };
   load_stage(0, 0);
 
@@ -547,6 +571,12 @@ __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned cha
                   acc[m][n], 0, 0, 0);
         }
       }
+    // A masked token's row of dL is zeros, which an infinity or NaN of the
+    // matrix turns into NaN: its row of dx is not taken from the product.
+    const int* live = reinterpret_cast<const int*>(smem + 2 * kStage) + b * kTokens;
+    bool drop[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) drop[n] = a.live && live[n * 32 + l % 32] == 0;
     wait_lds();
     // kQuad: lane l has 16 MB columns of token l % 32, from column 16 MB h, as
     // kVals 16-byte values.  Transposed within four lanes, these store 64
@@ -574,6 +604,9 @@ __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned cha
           }
         }
       }
+      if (drop[n])
+#pragma unroll
+        for (int i = 0; i < kVals; ++i) o[i] = u32x4_t{0, 0, 0, 0};
       const long long tb = (s0 + s) * kTokens + n * 32;
       if constexpr (kQuad) {
         const long long t = tb + (l % 32 & ~3);
@@ -726,7 +759,7 @@ DwPlan dw_plan(const Shape& s) {
 }
 
 struct GradLayout {
-  size_t zero, planes, wpad, bias, dw, total;
+  size_t zero, planes, live, wpad, bias, dw, total;
 };
 
 GradLayout grad_layout(const Shape& s) {
@@ -746,6 +779,7 @@ GradLayout grad_layout(const Shape& s) {
     L.planes = take((size_t)s.T * Ep * 4);
     L.wpad = take(s.E % 4 != 0 ? (size_t)s.d * Ep * 4 : 0);
   }
+  L.live = take((size_t)s.T * 4);
   L.bias = take((size_t)gate_grad_blocks(s) * s.E * 4);
   const int ns = dw_plan(s).splits;
   L.dw = take(ns > 1 ? (size_t)ns * s.d * s.E * 4 : 0);
@@ -789,7 +823,7 @@ void place_dx(DxArgs& a, int cols, int tokens, int slots) {
   a.t_ranges = (int)((steps + a.steps_per_range - 1) / a.steps_per_range);
 }
 constexpr int dx_lds(bool f32, int KS, int NB) {
-  return 2 * (f32 ? 1 : 2) * 32 * NB * KS * 32;
+  return 2 * 32 * NB * ((f32 ? 1 : 2) * KS * 32 + 4);
 }
 
 template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
@@ -930,6 +964,7 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
       ga.planes = reinterpret_cast<uint16_t*>(planes);
       ga.nplanes = g.dw ? 3 : 2;
     }
+    if (g.dx && g.gate.mask) ga.live = reinterpret_cast<int*>(base + lay.live);
     ga.zero_line = base + lay.zero;
     ga.bias_part = bias_part;
     // rows of the matrix that 16-byte loads cannot take are copied with Ep
@@ -958,6 +993,7 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
   if (g.dx && s.T > 0) {
     const bool padded = s.E % (f32 ? 4 : 8) != 0;
     xa.rows = planes;
+    xa.live = g.gate.mask ? reinterpret_cast<const int*>(base + lay.live) : nullptr;
     xa.w = padded ? base + lay.wpad : static_cast<const unsigned char*>(g.w_router);
     xa.w_pitch = padded ? Ep : s.E;
     xa.E = xa.w_pitch;

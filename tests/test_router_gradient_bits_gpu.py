@@ -100,3 +100,26 @@ def test_token_gradient_takes_16_bits_of_dl(T, E):
     got = backward(T, d, E, 2, idx, w, g, w_router)["dx"]
     exact = v.double()[:, None] * w_router[:, E - 1].double()     # 16 bits: a float32
     assert torch.equal(got, exact.float().to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("act", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("E", EXPERTS)
+@pytest.mark.parametrize("T", [45, 8207])
+def test_masked_rows_are_zero_whatever_the_matrix_holds(T, E, act):
+    """0 times an infinity or NaN of the matrix does not reach a masked token; a kept one's sum is not finite in
+    those columns, and what it is without them in the others."""
+    d = 256
+    idx, w = slots(T, [0, 1], 0.5)
+    g = torch.tensor([2.0, -2.0]).repeat(T, 1)
+    mask = (torch.rand(T, generator=gen(T)) < 0.6).to(torch.uint8)
+    keep = mask.bool()
+    w_router = bf16_randn(d, E, seed=E).to(act)
+    clean = backward(T, d, E, 2, idx, w, g, w_router, mask=mask, act=act)["dx"]
+    bad = w_router.clone()
+    bad[::2, E - 1] = float("inf")
+    bad[1::8, 2] = float("nan")
+    hit = ~torch.isfinite(bad).all(dim=1)
+    got = backward(T, d, E, 2, idx, w, g, bad, mask=mask, act=act)["dx"]
+    assert torch.all(got[~keep] == 0) and torch.all(clean[~keep] == 0)
+    assert not torch.isfinite(got[keep][:, hit]).any()
+    assert torch.equal(got[keep][:, ~hit], clean[keep][:, ~hit])
