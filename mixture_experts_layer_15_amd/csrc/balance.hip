@@ -468,7 +468,7 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
     return;
   }
   const int g = l % S::L, r = l / S::L;
-  const bool losses = a.dlosses != nullptr;
+  bool losses = a.dlosses != nullptr;  // (also N > 0, below)
   const bool gates = a.dtopk_w != nullptr;
   const long long t0 = blockIdx.x * ka.rows_per_block;
   const long long t1 = min(t0 + ka.rows_per_block, ka.T);
@@ -525,7 +525,8 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
 #pragma unroll
     for (int q = 0; q < S::Q; ++q)
       if (S::elem(g, q) < E) cen[q] = (float)((double)cnt[q] * E - mine);  // (an integer below 2^40)
-    if (n > 0) {
+    losses = n > 0;
+    if (losses) {
       ca = (float)(da / ((double)n * n * k));
       cz = (float)(dz * 2.0 / n);
     }
@@ -564,6 +565,9 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
         const float zl = cz * lse;
 #pragma unroll
         for (int q = 0; q < S::Q; ++q) v[q] = v[q] * inv * fmaf(ca, cen[q] - mean, zl);
+      } else {
+#pragma unroll
+        for (int q = 0; q < S::Q; ++q) v[q] = 0.0f;  // (logits, if they were read for N <= 0)
       }
       if (gates) {
         asm volatile("" ::: "memory");

@@ -123,3 +123,26 @@ def test_masked_rows_are_zero_whatever_the_matrix_holds(T, E, act):
     assert torch.all(got[~keep] == 0) and torch.all(clean[~keep] == 0)
     assert not torch.isfinite(got[keep][:, hit]).any()
     assert torch.equal(got[keep][:, ~hit], clean[keep][:, ~hit])
+
+
+@pytest.mark.parametrize("n_tokens", [0, -3])
+@pytest.mark.parametrize("T,E", [(40, 20), (5000, 20), (40, 131), (140000, 4)])
+def test_no_tokens_leave_the_losses_out_whatever_the_logits_hold(T, E, n_tokens):
+    """N <= 0: the gates' gradient alone, also for rows whose logits are NaN or infinite."""
+    k = 2
+    idx, w = slots(T, [0, E - 1], 0.5)
+    g = torch.randn(T, k, generator=gen(T))
+    L = torch.randn(T, E, generator=gen(E))
+    L[::3, 1] = float("nan")
+    L[1::3] = float("inf")
+    p = B.problem(T, 128, E, k, 128, 0, E, "bf16", "bf16")
+    o = {}
+    for losses in (False, True):
+        kw = dict(logits=L.to(DEV), counts=torch.full((E,), 7, dtype=torch.int32, device=DEV),
+                  n_tokens=torch.tensor([n_tokens], dtype=torch.int32, device=DEV),
+                  dlosses=torch.tensor([1.0, 1.0], device=DEV)) if losses else {}
+        o[losses] = torch.full((T, E), 7.0, device=DEV)
+        B.moe_route_backward(p, topk_idx=idx.to(DEV), topk_w=w.to(DEV), dtopk_w=g.to(DEV), dlogits=o[losses],
+                             ws=B.workspace(p, B.MOE_CALL_ROUTE_BACKWARD, DEV), **kw)
+    torch.cuda.synchronize()
+    assert torch.isfinite(o[False]).all() and torch.equal(o[True], o[False])
