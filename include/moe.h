@@ -457,16 +457,18 @@ size_t moe_grad_workspace_size(const moe_grad_t* g, int32_t n);
 /* moe_grad_norm - *norm = sqrt(sum over all values of g^2), summed in
  * float64 in a fixed order and rounded to float32; 0 for an empty list.
  *  g: host array, read before the call returns (the list travels with the
- *  launches).  norm: device float32.  Ranks that hold different parts of a
- *  model's gradients join their norms as the root of the sum of squares. */
+ *  launches).  norm: device float32, in no tensor of the list.  Ranks that
+ *  hold different parts of a model's gradients join their norms as the root
+ *  of the sum of squares. */
 moe_status_t moe_grad_norm(const moe_grad_t* g, int32_t n, float* norm, void* ws, size_t ws_bytes,
                            void* stream);
 
 /* moe_grad_clip - with v = *norm (device float32, of these or of more
- * tensors): out = grad * (max_norm / v) if max_norm < v < inf, else out = grad
- * (a norm that is not finite changes nothing: the caller sees it in *norm and
- * skips the step).  The scale and the product are float32, rounded once more
- * for bf16.  max_norm > 0 (inf clips nothing). */
+ * tensors; in no output of the list): out = grad * (max_norm / v) if
+ * max_norm < v < inf, else out = grad (a norm that is not finite changes
+ * nothing: the caller sees it in *norm and skips the step).  The scale and the
+ * product are float32, rounded once more for bf16.  max_norm > 0 (inf clips
+ * nothing). */
 moe_status_t moe_grad_clip(const moe_grad_t* g, int32_t n, const float* norm, float max_norm,
                            void* stream);
 

@@ -108,6 +108,19 @@ moe_status_t check_grads(const moe_grad_t* g, int32_t n, bool outputs) {
   return MOE_OK;
 }
 
+// Whether the norm's word lies in a tensor of the list (`outputs`: in one that
+// clipping writes, which other workgroups would still read it from).
+bool norm_in_list(const moe_grad_t* g, int32_t n, const float* norm, bool outputs) {
+  const uintptr_t v = reinterpret_cast<uintptr_t>(norm);
+  for (int i = 0; i < n; ++i) {
+    if (g[i].numel == 0) continue;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(outputs ? g[i].out : g[i].grad);
+    const uintptr_t e = b + (g[i].dtype == MOE_F32 ? 4 : 2) * (uintptr_t)g[i].numel;
+    if (v < e && v + sizeof(float) > b) return true;
+  }
+  return false;
+}
+
 // Device-memory layout of the moe_forward workspace.
 struct ForwardLayout {
   size_t logits, idx, w, counts, offsets, sorted, pos, y, router, permute, ffn, total;
@@ -388,6 +401,7 @@ moe_status_t moe_grad_norm(const moe_grad_t* g, int32_t n, float* norm, void* ws
   if (norm == nullptr || reinterpret_cast<uintptr_t>(norm) % 4 != 0 || !aligned16(ws))
     return MOE_ERR_INVALID_ARGUMENT;
   if (ws == nullptr || ws_bytes < moe::grad_ws_bytes(g, n)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (norm_in_list(g, n, norm, false)) return MOE_ERR_INVALID_ARGUMENT;
   return from_hip(moe::grad_norm(g, n, norm, ws, static_cast<hipStream_t>(stream)));
 }
 
@@ -397,7 +411,7 @@ moe_status_t moe_grad_clip(const moe_grad_t* g, int32_t n, const float* norm, fl
   if (st != MOE_OK) return st;
   if (norm == nullptr || reinterpret_cast<uintptr_t>(norm) % 4 != 0)
     return MOE_ERR_INVALID_ARGUMENT;
-  if (!(max_norm > 0.0f)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!(max_norm > 0.0f) || norm_in_list(g, n, norm, true)) return MOE_ERR_INVALID_ARGUMENT;
   return from_hip(moe::grad_clip(g, n, norm, max_norm, static_cast<hipStream_t>(stream)));
 }
 
