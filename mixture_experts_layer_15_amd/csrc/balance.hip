@@ -23,24 +23,20 @@
 // 16 logits each: the fewer lanes a row has, the fewer steps its maximum and
 // sum take, and the several rows of a wave share each step; L is at least
 // four where E allows, so that a load covers 64 consecutive bytes of a row.
-#include <algorithm>
-
 #include "moe_device.h"
 #include "moe_internal.h"
+#include "route_plan.h"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;      // of the balance loss
+constexpr int kThreads = kBalanceThreads;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kMaxRowBlocks = 512;
-constexpr int kGradThreads = 256;  // of the gradient
+constexpr int kGradThreads = kGateThreads;
 constexpr int kGradWaves = kGradThreads / kWave;
-constexpr int kMaxGradBlocks = 512;
-constexpr int kSoloPasses = 4;
+static_assert(kRowWave == kWave, "lanes of a wave");
 
-// A row of E logits on L lanes: lane g holds elements (c L + g) V + v,
-// c < C, v < V (V = 4: 16-byte loads, E a multiple of 4).
+// A RowGeom as a type.
 template <int V_, int L_, int C_>
 struct RowShape {
   static constexpr int V = V_, L = L_, C = C_;
@@ -49,45 +45,25 @@ struct RowShape {
   __device__ static int elem(int g, int q) { return ((q / V) * L + g) * V + q % V; }
 };
 
-template <class F>
-void with_row_shape(int E, F f) {
-  if (E % 4 == 0) {
-    if (E <= 4) return f(RowShape<4, 1, 1>{});
-    if (E <= 8) return f(RowShape<4, 2, 1>{});
-    if (E <= 16) return f(RowShape<4, 4, 1>{});
-    if (E <= 32) return f(RowShape<4, 4, 2>{});
-    if (E <= 64) return f(RowShape<4, 4, 4>{});
-    if (E <= 128) return f(RowShape<4, 8, 4>{});
-    if (E <= 256) return f(RowShape<4, 16, 4>{});
-    return f(RowShape<4, 32, 4>{});
-  }
-  if (E <= 4) return f(RowShape<1, 4, 1>{});
-  if (E <= 16) return f(RowShape<1, 16, 1>{});
-  if (E <= 32) return f(RowShape<1, 16, 2>{});
-  if (E <= 64) return f(RowShape<1, 16, 4>{});
-  if (E <= 128) return f(RowShape<1, 16, 8>{});
-  if (E <= 256) return f(RowShape<1, 16, 16>{});
-  return f(RowShape<1, 32, 16>{});
+template <int V, int L, int C, class F>
+bool if_geom(const RowGeom& g, F& f) {
+  if (g.V != V || g.L != L || g.C != C) return false;
+  f(RowShape<V, L, C>{});
+  return true;
 }
 
-// The gradient's row shapes for few rows: more lanes a row, so that the rows
-// spread over more compute units and a lane stores less.
+// Calls f with the shape of a geometry that row_geom or wide_row_geom gives.
 template <class F>
-void with_wide_row_shape(int E, F f) {
-  if (E % 4 == 0) {
-    if (E <= 16) return with_row_shape(E, f);
-    if (E <= 32) return f(RowShape<4, 8, 1>{});
-    if (E <= 64) return f(RowShape<4, 16, 1>{});
-    if (E <= 128) return f(RowShape<4, 32, 1>{});
-    if (E <= 256) return f(RowShape<4, 64, 1>{});
-    return f(RowShape<4, 64, 2>{});
-  }
-  if (E <= 16) return with_row_shape(E, f);
-  if (E <= 32) return f(RowShape<1, 32, 1>{});
-  if (E <= 64) return f(RowShape<1, 64, 1>{});
-  if (E <= 128) return f(RowShape<1, 64, 2>{});
-  if (E <= 256) return f(RowShape<1, 64, 4>{});
-  return f(RowShape<1, 64, 8>{});
+void with_row_shape(const RowGeom& g, F f) {
+  (void)(if_geom<4, 1, 1>(g, f) || if_geom<4, 2, 1>(g, f) || if_geom<4, 4, 1>(g, f) ||
+         if_geom<4, 4, 2>(g, f) || if_geom<4, 4, 4>(g, f) || if_geom<4, 8, 4>(g, f) ||
+         if_geom<4, 16, 4>(g, f) || if_geom<4, 32, 4>(g, f) || if_geom<4, 8, 1>(g, f) ||
+         if_geom<4, 16, 1>(g, f) || if_geom<4, 32, 1>(g, f) || if_geom<4, 64, 1>(g, f) ||
+         if_geom<4, 64, 2>(g, f) || if_geom<1, 4, 1>(g, f) || if_geom<1, 16, 1>(g, f) ||
+         if_geom<1, 16, 2>(g, f) || if_geom<1, 16, 4>(g, f) || if_geom<1, 16, 8>(g, f) ||
+         if_geom<1, 16, 16>(g, f) || if_geom<1, 32, 16>(g, f) || if_geom<1, 32, 1>(g, f) ||
+         if_geom<1, 64, 1>(g, f) || if_geom<1, 64, 2>(g, f) || if_geom<1, 64, 4>(g, f) ||
+         if_geom<1, 64, 8>(g, f));
 }
 
 template <class S>
@@ -652,62 +628,6 @@ __global__ __launch_bounds__(kGradThreads) void gate_grad_rows(GateGradKernelArg
     a.bias_part[(size_t)blockIdx.x * E + e] = (float)col_total<kGradWaves>(red, E, e);
 }
 
-// Workgroups of a row kernel that passes over `pass` rows at a time: whole
-// passes, as many workgroups as there are passes up to `most`.
-int row_blocks(long long T, long long pass, int most, long long* rows_per_block) {
-  const long long passes = std::max<long long>((T + pass - 1) / pass, 1);
-  const long long each = (passes + most - 1) / most;
-  *rows_per_block = each * pass;
-  return (int)((passes + each - 1) / each);
-}
-
-// The balance loss: up to four passes one workgroup makes them all, in one
-// launch (256 tokens of 128, a call among others: 8.4 us, in two kernels
-// 11.5 us; at eight passes, 1000 tokens of 64, 12.8 against 11.6 us).  Below
-// 64 passes the wide shape spreads the rows (the two kernels together: 1000
-// tokens of 64, 10.5 us, wide 7.8 us; 2048 of 128, 10.3 and 8.9 us; 8192 of
-// 128, which are 128 passes, 10.8 and 11.1 us).
-long long balance_pass(const Shape& s) {
-  long long pass = 0;
-  with_row_shape(s.E, [&](auto sh) { pass = kWaves * decltype(sh)::R; });
-  return pass;
-}
-template <class F>
-void with_balance_shape(const Shape& s, F f) {
-  const long long pass = balance_pass(s);
-  if (s.T > kSoloPasses * pass && s.T < 64 * pass) return with_wide_row_shape(s.E, f);
-  return with_row_shape(s.E, f);
-}
-int balance_blocks(const Shape& s, long long* rows) {
-  long long pass = balance_pass(s);
-  if (s.T <= kSoloPasses * pass) {
-    *rows = kSoloPasses * pass;
-    return 1;
-  }
-  with_balance_shape(s, [&](auto sh) { pass = kWaves * decltype(sh)::R; });
-  // Rows of 16-byte loads: one workgroup a compute unit, with half the partial
-  // sums to add (32768 tokens of 128: both kernels 13.4 us, 16.5 us with 512
-  // workgroups; 131072 of 256: 34.8 and 35.4 us); of 4-byte loads two (65536
-  // tokens of 511: 35.6 us, 39.2 us with 256).
-  return row_blocks(s.T, pass, s.E % 4 == 0 ? 256 : kMaxRowBlocks, rows);
-}
-
-// Calls f with the gradient's row shape: the wide one up to 512 passes of the
-// other (2048 tokens, E = 64: 7.6 us, wide 4.8 us; 8192, E = 128: 10.7 and
-// 9.6 us; 16384, E = 256, 1024 passes: 16.8 and 21.2 us).
-template <class F>
-void with_grad_shape(const Shape& s, F f) {
-  long long pass = 0;
-  with_row_shape(s.E, [&](auto sh) { pass = kGradWaves * decltype(sh)::R; });
-  if (s.T < 512 * pass) return with_wide_row_shape(s.E, f);
-  return with_row_shape(s.E, f);
-}
-int grad_blocks(const Shape& s, long long* rows) {
-  long long pass = 0;
-  with_grad_shape(s, [&](auto sh) { pass = kGradWaves * decltype(sh)::R; });
-  return row_blocks(s.T, pass, kMaxGradBlocks, rows);
-}
-
 struct BalanceLayout {
   size_t part, zpart, npart, joined, total;
 };
@@ -715,7 +635,7 @@ struct BalanceLayout {
 BalanceLayout balance_layout(const Shape& s) {
   BalanceLayout L{};
   long long rows;
-  const int nb = balance_blocks(s, &rows);
+  const int nb = balance_blocks(s.T, s.E, &rows);
   size_t o = 0;
   auto take = [&o](size_t bytes) {
     const size_t at = o;
@@ -746,7 +666,7 @@ hipError_t balance_loss(const Shape& s, const float* logits, const int32_t* topk
   a.T = s.T;
   a.E = s.E;
   a.k = s.k;
-  a.nb = balance_blocks(s, &a.rows_per_block);
+  a.nb = balance_blocks(s.T, s.E, &a.rows_per_block);
   a.part = reinterpret_cast<ColPart*>(base + lay.part);
   a.zpart = reinterpret_cast<double*>(base + lay.zpart);
   a.npart = reinterpret_cast<int*>(base + lay.npart);
@@ -755,7 +675,7 @@ hipError_t balance_loss(const Shape& s, const float* logits, const int32_t* topk
   a.n_tokens = n_tokens;
   a.prob_mean = prob_mean;
   a.losses = losses;
-  with_balance_shape(s, [&](auto sh) {
+  with_row_shape(balance_geom(s.T, s.E), [&](auto sh) {
     using S = decltype(sh);
     if (a.nb == 1)
       hipLaunchKernelGGL((balance_rows<S, true>), dim3(1), dim3(kThreads), 0, st, a);
@@ -771,7 +691,7 @@ hipError_t balance_loss(const Shape& s, const float* logits, const int32_t* topk
 
 int gate_grad_blocks(const Shape& s) {
   long long rows;
-  return grad_blocks(s, &rows);
+  return gate_blocks(s.T, s.E, &rows);
 }
 
 hipError_t gate_grad(const Shape& s, const GateGradArgs& a, int Ep, hipStream_t st) {
@@ -781,10 +701,10 @@ hipError_t gate_grad(const Shape& s, const GateGradArgs& a, int Ep, hipStream_t 
   ka.E = s.E;
   ka.k = s.k;
   ka.Ep = Ep;
-  ka.blocks = grad_blocks(s, &ka.rows_per_block);
+  ka.blocks = gate_blocks(s.T, s.E, &ka.rows_per_block);
   ka.act_bytes = act_bytes(s);
   const int nb = ka.blocks + (a.pad_src ? s.d / kGradWaves : 0);
-  with_grad_shape(s, [&](auto sh) {
+  with_row_shape(gate_geom(s.T, s.E), [&](auto sh) {
     using S = decltype(sh);
     hipLaunchKernelGGL((gate_grad_rows<S>), dim3(nb), dim3(kGradThreads), 0, st, ka);
   });

@@ -17,11 +17,11 @@
 // float32 activations: the same kernels on the float32 matrix instructions,
 // with dL as it is.
 #include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 #include "moe_device.h"
 #include "moe_internal.h"
+#include "route_plan.h"
 
 namespace moe {
 namespace {
@@ -137,8 +137,6 @@ __device__ __forceinline__ void dma4(const void* src, uint32_t lds) {
 // operands of x, so a wave is taller in columns of x than in experts: LDS
 // bandwidth bounds it otherwise.  The waves are WC x WE, times KG groups that
 // take every KG-th step of 16 tokens and are added at the end.
-constexpr int kSegment = 16384;  // tokens whose mask bits are held in LDS
-
 template <bool kF32, int kRowBytes>
 __device__ __forceinline__ int tr_swz(int t) {
   if constexpr (kF32) return 0;  // plain reads: a lane a value, consecutive lanes
@@ -704,59 +702,7 @@ __global__ __launch_bounds__(kSumThreads) void router_grad_sum(SumArgs a) {
   }
 }
 
-// Experts in a row of the planes: the steps that router_dx_bf16 is made for.
-int padded_experts(const Shape& s) { return s.E <= 32 ? 32 : (s.E + 63) / 64 * 64; }
-
-// Plan of the dW_r kernel: its tile, and the parts of the token range.
-struct DwPlan {
-  int bc, be;
-  int splits;
-};
-
-// One workgroup fits a compute unit.  A part costs the rounds of workgroups
-// over the 256 compute units times (start and end of a workgroup, 4 us, plus
-// its tokens at the measured time each), plus its partial sums, written and
-// read at 4 TB/s.  The tall tiles have the better rate on many tokens of wide
-// rows but need that many more parts to fill the chip.  Measured, 16384
-// tokens of 7168: E = 256, 256 x 128 tiles 168 us, 128 x 128 198 us; E = 64,
-// 256 x 64 59 us, 128 x 64 67 us; E = 8, 256 x 32 44 us, 128 x 32 48 us
-// (5.3 TB/s of x).  8192 tokens of 2048, E = 128: 256 x 128 22.0 us with 32
-// parts, 128 x 128 18.8 us with 16.
-double dw_cost(const Shape& s, int bc, int be, double ns_token, int splits) {
-  const double tiles = (double)((s.d + bc - 1) / bc) * ((s.E + be - 1) / be);
-  const double rounds = std::ceil(tiles * splits / 256.0);
-  const double tokens = std::ceil((double)s.T / splits / 64.0) * 64.0;
-  return rounds * (4000.0 + tokens * ns_token) +
-         (splits > 1 ? 2.0 * splits * s.d * s.E * 4 / 4000.0 : 0.0);
-}
-
-DwPlan dw_plan(const Shape& s) {
-  DwPlan best{128, 32, 1};
-  double cost = -1.0;
-  auto offer = [&](int bc, int be, double ns_token) {
-    // (the plan is made several times a call: few candidates)
-    for (const int n : {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 18, 20, 24, 28, 32, 40, 48, 64}) {
-      if (n > 1 && (long long)n * 64 > s.T + 63) break;
-      const double c = dw_cost(s, bc, be, ns_token, n);
-      if (cost < 0 || c < cost) {
-        cost = c;
-        best = DwPlan{bc, be, n};
-      }
-    }
-  };
-  const bool bf16 = s.act == kBF16;
-  if (s.E <= 32) {
-    offer(128, 32, bf16 ? 12.0 : 22.0);
-    if (bf16) offer(256, 32, 22.0);
-  } else if (s.E <= 64) {
-    offer(128, 64, bf16 ? 17.0 : 30.0);
-    if (bf16) offer(256, 64, 30.0);
-  } else {
-    offer(128, 128, bf16 ? 25.0 : 60.0);
-    if (bf16) offer(256, 128, 44.0);
-  }
-  return best;
-}
+DwPlan plan_of(const Shape& s) { return dw_plan(s.T, s.d, s.E, s.act == kBF16); }
 
 struct GradLayout {
   size_t zero, planes, live, wpad, bias, dw, total;
@@ -770,7 +716,7 @@ GradLayout grad_layout(const Shape& s) {
     o += align_up(bytes);
     return at;
   };
-  const int Ep = padded_experts(s);
+  const int Ep = padded_experts(s.E);
   L.zero = take(kZeroLineBytes);
   if (s.act == kBF16) {
     L.planes = take((size_t)3 * s.T * Ep * 2);
@@ -781,7 +727,7 @@ GradLayout grad_layout(const Shape& s) {
   }
   L.live = take((size_t)s.T * 4);
   L.bias = take((size_t)gate_grad_blocks(s) * s.E * 4);
-  const int ns = dw_plan(s).splits;
+  const int ns = plan_of(s).splits;
   L.dw = take(ns > 1 ? (size_t)ns * s.d * s.E * 4 : 0);
   L.total = o;
   return L;
@@ -791,7 +737,7 @@ template <class C>
 void place_dw(DwArgs& a) {
   a.c_tiles = (a.d + C::BC - 1) / C::BC;
   a.e_tiles = (a.E + C::BE - 1) / C::BE;
-  a.t_per_split = ((a.T + a.splits - 1) / a.splits + 63) / 64 * 64;
+  a.t_per_split = dw_tokens_per_split(a.T, a.splits);
 }
 template <class C>
 int dw_lds(const DwArgs& a) {
@@ -842,17 +788,10 @@ hipError_t launch_dx_as(DxArgs a, hipStream_t st) {
 }
 
 // The variant for KS steps: a wave's share of the matrix takes 4 MB KS
-// registers, a stage 32 NB x 32 KS bytes of LDS a plane.  (With 256 experts, 64 tokens
-// a stage leave no registers for the transposition of the stores, with more no
-// LDS.)  For few tokens one of 128
-// columns and 32 tokens a workgroup (one token of 4096 x 128, float32: 6.2 us,
-// 23.8 us wide).
-bool few_tokens(const Shape& s) {
-  // workgroups of 512 columns and 64 tokens for less than half of the compute
-  // units
-  return (long long)((s.d + 511) / 512) * ((s.T + 63) / 64) < 128;
-}
-
+// registers, a stage 32 NB x 32 KS bytes of LDS a plane.  (From 256 experts on,
+// 64 tokens a stage leave no registers for the transposition of the stores, or
+// no LDS.)  For few tokens one of 128 columns and 32 tokens a workgroup (one
+// token of 4096 x 128, float32: 6.2 us, 23.8 us wide).
 template <bool kF32, int MB, int KS, int NB, int NW, int kMinWaves>
 hipError_t launch_dx_for(const DxArgs& a, bool few, hipStream_t st) {
   if (few) return launch_dx_as<kF32, 1, KS, 1, 4, 1>(a, st);
@@ -941,8 +880,8 @@ size_t route_backward_ws_bytes(const Shape& s) { return grad_layout(s).total; }
 hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipStream_t st) {
   unsigned char* base = static_cast<unsigned char*>(ws);
   const GradLayout lay = grad_layout(s);
-  const int Ep = padded_experts(s);
-  const DwPlan plan = dw_plan(s);
+  const int Ep = padded_experts(s.E);
+  const DwPlan plan = plan_of(s);
   const int ns = plan.splits;
   const bool f32 = s.act != kBF16;
   const bool products = s.T > 0 && (g.dw || g.dx);
@@ -1001,11 +940,8 @@ hipError_t route_backward(const Shape& s, const RouteGradArgs& g, void* ws, hipS
     xa.T = s.T;
     xa.d = s.d;
   }
-  // few tokens: both products in one launch (a launch less, and the narrow
-  // grids side by side)
-  const bool few = few_tokens(s);
-  // (float32 rows of more than 256 experts leave eight waves no registers)
-  const bool both = products && g.dw && g.dx && few && plan.bc == 128 && (!f32 || Ep <= 256);
+  const bool few = few_tokens(s.T, s.d);
+  const bool both = products && g.dw && g.dx && products_in_one_launch(s.T, s.d, s.E, !f32);
   hipError_t e = hipSuccess;
   if (both) {
     e = f32 ? launch_products<true, 8>(wa, xa, Ep, st) : launch_products<false, 4>(wa, xa, Ep, st);
