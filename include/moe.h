@@ -369,7 +369,9 @@ moe_status_t moe_eplb_remap(int32_t T, int32_t k, int32_t E, int32_t G, const in
  * All zero for N = 0 (T = 0 included).  Ids outside [0, E) are not counted;
  * an id that a row names twice counts twice.  -inf logits have p = 0; a row
  * of -inf only adds nothing to prob_mean and losses[1]; a NaN or +inf logit
- * of a kept token makes prob_mean and the losses NaN.
+ * of a kept token makes prob_mean and the losses NaN.  losses[0], at least
+ * 1 / (k E) with the ids of each row's largest logits, is summed in steps of
+ * 2^-48.
  *  logits [T][E], topk_idx [T][k]: as written by moe_route.
  *  counts [E] int32, n_tokens [1] int32 (N), prob_mean [E] float32,
  *  losses [2] float32: outputs, all required.  Ranks that share a batch add

@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
   // slots per expert: integer sums, so the order of the atomics is free
   const long long slots = (long long)rows * a.k;
   for (long long s = tid; s < slots; s += kThreads) {
-    if (mask && mask[slots < (1LL << 31) ? (uint32_t)s / (uint32_t)a.k : s / a.k] == 0) continue;
+    if (mask && mask[(uint32_t)s / (uint32_t)a.k] == 0) continue;  // (T k < 2^31)
     const int e = idx[s];
     if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
   }
@@ -293,7 +293,9 @@ __global__ __launch_bounds__(kThreads) void balance_rows(BalanceArgs a) {
 // abreast, in a fixed order.  The workgroups' shares of the balance loss meet
 // in one 64-bit atomic: arrivals in the top six bits (at most 32 workgroups),
 // below them the sum in fixed point, 48 bits behind the point (the loss is at
-// most E = 512).  An integer sum has no order, and the last to arrive has it
+// most E = 512; with the ids of each row's largest logits it is at least
+// 1 / (k E) >= 2^-18, so that 32 halves of 2^-48 are below a float32's half
+// step).  An integer sum has no order, and the last to arrive has it
 // from the atomic itself, without a fence (which cost 2 us).
 constexpr int kFinThreads = 1024;
 constexpr int kFinCols = 16;

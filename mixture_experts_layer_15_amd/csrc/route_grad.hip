@@ -95,8 +95,8 @@ __device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
 // address of four 16-bit values of row j / 4, columns 4 (j % 4) .. + 3, and
 // gets column j of the four rows.
 __device__ __forceinline__ u32x2_t read_tr(uint32_t lds) {
-  typedef short s16x4_t __attribute__((ext_vector_type(4)));
 #if defined(__HIP_DEVICE_COMPILE__)
+  typedef short s16x4_t __attribute__((ext_vector_type(4)));
   return __builtin_bit_cast(
       u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                    (__attribute__((address_space(3))) s16x4_t*)(uintptr_t)lds));
