@@ -581,7 +581,7 @@ __device__ __forceinline__ void dx_tile(const DxArgs& a, int block, unsigned cha
     // consecutive bytes of one token, in four stores of the lanes' four
     // tokens: whole pieces of a line, which may stream past the caches (16384
     // tokens of 7168 x 8: the whole call 134 us, with 32-byte pieces, 128 us
-    // with 64-byte ones, 108 us streaming; 32-byte pieces streaming are five
+    // with 64-byte ones, 106 us streaming; 32-byte pieces streaming are five
     // times slower).
     constexpr int kVals = MB * kSize;
 #pragma unroll

@@ -123,11 +123,11 @@ struct DwPlan {
 // over the 256 compute units times (start and end of a workgroup, 4 us, plus
 // its tokens at the measured time each), plus its partial sums, written and
 // read at 4 TB/s.  The tall tiles have the better rate on many tokens of wide
-// rows but need that many more parts to fill the chip.  Measured, 16384
-// tokens of 7168: E = 256, 256 x 128 tiles 168 us, 128 x 128 198 us; E = 64,
-// 256 x 64 59 us, 128 x 64 67 us; E = 8, 256 x 32 44 us, 128 x 32 48 us
-// (5.3 TB/s of x).  8192 tokens of 2048, E = 128: 256 x 128 22.0 us with 32
-// parts, 128 x 128 18.8 us with 16.
+// rows but need that many more parts to fill the chip.  Measured, 24 launches
+// over 12 sets of tokens, twice: 16384 tokens of 7168, E = 256, 256 x 128 tiles
+// 177 and 214 us, 128 x 128 200 and 222 us; E = 64, 256 x 64 60 us, 128 x 64 73
+// to 75 us; E = 8, 256 x 32 43 us, 128 x 32 48 us (5.4 TB/s of x).  8192 tokens
+// of 2048, E = 128: 256 x 128 23.5 us with 32 parts, 128 x 128 21 us with 16.
 inline double dw_cost(long long T, int d, int E, int bc, int be, double ns_token, int splits) {
   const double tiles = (double)((d + bc - 1) / bc) * ((E + be - 1) / be);
   const double rounds = std::ceil(tiles * splits / 256.0);
