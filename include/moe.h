@@ -123,7 +123,9 @@ typedef enum {
   MOE_CALL_FORWARD = 2,
   MOE_CALL_ROUTE = 3,
   MOE_CALL_BALANCE_LOSS = 4,
-  MOE_CALL_ROUTE_BACKWARD = 5
+  MOE_CALL_ROUTE_BACKWARD = 5,
+  MOE_CALL_NORM_BACKWARD = 6,
+  MOE_CALL_COMBINE_NORM_BACKWARD = 7
 } moe_call_t;
 
 /* Layout of the expert weight matrices. */
@@ -473,6 +475,106 @@ moe_status_t moe_grad_norm(const moe_grad_t* g, int32_t n, float* norm, void* ws
  * nothing). */
 moe_status_t moe_grad_clip(const moe_grad_t* g, int32_t n, const float* norm, float max_norm,
                            void* stream);
+
+/* ---- Norms around the layer ----
+ *
+ * A transformer block normalises what it feeds to the layer and adds what
+ * comes back to its residual stream; "What is an MoE layer?" puts the layer in
+ * the place of such a block's feed-forward network.  The pages give no
+ * formula; this is the root-mean-square norm (Zhang and Sennrich 2019) before
+ * the layer, and after it one more with an optional gate per channel and a
+ * residual scale, joined to the combine.  With r(v) = 1 / sqrt(mean_c(v[c]^2)
+ * + eps) over the d columns of a row:
+ *    moe_norm:          x = h r(h) weight
+ *    moe_combine_norm:  c = moe_combine's sum, in float32
+ *                       out = res_scale h + gate (c r(c) weight)
+ *                       next_x = out r(out) next_weight   (out as stored)
+ * The calls check that every array is 16-byte aligned.  weight, gate and
+ * their gradients are float32 [d].  Of p, only T, d, act and (in the combine)
+ * k matter (the rest must be valid).  Sums are float32, so a row whose squares
+ * leave the float32 range is outside the contract; values are rounded once,
+ * where they are stored.  eps > 0.  A row of zeros gives zeros.
+ *
+ * moe_norm
+ *  h [T][d] act; x [T][d] act output, may be h; rstd [T] float32 output r, or
+ *  NULL. */
+moe_status_t moe_norm(const moe_problem_t* p, const void* h, const float* weight, float eps,
+                      void* x, float* rstd, void* stream);
+
+/* Arguments of moe_norm_backward.  dh or dweight is given. */
+typedef struct {
+  const void* dx;      /* [T][d] act: gradient of x */
+  const void* h;       /* [T][d] act */
+  const float* weight; /* [d] */
+  const float* rstd;   /* [T] as written by the forward call */
+  const void* dout;    /* [T][d] act, or NULL: gradient that reaches h beside the norm */
+  void* dh;            /* [T][d] act output or NULL; may be dx or dout, not h */
+  float* dweight;      /* [d] float32 output or NULL */
+  float res_scale;     /* factor of dout */
+} moe_norm_backward_args_t;
+
+/* moe_norm_backward - with n = h r and u = dx weight:
+ *    dh = r (u - n mean_c(n u)) + res_scale dout,   dweight = sum_t dx n
+ * (dout: the gradient of moe_combine_norm's out, whose residual h is).  T = 0
+ * writes zeros to dweight.
+ *  ws, ws_bytes: scratch of moe_workspace_size(p, MOE_CALL_NORM_BACKWARD). */
+moe_status_t moe_norm_backward(const moe_problem_t* p, const moe_norm_backward_args_t* a, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* Arguments of moe_combine_norm. */
+typedef struct {
+  const void* y;            /* [T*k][d] act, expert rows */
+  const int32_t* slot_pos;  /* [T*k] as written by moe_permute, or NULL: k = 1 and
+                               row t of y is token t's (the output of moe_combine,
+                               of a rank exchange or of a dense block) */
+  const float* topk_w;      /* [T*k] gates, or NULL (y already weighted) */
+  const void* h;            /* [T][d] act: the residual */
+  const float* weight;      /* [d] */
+  const float* gate;        /* [d] or NULL (1) */
+  void* out;                /* [T][d] act output; may be h */
+  float* rstd;              /* [T] output r(c), or NULL */
+  const float* next_weight; /* [d], or NULL: no next norm */
+  void* next_x;             /* [T][d] act output (with next_weight) */
+  float* next_rstd;         /* [T] output r(out), or NULL */
+  float eps;                /* of both norms */
+  float res_scale;
+} moe_combine_norm_args_t;
+
+/* moe_combine_norm - see above.  The norm is that of the whole sum: on an
+ * expert-parallel rank run moe_combine, add the ranks' sums, and call this
+ * with slot_pos NULL.  A token with no kept slot gets res_scale h.  A slot_pos
+ * outside [0, T*k) means not kept. */
+moe_status_t moe_combine_norm(const moe_problem_t* p, const moe_combine_norm_args_t* a,
+                              void* stream);
+
+/* Arguments of moe_combine_norm_backward.  At least one output is given. */
+typedef struct {
+  const void* dout;        /* [T][d] act: gradient of out (that of next_x included:
+                              moe_norm_backward with out as its h) */
+  const void* y;           /* [T*k][d] act */
+  const int32_t* slot_pos; /* [T*k], or NULL as above */
+  const float* topk_w;     /* [T*k] or NULL */
+  const float* weight;     /* [d] */
+  const float* rstd;       /* [T] as written by the forward call */
+  const float* gate;       /* [d] or NULL */
+  void* dy;                /* [T*k][d] act output or NULL; not y or dout */
+  float* dtopk_w;          /* [T*k] float32 output or NULL (NULL without slot_pos) */
+  float* dweight;          /* [d] float32 output or NULL */
+  float* dgate;            /* [d] float32 output or NULL */
+} moe_combine_norm_backward_args_t;
+
+/* moe_combine_norm_backward - with n = c r, u = weight gate dout:
+ *    dc = r (u - n mean_c(n u)),  dy[slot_pos[s]] = (topk_w ? topk_w[s] : 1) dc[t]
+ *    dtopk_w[s] = sum_c dc[t][c] y[slot_pos[s]][c]
+ *    dweight = gate sum_t dout n,  dgate = weight sum_t dout n
+ * (the residual's gradient is res_scale dout: moe_norm_backward adds it).
+ * dtopk_w is 0 at slots that are not kept; rows of dy that no kept slot names
+ * are not written.  T = 0 writes zeros to dweight and dgate.
+ *  ws, ws_bytes: scratch of
+ *           moe_workspace_size(p, MOE_CALL_COMBINE_NORM_BACKWARD). */
+moe_status_t moe_combine_norm_backward(const moe_problem_t* p,
+                                       const moe_combine_norm_backward_args_t* a, void* ws,
+                                       size_t ws_bytes, void* stream);
 
 /* Blocked weight layout (for callers that convert weights once at load
  * time): each expert matrix [Nout][K] is stored as [Nout/32][K/64] units of

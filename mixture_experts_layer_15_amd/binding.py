@@ -23,6 +23,7 @@ MOE_OK, MOE_ERR_INVALID_ARGUMENT, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE_TOO_SMA
 MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_MXFP4 = range(4)
 MOE_CALL_PERMUTE, MOE_CALL_EXPERT_FFN, MOE_CALL_FORWARD, MOE_CALL_ROUTE = range(4)
 MOE_CALL_BALANCE_LOSS, MOE_CALL_ROUTE_BACKWARD = 4, 5
+MOE_CALL_NORM_BACKWARD, MOE_CALL_COMBINE_NORM_BACKWARD = 6, 7
 MOE_GRAD_MAX_TENSORS = 4096   # include/moe.h
 MOE_FORWARD_EVENTS = 7
 MOE_LAYOUT_ROWS, MOE_LAYOUT_BLOCKED = range(2)
@@ -54,6 +55,23 @@ class RouteBackwardArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("x", "w_router", "logits", "topk_idx", "topk_w", "dtopk_w", "token_mask",
                  "counts", "n_tokens", "dlosses", "dlogits", "dx", "dw_router", "dbias")]
+
+
+class NormBackwardArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("dx", "h", "weight", "rstd", "dout", "dh", "dweight")] + [("res_scale", ctypes.c_float)]
+
+
+class CombineNormArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("y", "slot_pos", "topk_w", "h", "weight", "gate", "out", "rstd", "next_weight",
+                 "next_x", "next_rstd")] + [("eps", ctypes.c_float), ("res_scale", ctypes.c_float)]
+
+
+class CombineNormBackwardArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("dout", "y", "slot_pos", "topk_w", "weight", "rstd", "gate", "dy", "dtopk_w",
+                 "dweight", "dgate")]
 
 
 _GRAD = "PPqi4x"   # moe_grad_t
@@ -95,10 +113,15 @@ def load_library() -> ctypes.CDLL:
     lib.moe_grad_workspace_size.restype = sz
     lib.moe_grad_norm.argtypes = [vp, i32, vp, vp, sz, vp]
     lib.moe_grad_clip.argtypes = [vp, i32, vp, ctypes.c_float, vp]
+    lib.moe_norm.argtypes = [P, vp, vp, ctypes.c_float, vp, vp, vp]
+    lib.moe_norm_backward.argtypes = [P, ctypes.POINTER(NormBackwardArgs), vp, sz, vp]
+    lib.moe_combine_norm.argtypes = [P, ctypes.POINTER(CombineNormArgs), vp]
+    lib.moe_combine_norm_backward.argtypes = [P, ctypes.POINTER(CombineNormBackwardArgs), vp, sz, vp]
     for f in ("moe_route", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_forward",
               "moe_forward_noalloc", "moe_eplb_plan", "moe_eplb_remap", "moe_pack_weights",
               "moe_balance_loss", "moe_route_backward", "moe_combine_backward", "moe_grad_norm",
-              "moe_grad_clip"):
+              "moe_grad_clip", "moe_norm", "moe_norm_backward", "moe_combine_norm",
+              "moe_combine_norm_backward"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -431,6 +454,67 @@ def moe_grad_clip(grads, norm, max_norm: float, stream=None) -> None:
     g = _grads(c, grads, dev)
     _check(c, load_library().moe_grad_clip(g.array, g.n, _arg(c, "norm", norm, torch.float32, 1, dev),
                                            max_norm, st))
+
+
+# ---- norms around the layer (tensors checked as above)
+
+def moe_norm(p, h, weight, eps: float, x, rstd=None, stream=None) -> None:
+    """The norm before the layer: x = h r weight, r into ``rstd`` (see moe.h)."""
+    c = "moe_norm"
+    dev, st = _current(c, stream)
+    f32, act, n = torch.float32, _act(c, p), p.T * p.d
+    _check(c, load_library().moe_norm(
+        ctypes.byref(p), _arg(c, "h", h, act, n, dev), _arg(c, "weight", weight, f32, p.d, dev), eps,
+        _arg(c, "x", x, act, n, dev), _arg(c, "rstd", rstd, f32, p.T, dev), st))
+
+
+def moe_norm_backward(p, *, dx, h, weight, rstd, ws, dout=None, res_scale: float = 1.0, dh=None,
+                      dweight=None, stream=None) -> None:
+    """Gradient of the norm before the layer, joined to ``res_scale * dout`` (see moe.h)."""
+    c = "moe_norm_backward"
+    dev, st = _current(c, stream)
+    f32, act, n = torch.float32, _act(c, p), p.T * p.d
+    a = NormBackwardArgs(
+        _arg(c, "dx", dx, act, n, dev), _arg(c, "h", h, act, n, dev),
+        _arg(c, "weight", weight, f32, p.d, dev), _arg(c, "rstd", rstd, f32, p.T, dev),
+        _arg(c, "dout", dout, act, n, dev), _arg(c, "dh", dh, act, n, dev),
+        _arg(c, "dweight", dweight, f32, p.d, dev), res_scale)
+    wp, wn = _ws_arg(c, ws, dev)
+    _check(c, load_library().moe_norm_backward(ctypes.byref(p), ctypes.byref(a), wp, wn, st))
+
+
+def moe_combine_norm(p, *, y, h, weight, eps: float, out, slot_pos=None, topk_w=None, gate=None,
+                     res_scale: float = 1.0, rstd=None, next_weight=None, next_x=None,
+                     next_rstd=None, stream=None) -> None:
+    """Combine, norm, gate and residual after the layer, and the next block's norm (see moe.h)."""
+    c = "moe_combine_norm"
+    dev, st = _current(c, stream)
+    f32, act, n, S = torch.float32, _act(c, p), p.T * p.d, p.T * p.k
+    a = CombineNormArgs(
+        _arg(c, "y", y, act, S * p.d, dev), _arg(c, "slot_pos", slot_pos, torch.int32, S, dev),
+        _arg(c, "topk_w", topk_w, f32, S, dev), _arg(c, "h", h, act, n, dev),
+        _arg(c, "weight", weight, f32, p.d, dev), _arg(c, "gate", gate, f32, p.d, dev),
+        _arg(c, "out", out, act, n, dev), _arg(c, "rstd", rstd, f32, p.T, dev),
+        _arg(c, "next_weight", next_weight, f32, p.d, dev), _arg(c, "next_x", next_x, act, n, dev),
+        _arg(c, "next_rstd", next_rstd, f32, p.T, dev), eps, res_scale)
+    _check(c, load_library().moe_combine_norm(ctypes.byref(p), ctypes.byref(a), st))
+
+
+def moe_combine_norm_backward(p, *, dout, y, weight, rstd, ws, slot_pos=None, topk_w=None, gate=None,
+                              dy=None, dtopk_w=None, dweight=None, dgate=None, stream=None) -> None:
+    """Gradients of the expert rows, the gates, the norm's weight and the channel gate (see moe.h)."""
+    c = "moe_combine_norm_backward"
+    dev, st = _current(c, stream)
+    f32, act, n, S = torch.float32, _act(c, p), p.T * p.d, p.T * p.k
+    a = CombineNormBackwardArgs(
+        _arg(c, "dout", dout, act, n, dev), _arg(c, "y", y, act, S * p.d, dev),
+        _arg(c, "slot_pos", slot_pos, torch.int32, S, dev), _arg(c, "topk_w", topk_w, f32, S, dev),
+        _arg(c, "weight", weight, f32, p.d, dev), _arg(c, "rstd", rstd, f32, p.T, dev),
+        _arg(c, "gate", gate, f32, p.d, dev), _arg(c, "dy", dy, act, S * p.d, dev),
+        _arg(c, "dtopk_w", dtopk_w, f32, S, dev), _arg(c, "dweight", dweight, f32, p.d, dev),
+        _arg(c, "dgate", dgate, f32, p.d, dev))
+    wp, wn = _ws_arg(c, ws, dev)
+    _check(c, load_library().moe_combine_norm_backward(ctypes.byref(p), ctypes.byref(a), wp, wn, st))
 
 
 def workspace(p: Problem, call: int, device="cuda") -> torch.Tensor:

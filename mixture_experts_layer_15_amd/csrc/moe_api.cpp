@@ -169,6 +169,9 @@ size_t moe_workspace_size(const moe_problem_t* p, int32_t call) {
       return moe::balance_ws_bytes(s);
     case MOE_CALL_ROUTE_BACKWARD:
       return moe::route_backward_ws_bytes(s);
+    case MOE_CALL_NORM_BACKWARD:
+    case MOE_CALL_COMBINE_NORM_BACKWARD:
+      return moe::norm_grad_ws_bytes(s);
     default:
       return 0;
   }
@@ -413,6 +416,80 @@ moe_status_t moe_grad_clip(const moe_grad_t* g, int32_t n, const float* norm, fl
     return MOE_ERR_INVALID_ARGUMENT;
   if (!(max_norm > 0.0f) || norm_in_list(g, n, norm, true)) return MOE_ERR_INVALID_ARGUMENT;
   return from_hip(moe::grad_clip(g, n, norm, max_norm, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_norm(const moe_problem_t* p, const void* h, const float* weight, float eps,
+                      void* x, float* rstd, void* stream) {
+  Shape s;
+  moe_status_t st = check_problem(p, &s);
+  if (st != MOE_OK) return st;
+  if (!(eps > 0.0f) || !all_aligned16(h, weight, x, rstd)) return MOE_ERR_INVALID_ARGUMENT;
+  if (s.T == 0) return MOE_OK;
+  if (h == nullptr || weight == nullptr || x == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  return from_hip(moe::norm(s, h, weight, eps, x, rstd, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_norm_backward(const moe_problem_t* p, const moe_norm_backward_args_t* a, void* ws,
+                               size_t ws_bytes, void* stream) {
+  Shape s;
+  moe_status_t st = check_problem(p, &s);
+  if (st != MOE_OK) return st;
+  if (a == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (!all_aligned16(a->dx, a->h, a->weight, a->rstd, a->dout, a->dh, a->dweight, ws))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (s.T > 0) {
+    if (a->dx == nullptr || a->h == nullptr || a->weight == nullptr || a->rstd == nullptr)
+      return MOE_ERR_INVALID_ARGUMENT;
+    if ((a->dh == nullptr && a->dweight == nullptr) || a->dh == a->h)
+      return MOE_ERR_INVALID_ARGUMENT;
+  }
+  if (ws == nullptr || ws_bytes < moe::norm_grad_ws_bytes(s)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return from_hip(moe::norm_backward(s, *a, ws, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_combine_norm(const moe_problem_t* p, const moe_combine_norm_args_t* a,
+                              void* stream) {
+  Shape s;
+  moe_status_t st = check_problem(p, &s);
+  if (st != MOE_OK) return st;
+  if (a == nullptr || !(a->eps > 0.0f)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!all_aligned16(a->y, a->slot_pos, a->topk_w, a->h, a->weight, a->gate, a->out, a->rstd,
+                     a->next_weight, a->next_x, a->next_rstd))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (s.T == 0) return MOE_OK;
+  if (a->y == nullptr || a->h == nullptr || a->weight == nullptr || a->out == nullptr)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (a->slot_pos == nullptr && s.k != 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (a->next_weight == nullptr ? a->next_x != nullptr || a->next_rstd != nullptr
+                                : a->next_x == nullptr)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (a->out == a->y || a->next_x == a->out || (a->next_x != nullptr && a->next_x == a->y) ||
+      (a->rstd != nullptr && a->rstd == a->next_rstd))
+    return MOE_ERR_INVALID_ARGUMENT;
+  return from_hip(moe::combine_norm(s, *a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_combine_norm_backward(const moe_problem_t* p,
+                                       const moe_combine_norm_backward_args_t* a, void* ws,
+                                       size_t ws_bytes, void* stream) {
+  Shape s;
+  moe_status_t st = check_problem(p, &s);
+  if (st != MOE_OK) return st;
+  if (a == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (!all_aligned16(a->dout, a->y, a->slot_pos, a->topk_w, a->weight, a->rstd, a->gate, a->dy,
+                     a->dtopk_w, a->dweight, a->dgate, ws))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (s.T > 0) {
+    if (a->dout == nullptr || a->y == nullptr || a->weight == nullptr || a->rstd == nullptr)
+      return MOE_ERR_INVALID_ARGUMENT;
+    if (a->dy == nullptr && a->dtopk_w == nullptr && a->dweight == nullptr && a->dgate == nullptr)
+      return MOE_ERR_INVALID_ARGUMENT;
+    if (a->slot_pos == nullptr && (s.k != 1 || a->dtopk_w != nullptr))
+      return MOE_ERR_INVALID_ARGUMENT;
+    if (a->dy != nullptr && (a->dy == a->y || a->dy == a->dout)) return MOE_ERR_INVALID_ARGUMENT;
+  }
+  if (ws == nullptr || ws_bytes < moe::norm_grad_ws_bytes(s)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  return from_hip(moe::combine_norm_backward(s, *a, ws, static_cast<hipStream_t>(stream)));
 }
 
 moe_status_t moe_pack_weights(const moe_problem_t* p, int32_t which, const void* src, void* dst,

@@ -146,6 +146,16 @@ hipError_t grad_norm(const moe_grad_t* g, int n, float* norm, void* ws, hipStrea
 hipError_t grad_clip(const moe_grad_t* g, int n, const float* norm, float max_norm,
                      hipStream_t st);
 
+// ---- norm.hip
+size_t norm_grad_ws_bytes(const Shape& s);  // of either backward pass
+hipError_t norm(const Shape& s, const void* h, const float* weight, float eps, void* x, float* rstd,
+                hipStream_t st);
+hipError_t norm_backward(const Shape& s, const moe_norm_backward_args_t& g, void* ws,
+                         hipStream_t st);
+hipError_t combine_norm(const Shape& s, const moe_combine_norm_args_t& g, hipStream_t st);
+hipError_t combine_norm_backward(const Shape& s, const moe_combine_norm_backward_args_t& g,
+                                 void* ws, hipStream_t st);
+
 // Blocked layout of one stored expert weight matrix [Nout][K] (any weight
 // format but float32): [Nout/32][K/64][32 rows][64 K values], each 32 x 64
 // unit being the LDS image the expert GEMMs stage for that block (rows in

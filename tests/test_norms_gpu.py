@@ -1,0 +1,293 @@
+"""Norms around the layer against 64 bits (bounds of tests/norm_reference.py,
+element by element), on every row-group size, both types, rows without a kept
+slot, in place, on another stream and replayed from a captured graph."""
+import pytest
+import torch
+
+import norm_reference as R
+from mixture_experts_layer_15_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+EPS = 1e-5
+ACT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.load_library()
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _within(got, want, err, what):
+    got = got.double()
+    assert torch.isfinite(got).all(), what
+    over = (got - want).abs() - err
+    assert float(over.max()) <= 0, (what, float(over.max()), float((got - want).abs().max()))
+
+
+def _problem(T, d, k=1, act="bf16", E=64):
+    return B.problem(T, d, E, k, 128, act=act, weight=act)
+
+
+# a row group of every kind: a wave of one and two chunks, 256 threads of one, two and four, 1024 of two, four, eight
+WIDTHS = [128, 640, 1152, 2048, 2176, 7168, 9216, 17408, 65536]
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("d", WIDTHS)
+@pytest.mark.parametrize("T", [1, 37])
+def test_norm(act, d, T):
+    g = _gen(d + T)
+    h = (torch.randn(T, d, generator=g, device=DEV) * torch.exp(torch.randn(d, generator=g, device=DEV))).to(ACT[act])
+    h[T // 2, : d // 2] = 0
+    if T > 1:
+        h[-1] = 0
+    w = torch.randn(d, generator=g, device=DEV)
+    x = torch.full_like(h, float("nan"))
+    r = torch.full((T,), float("nan"), device=DEV)
+    p = _problem(T, d, act=act)
+    B.moe_norm(p, h, w, EPS, x, r)
+    want, err, rr, dr = R.norm(h.double(), w.double(), EPS)
+    _within(x, want, R.stored(want, err, h.dtype), "x")
+    _within(r, rr, rr * (dr + R.U), "rstd")
+    again = h.clone()
+    B.moe_norm(p, again, w, EPS, again)      # in place, without rstd
+    assert torch.equal(again, x)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("d", WIDTHS)
+@pytest.mark.parametrize("T", [1, 3, 131])
+def test_norm_backward(act, d, T):
+    if T * d > 3e6:
+        T = 40
+    g = _gen(7 * d + T)
+    t = ACT[act]
+    h, dx, dout = (torch.randn(T, d, generator=g, device=DEV).to(t) for _ in range(3))
+    w = torch.randn(d, generator=g, device=DEV)
+    r = R.rstd(h.double(), EPS).float()
+    p = _problem(T, d, act=act)
+    ws = B.workspace(p, B.MOE_CALL_NORM_BACKWARD, DEV).fill_(0xFF)
+    for with_dout in (True, False):
+        dh, dw = torch.full_like(h, float("nan")), torch.full((d,), float("nan"), device=DEV)
+        B.moe_norm_backward(p, dx=dx, h=h, weight=w, rstd=r, dout=dout if with_dout else None, res_scale=0.5, dh=dh, dweight=dw, ws=ws)
+        n, u = h.double() * r.double()[:, None], dx.double() * w.double()
+        m, ma = (n * u).mean(dim=1, keepdim=True), (n * u).abs().mean(dim=1, keepdim=True)
+        rr = r.double()[:, None]
+        res = 0.5 * dout.double() if with_dout else torch.zeros_like(u)
+        want = rr * (u - n * m) + res
+        dm = (R.chain(d) + 4) * R.U * ma
+        err = rr * (n.abs() * dm + 5 * R.U * (u.abs() + (n * m).abs())) + 2 * R.U * (res.abs() + want.abs())
+        _within(dh, want, R.stored(want, err, t), "dh")
+        s = (dx.double() * n)
+        _within(dw, s.sum(dim=0), (T / 256 + 150) * R.U * s.abs().sum(dim=0), "dweight")
+    # each output alone, and dh over dx
+    dw2 = torch.empty_like(dw)
+    B.moe_norm_backward(p, dx=dx, h=h, weight=w, rstd=r, dweight=dw2, ws=ws)
+    assert torch.equal(dw2, dw)
+    over = dx.clone()
+    B.moe_norm_backward(p, dx=over, h=h, weight=w, rstd=r, dh=over, ws=ws)
+    assert torch.equal(over, dh)
+
+
+def test_norm_backward_of_no_tokens():
+    p = _problem(0, 256)
+    ws = B.workspace(p, B.MOE_CALL_NORM_BACKWARD, DEV)
+    e = torch.empty(0, 256, dtype=torch.bfloat16, device=DEV)
+    w, dw = torch.ones(256, device=DEV), torch.full((256,), float("nan"), device=DEV)
+    B.moe_norm_backward(p, dx=e, h=e, weight=w, rstd=torch.empty(0, device=DEV), dweight=dw, ws=ws)
+    assert not dw.any()
+    dw.fill_(float("nan"))
+    dg = dw.clone()
+    B.moe_combine_norm_backward(p, dout=e, y=e, weight=w, rstd=torch.empty(0, device=DEV), dweight=dw, dgate=dg, ws=ws)
+    assert not dw.any() and not dg.any()
+
+
+def _slots(T, k, g, drop):
+    """slot_pos [T*k]: kept slots in a shuffled order, the others -1 (token 0 keeps none where `drop`), one out of range."""
+    keep = torch.rand(T * k, generator=g, device=DEV) > (0.3 if drop else -1.0)
+    if drop:
+        keep[:k] = False
+    order = torch.randperm(T * k, generator=g, device=DEV)
+    order = order[keep[order]]
+    pos = torch.full((T * k,), -1, dtype=torch.int32, device=DEV)
+    pos[order] = torch.arange(order.numel(), dtype=torch.int32, device=DEV)
+    if drop and T * k > 1:
+        pos[0] = T * k      # outside [0, T*k): not kept
+    return pos, int(order.numel())
+
+
+SHAPES = [(1, 128, 1), (5, 128, 8), (33, 640, 3), (9, 2048, 8), (17, 2048, 9), (6, 7168, 8), (4, 7168, 20), (3, 9216, 8), (3, 17408, 2),
+          (2, 65536, 8), (2, 65536, 17)]
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,k", SHAPES)
+@pytest.mark.parametrize("gated,drop,weighted", [(True, False, True), (False, True, True), (True, True, False)])
+def test_combine_norm(act, T, d, k, gated, drop, weighted):
+    g = _gen(T * d + k)
+    t = ACT[act]
+    pos, kept = _slots(T, k, g, drop)
+    y = torch.randn(T * k, d, generator=g, device=DEV).to(t)
+    y[kept:] = float("nan")                  # rows behind the last kept slot are not read
+    h = torch.randn(T, d, generator=g, device=DEV).to(t)
+    w, nw = torch.randn(d, generator=g, device=DEV), torch.randn(d, generator=g, device=DEV)
+    gate = torch.randn(d, generator=g, device=DEV) if gated else None
+    tw = torch.rand(T, k, generator=g, device=DEV) if weighted else None
+    p = _problem(T, d, k, act)
+    nan = float("nan")
+    out, nx = torch.full_like(h, nan), torch.full_like(h, nan)
+    r, nr = torch.full((T,), nan, device=DEV), torch.full((T,), nan, device=DEV)
+    B.moe_combine_norm(p, y=y, slot_pos=pos, topk_w=tw, h=h, weight=w, gate=gate, eps=EPS, res_scale=0.75, out=out, rstd=r,
+                       next_weight=nw, next_x=nx, next_rstd=nr)
+    at = torch.where(pos >= T * k, -1, pos).view(T, k).long()
+    clean = y.double().nan_to_num()
+    want, err, rr, dr = R.after(clean, at, None if tw is None else tw.double(), h.double(), w.double(),
+                                None if gate is None else gate.double(), EPS, 0.75)
+    _within(out, want, R.stored(want, err, t), "out")
+    _within(r, rr, rr * (dr + R.U), "rstd")
+    nwant, nerr, nrr, ndr = R.norm(out.double(), nw.double(), EPS)     # of the stored out
+    _within(nx, nwant, R.stored(nwant, nerr, t), "next_x")
+    _within(nr, nrr, nrr * (ndr + R.U), "next_rstd")
+    if drop:                                  # token 0 keeps no slot
+        assert torch.equal(out[0].double(), (0.75 * h[0].float()).to(t).double())
+    # in place over the residual, without the next norm
+    again = h.clone()
+    B.moe_combine_norm(p, y=y, slot_pos=pos, topk_w=tw, h=again, weight=w, gate=gate, eps=EPS, res_scale=0.75, out=again)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,k", SHAPES + [(700, 256, 4), (2500, 1152, 2)])
+@pytest.mark.parametrize("gated,drop,weighted", [(True, False, True), (False, True, True), (True, True, False)])
+def test_combine_norm_backward(act, T, d, k, gated, drop, weighted):
+    g = _gen(3 * T * d + k)
+    t = ACT[act]
+    pos, kept = _slots(T, k, g, drop)
+    y = torch.randn(T * k, d, generator=g, device=DEV).to(t)
+    y[kept:] = float("nan")
+    dout = torch.randn(T, d, generator=g, device=DEV).to(t)
+    w = torch.randn(d, generator=g, device=DEV)
+    gate = torch.randn(d, generator=g, device=DEV) if gated else None
+    tw = torch.rand(T, k, generator=g, device=DEV) + 0.1 if weighted else None
+    at = torch.where(pos >= T * k, -1, pos).view(T, k).long()
+    clean = y.double().nan_to_num().requires_grad_(True)
+    tw64 = (torch.ones(T, k, dtype=torch.float64, device=DEV) if tw is None else tw.double()).requires_grad_(True)
+    w64 = w.double().requires_grad_(True)
+    gate64 = torch.ones(d, dtype=torch.float64, device=DEV) if gate is None else gate.double()
+    gate64.requires_grad_(True)
+    c, ec = R.combined(clean.detach(), at, tw64.detach())
+    r = R.rstd(c, EPS).float()
+    rr = r.double()[:, None]
+    # the gradient with r's own derivative, at the r that the call is given
+    r_of = lambda v: R.rstd(v, EPS) * (r.double() / R.rstd(c, EPS))  # noqa: E731
+    dy64, dtw64, dw64, dg64 = torch.autograd.grad(R.loss_after(clean, at, tw64, w64, gate64, r_of, dout.double()),
+                                                  (clean, tw64, w64, gate64))
+    p = _problem(T, d, k, act)
+    ws = B.workspace(p, B.MOE_CALL_COMBINE_NORM_BACKWARD, DEV).fill_(0xFF)
+    dy = torch.full_like(y, 7.0)
+    dtw = torch.full((T, k), float("nan"), device=DEV)
+    dw, dg = torch.full((d,), float("nan"), device=DEV), torch.full((d,), float("nan"), device=DEV)
+    kw = dict(dout=dout, y=y, slot_pos=pos, topk_w=tw, weight=w, rstd=r, gate=gate, ws=ws)
+    B.moe_combine_norm_backward(p, dy=dy, dtopk_w=dtw, dweight=dw, dgate=dg, **kw)
+    # bounds: c is off by ec, n = c r, u = w g dout; r's relative error against c's own (2^-24) enters dc once more
+    u = w.double() * gate64.detach() * dout.double()
+    n, en = c * rr, ec * rr + 2 * R.U * (c * rr).abs()
+    m = (n * u).mean(dim=1, keepdim=True)
+    em = (en * u.abs()).mean(dim=1, keepdim=True) + (R.chain(d) + 5) * R.U * (n * u).abs().mean(dim=1, keepdim=True)
+    edc = rr * (n.abs() * em + en * m.abs() + 6 * R.U * (u.abs() + (n * m).abs()))
+    wmax = tw64.detach().abs()
+    for i in range(k):
+        rows = at[:, i] >= 0
+        if not rows.any():
+            continue
+        q = at[rows, i]
+        err = wmax[rows, i, None] * edc[rows] + 2 * R.U * dy64[q].abs()
+        _within(dy[q], dy64[q], R.stored(dy64[q], err, t), "dy")
+        yy = clean.detach()[q].abs()
+        row = (R.chain(d) + 8) * R.U
+        et = rr[rows, 0] * (row * (u[rows].abs() * yy).sum(dim=1)
+                            + (rr * m.abs())[rows, 0] * ((ec[rows] * yy).sum(dim=1) + row * (c[rows].abs() * yy).sum(dim=1))
+                            + (rr * em)[rows, 0] * (c[rows].abs() * yy).sum(dim=1)) + (edc[rows] * yy).sum(dim=1)
+        _within(dtw[rows, i], dtw64[rows, i], et + 4 * R.U * dtw64[rows, i].abs() + 1e-38, "dtopk_w")
+    assert not dtw[at < 0].any()
+    if kept < T * k:
+        assert (dy[kept:] == 7.0).all()       # rows that no kept slot names are left as they were
+    o = dout.double()
+    es = (o.abs() * en).sum(dim=0) + (T / 256 + 150) * R.U * (o * n).abs().sum(dim=0)
+    _within(dw, dw64, gate64.detach().abs() * es + 2 * R.U * dw64.abs() + 1e-38, "dweight")
+    _within(dg, dg64, w.double().abs() * es + 2 * R.U * dg64.abs() + 1e-38, "dgate")
+    # an output alone has the same bits
+    for name, full in (("dy", dy), ("dtopk_w", dtw), ("dweight", dw), ("dgate", dg)):
+        alone = torch.full_like(full, 7.0)
+        B.moe_combine_norm_backward(p, **{name: alone}, **kw)
+        assert torch.equal(alone, full), name
+
+
+def test_rows_without_slots():
+    """slot_pos None: row t is token t's, as after an exchange between ranks; the same as k = 1 with the identity."""
+    T, d = 21, 640
+    g = _gen(5)
+    y, h, dout = (torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16) for _ in range(3))
+    w = torch.randn(d, generator=g, device=DEV)
+    p = _problem(T, d, 1)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    outs, grads = [], []
+    for sp in (None, pos):
+        out, r = torch.empty_like(h), torch.empty(T, device=DEV)
+        B.moe_combine_norm(p, y=y, slot_pos=sp, h=h, weight=w, eps=EPS, out=out, rstd=r)
+        dy, dw = torch.empty_like(y), torch.empty(d, device=DEV)
+        B.moe_combine_norm_backward(p, dout=dout, y=y, slot_pos=sp, weight=w, rstd=r, dy=dy, dweight=dw,
+                                    ws=B.workspace(p, B.MOE_CALL_COMBINE_NORM_BACKWARD, DEV))
+        outs.append(out)
+        grads.append((dy, dw))
+    assert torch.equal(outs[0], outs[1])
+    assert torch.equal(grads[0][0], grads[1][0]) and torch.equal(grads[0][1], grads[1][1])
+
+
+def test_captured_and_other_stream():
+    """Forward and backward in one captured graph, replayed with new inputs between eager work, and on a side stream."""
+    T, d, k = 65, 2048, 8
+    g = _gen(9)
+    pos, _ = _slots(T, k, g, False)
+    p = _problem(T, d, k)
+    w, gate = torch.randn(d, generator=g, device=DEV), torch.randn(d, generator=g, device=DEV)
+    y, h, dout = (torch.randn(n, d, generator=g, device=DEV).to(torch.bfloat16) for n in (T * k, T, T))
+    tw = torch.rand(T, k, generator=g, device=DEV)
+    o = dict(out=torch.empty_like(h), r=torch.empty(T, device=DEV), nx=torch.empty_like(h), nr=torch.empty(T, device=DEV),
+             dy=torch.empty_like(y), dtw=torch.empty_like(tw), dw=torch.empty(d, device=DEV), dg=torch.empty(d, device=DEV),
+             dh=torch.empty_like(h), dnw=torch.empty(d, device=DEV))
+
+    def step(ws, stream=None):
+        B.moe_combine_norm(p, y=y, slot_pos=pos, topk_w=tw, h=h, weight=w, gate=gate, eps=EPS, out=o["out"], rstd=o["r"],
+                           next_weight=w, next_x=o["nx"], next_rstd=o["nr"], stream=stream)
+        B.moe_norm_backward(p, dx=dout, h=o["out"], weight=w, rstd=o["nr"], dout=dout, dh=o["dh"], dweight=o["dnw"], ws=ws, stream=stream)
+        B.moe_combine_norm_backward(p, dout=o["dh"], y=y, slot_pos=pos, topk_w=tw, weight=w, rstd=o["r"], gate=gate, dy=o["dy"],
+                                    dtopk_w=o["dtw"], dweight=o["dw"], dgate=o["dg"], ws=ws, stream=stream)
+    ws = B.workspace(p, B.MOE_CALL_COMBINE_NORM_BACKWARD, DEV)
+    step(ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(ws)
+    side = torch.cuda.Stream()
+    for n in range(3):
+        for t in (y, h, dout):
+            t.copy_(torch.randn(t.shape, generator=g, device=DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {k_: v.clone() for k_, v in o.items()}
+        for v in o.values():
+            v.zero_()
+        torch.cuda.synchronize()
+        step(B.workspace(p, B.MOE_CALL_COMBINE_NORM_BACKWARD, DEV), stream=side)
+        side.synchronize()
+        for name, v in o.items():
+            assert torch.equal(v, got[name]), (n, name)
