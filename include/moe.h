@@ -125,7 +125,8 @@ typedef enum {
   MOE_CALL_BALANCE_LOSS = 4,
   MOE_CALL_ROUTE_BACKWARD = 5,
   MOE_CALL_NORM_BACKWARD = 6,
-  MOE_CALL_COMBINE_NORM_BACKWARD = 7
+  MOE_CALL_COMBINE_NORM_BACKWARD = 7,
+  MOE_CALL_EXPERT_FFN_MX = 8
 } moe_call_t;
 
 /* Layout of the expert weight matrices. */
@@ -575,6 +576,57 @@ typedef struct {
 moe_status_t moe_combine_norm_backward(const moe_problem_t* p,
                                        const moe_combine_norm_backward_args_t* a, void* ws,
                                        size_t ws_bytes, void* stream);
+
+/* ---- 4-bit activations (MXFP4) ----
+ *
+ * "Serving MoE models with expert parallelism on 8xH200" (reviosa), section
+ * "Quantization choices", weighs 4-bit expert weights.  These calls make them
+ * on the device, and run the expert network with the activations in the same
+ * format, on the matrix instructions that multiply 4-bit operands.
+ *
+ * moe_mx_quantize - blocks of 32 consecutive values v of a row become
+ *    X = floor(log2(max |v|)) - 2, clamped to -127 .. 125 (0 for a block of zeros)
+ *    scale byte X + 127,  codes = the E2M1 value nearest to v / 2^X
+ * (OCP MX v1.0; ties to the even code, magnitudes above 6 become 6, the sign
+ * of a value that rounds to zero is kept).  A block with an infinity or a NaN
+ * gets the scale byte 255 (NaN) and codes 0.
+ *  src [batch][rows][cols] of dtype MOE_F32 or MOE_BF16; codes
+ *  [batch][rows][cols / 2] bytes, element 2j in the low nibble of byte j;
+ *  scales: MOE_MX_SCALES_ROW [batch][rows][cols / 32] (activations), or
+ *  MOE_MX_SCALES_BLOCK [batch][cols / 32][rows] (expert weights: batch = E_l,
+ *  rows = F, cols = d for w_gate and w_up, rows = d, cols = F for w_down).
+ *  cols is a multiple of 32, at most 65536; batch * rows < 2^31.  Arrays are
+ *  16-byte aligned.  batch = 0 or rows = 0 enqueues nothing.
+ * moe_mx_dequantize - the values back, into dst of dtype MOE_F32 or MOE_BF16
+ *  (exact in both for scale bytes 0 .. 252; byte 255 gives NaN, 253 and 254
+ *  are outside the contract). */
+typedef enum { MOE_MX_SCALES_ROW = 0, MOE_MX_SCALES_BLOCK = 1 } moe_mx_scales_t;
+
+moe_status_t moe_mx_quantize(int32_t batch, int32_t rows, int32_t cols, int32_t dtype,
+                             const void* src, void* codes, void* scales, int32_t scale_layout,
+                             void* stream);
+moe_status_t moe_mx_dequantize(int32_t batch, int32_t rows, int32_t cols, int32_t dtype,
+                               const void* codes, const void* scales, void* dst,
+                               int32_t scale_layout, void* stream);
+
+/* moe_expert_ffn_mx - moe_expert_ffn on 4-bit activations: with A the values
+ * that x_codes and x_scales stand for, and Q the conversion of moe_mx_quantize
+ * (blocks of 32 features),
+ *    h = silu(A Wg) * (A Wu) in float32,  y[p] = (Q(h) Wd) (topk_w ? topk_w[s] : 1)
+ * rounded once to bfloat16.  Products are exact, sums float32.  A row with a
+ * scale byte 255 (and one whose h holds an infinity or a NaN) gives NaN.
+ *  p: act MOE_BF16 (the format of y), weight MOE_MXFP4, either layout.
+ *  x_codes [T][d / 2], x_scales [T][d / 32] (MOE_MX_SCALES_ROW).
+ *  The other arguments are those of moe_expert_ffn; segment bounds in offsets
+ *  are held inside [0, T*k].  Rows of y behind the last kept row are not
+ *  written.  Arrays are 16-byte aligned.
+ *  ws, ws_bytes: scratch of moe_workspace_size(p, MOE_CALL_EXPERT_FFN_MX). */
+moe_status_t moe_expert_ffn_mx(const moe_problem_t* p, const void* x_codes, const void* x_scales,
+                               const int32_t* sorted_slot, const int32_t* offsets,
+                               const void* w_gate, const void* w_up, const void* w_down,
+                               const void* s_gate, const void* s_up, const void* s_down,
+                               const float* topk_w, void* y, void* ws, size_t ws_bytes,
+                               void* stream);
 
 /* Blocked weight layout (for callers that convert weights once at load
  * time): each expert matrix [Nout][K] is stored as [Nout/32][K/64] units of

@@ -24,6 +24,8 @@ MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_MXFP4 = range(4)
 MOE_CALL_PERMUTE, MOE_CALL_EXPERT_FFN, MOE_CALL_FORWARD, MOE_CALL_ROUTE = range(4)
 MOE_CALL_BALANCE_LOSS, MOE_CALL_ROUTE_BACKWARD = 4, 5
 MOE_CALL_NORM_BACKWARD, MOE_CALL_COMBINE_NORM_BACKWARD = 6, 7
+MOE_CALL_EXPERT_FFN_MX = 8
+MOE_MX_SCALES_ROW, MOE_MX_SCALES_BLOCK = range(2)
 MOE_GRAD_MAX_TENSORS = 4096   # include/moe.h
 MOE_FORWARD_EVENTS = 7
 MOE_LAYOUT_ROWS, MOE_LAYOUT_BLOCKED = range(2)
@@ -117,11 +119,15 @@ def load_library() -> ctypes.CDLL:
     lib.moe_norm_backward.argtypes = [P, ctypes.POINTER(NormBackwardArgs), vp, sz, vp]
     lib.moe_combine_norm.argtypes = [P, ctypes.POINTER(CombineNormArgs), vp]
     lib.moe_combine_norm_backward.argtypes = [P, ctypes.POINTER(CombineNormBackwardArgs), vp, sz, vp]
+    lib.moe_mx_quantize.argtypes = [i32, i32, i32, i32, vp, vp, vp, i32, vp]
+    lib.moe_mx_dequantize.argtypes = [i32, i32, i32, i32, vp, vp, vp, i32, vp]
+    lib.moe_expert_ffn_mx.argtypes = [P] + [vp] * 13 + [sz, vp]
     for f in ("moe_route", "moe_permute", "moe_expert_ffn", "moe_combine", "moe_forward",
               "moe_forward_noalloc", "moe_eplb_plan", "moe_eplb_remap", "moe_pack_weights",
               "moe_balance_loss", "moe_route_backward", "moe_combine_backward", "moe_grad_norm",
               "moe_grad_clip", "moe_norm", "moe_norm_backward", "moe_combine_norm",
-              "moe_combine_norm_backward"):
+              "moe_combine_norm_backward", "moe_mx_quantize", "moe_mx_dequantize",
+              "moe_expert_ffn_mx"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -515,6 +521,55 @@ def moe_combine_norm_backward(p, *, dout, y, weight, rstd, ws, slot_pos=None, to
         _arg(c, "dgate", dgate, f32, p.d, dev))
     wp, wn = _ws_arg(c, ws, dev)
     _check(c, load_library().moe_combine_norm_backward(ctypes.byref(p), ctypes.byref(a), wp, wn, st))
+
+
+# ---- 4-bit activations (tensors checked as above)
+
+def _convert(call: str, values, codes, scales, layout: int, stream):
+    dev, st = _current(call, stream)
+    if values.dim() < 2 or values.shape[-1] == 0 or values.shape[-1] % 32:
+        _refuse(call, f"values of shape {tuple(values.shape)}: at least two dimensions, the last a multiple of 32")
+    if values.dtype not in _GRAD_CODE:
+        raise MoEError(call, MOE_ERR_UNSUPPORTED, f"values are {values.dtype}, not float32 or bfloat16")
+    rows, cols = values.shape[-2:]
+    n = values.numel()
+    batch = n // (rows * cols) if n else 0
+    return (batch, rows, cols, _GRAD_CODE[values.dtype], _arg(call, "values", values, values.dtype, n, dev),
+            _arg(call, "codes", codes, torch.uint8, n // 2, dev),
+            _arg(call, "scales", scales, torch.uint8, n // 32, dev), layout, st)
+
+
+def moe_mx_quantize(values, codes, scales, layout: int = MOE_MX_SCALES_ROW, stream=None) -> None:
+    """MXFP4 codes and scales of ``values`` [..., rows, cols] (see moe.h)."""
+    c = "moe_mx_quantize"
+    b, r, n, t, v, q, s, layout, st = _convert(c, values, codes, scales, layout, stream)
+    _check(c, load_library().moe_mx_quantize(b, r, n, t, v, q, s, layout, st))
+
+
+def moe_mx_dequantize(codes, scales, values, layout: int = MOE_MX_SCALES_ROW, stream=None) -> None:
+    """The values [..., rows, cols] that MXFP4 codes and scales stand for (see moe.h)."""
+    c = "moe_mx_dequantize"
+    b, r, n, t, v, q, s, layout, st = _convert(c, values, codes, scales, layout, stream)
+    _check(c, load_library().moe_mx_dequantize(b, r, n, t, q, s, v, layout, st))
+
+
+def moe_expert_ffn_mx(p, x_codes, x_scales, sorted_slot, offsets, w_gate, w_up, w_down, s_gate, s_up,
+                      s_down, topk_w, y, ws, stream=None) -> None:
+    """The expert network on 4-bit activations and weights (see moe.h)."""
+    c = "moe_expert_ffn_mx"
+    dev, st = _current(c, stream)
+    u8, i32, S, W = torch.uint8, torch.int32, p.T * p.k, p.num_local * p.F * p.d
+    wp, wn = _ws_arg(c, ws, dev)
+    _check(c, load_library().moe_expert_ffn_mx(
+        ctypes.byref(p), _arg(c, "x_codes", x_codes, u8, p.T * p.d // 2, dev),
+        _arg(c, "x_scales", x_scales, u8, p.T * p.d // 32, dev),
+        _arg(c, "sorted_slot", sorted_slot, i32, S, dev),
+        _arg(c, "offsets", offsets, i32, p.num_local + 1, dev),
+        _arg(c, "w_gate", w_gate, u8, W // 2, dev), _arg(c, "w_up", w_up, u8, W // 2, dev),
+        _arg(c, "w_down", w_down, u8, W // 2, dev), _arg(c, "s_gate", s_gate, u8, W // 32, dev),
+        _arg(c, "s_up", s_up, u8, W // 32, dev), _arg(c, "s_down", s_down, u8, W // 32, dev),
+        _arg(c, "topk_w", topk_w, torch.float32, S, dev),
+        _arg(c, "y", y, torch.bfloat16, S * p.d, dev), wp, wn, st))
 
 
 def workspace(p: Problem, call: int, device="cuda") -> torch.Tensor:

@@ -121,6 +121,23 @@ bool norm_in_list(const moe_grad_t* g, int32_t n, const float* norm, bool output
   return false;
 }
 
+// Arguments of moe_mx_quantize and moe_mx_dequantize; *none: no values.
+moe_status_t check_convert(int32_t batch, int32_t rows, int32_t cols, int32_t dtype,
+                           const void* values, const void* codes, const void* scales,
+                           int32_t scale_layout, bool* none) {
+  if (batch < 0 || rows < 0 || cols <= 0 || cols % 32 != 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (scale_layout != MOE_MX_SCALES_ROW && scale_layout != MOE_MX_SCALES_BLOCK)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (dtype != MOE_F32 && dtype != MOE_BF16)
+    return dtype > MOE_BF16 && dtype <= MOE_MXFP4 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARGUMENT;
+  if (cols > 65536 || (long long)batch * rows >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!all_aligned16(values, codes, scales)) return MOE_ERR_INVALID_ARGUMENT;
+  *none = batch == 0 || rows == 0;
+  if (!*none && (values == nullptr || codes == nullptr || scales == nullptr))
+    return MOE_ERR_INVALID_ARGUMENT;
+  return MOE_OK;
+}
+
 // Device-memory layout of the moe_forward workspace.
 struct ForwardLayout {
   size_t logits, idx, w, counts, offsets, sorted, pos, y, router, permute, ffn, total;
@@ -172,6 +189,8 @@ size_t moe_workspace_size(const moe_problem_t* p, int32_t call) {
     case MOE_CALL_NORM_BACKWARD:
     case MOE_CALL_COMBINE_NORM_BACKWARD:
       return moe::norm_grad_ws_bytes(s);
+    case MOE_CALL_EXPERT_FFN_MX:
+      return s.weight == MOE_MXFP4 ? moe::mx_ffn_ws_bytes(s) : 0;
     default:
       return 0;
   }
@@ -490,6 +509,60 @@ moe_status_t moe_combine_norm_backward(const moe_problem_t* p,
   }
   if (ws == nullptr || ws_bytes < moe::norm_grad_ws_bytes(s)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   return from_hip(moe::combine_norm_backward(s, *a, ws, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_mx_quantize(int32_t batch, int32_t rows, int32_t cols, int32_t dtype,
+                             const void* src, void* codes, void* scales, int32_t scale_layout,
+                             void* stream) {
+  bool none = false;
+  const moe_status_t st =
+      check_convert(batch, rows, cols, dtype, src, codes, scales, scale_layout, &none);
+  if (st != MOE_OK || none) return st;
+  if (codes == src || scales == src || codes == scales) return MOE_ERR_INVALID_ARGUMENT;
+  return from_hip(moe::mx_quantize(batch, rows, cols, dtype == MOE_BF16, src,
+                                   static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales),
+                                   scale_layout, static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_mx_dequantize(int32_t batch, int32_t rows, int32_t cols, int32_t dtype,
+                               const void* codes, const void* scales, void* dst,
+                               int32_t scale_layout, void* stream) {
+  bool none = false;
+  const moe_status_t st =
+      check_convert(batch, rows, cols, dtype, dst, codes, scales, scale_layout, &none);
+  if (st != MOE_OK || none) return st;
+  if (dst == codes || dst == scales) return MOE_ERR_INVALID_ARGUMENT;
+  return from_hip(moe::mx_dequantize(batch, rows, cols, dtype == MOE_BF16,
+                                     static_cast<const uint8_t*>(codes),
+                                     static_cast<const uint8_t*>(scales), dst, scale_layout,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+moe_status_t moe_expert_ffn_mx(const moe_problem_t* p, const void* x_codes, const void* x_scales,
+                               const int32_t* sorted_slot, const int32_t* offsets,
+                               const void* w_gate, const void* w_up, const void* w_down,
+                               const void* s_gate, const void* s_up, const void* s_down,
+                               const float* topk_w, void* y, void* ws, size_t ws_bytes,
+                               void* stream) {
+  Shape s;
+  moe_status_t st = check_problem(p, &s);
+  if (st != MOE_OK) return st;
+  if (s.weight != MOE_MXFP4) return MOE_ERR_UNSUPPORTED;
+  if (!all_aligned16(x_codes, x_scales, sorted_slot, offsets, w_gate, w_up, w_down, s_gate, s_up,
+                     s_down, topk_w, y, ws))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (w_gate == nullptr || w_up == nullptr || w_down == nullptr || s_gate == nullptr ||
+      s_up == nullptr || s_down == nullptr)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (s.T > 0 && (x_codes == nullptr || x_scales == nullptr || sorted_slot == nullptr ||
+                  offsets == nullptr || y == nullptr))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (ws == nullptr || ws_bytes < moe::mx_ffn_ws_bytes(s)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (s.T == 0) return MOE_OK;
+  return from_hip(moe::expert_ffn_mx(s, static_cast<const uint8_t*>(x_codes),
+                                     static_cast<const uint8_t*>(x_scales), sorted_slot, offsets,
+                                     w_gate, w_up, w_down, s_gate, s_up, s_down, topk_w, y, ws,
+                                     static_cast<hipStream_t>(stream)));
 }
 
 moe_status_t moe_pack_weights(const moe_problem_t* p, int32_t which, const void* src, void* dst,

@@ -156,6 +156,18 @@ hipError_t combine_norm(const Shape& s, const moe_combine_norm_args_t& g, hipStr
 hipError_t combine_norm_backward(const Shape& s, const moe_combine_norm_backward_args_t& g,
                                  void* ws, hipStream_t st);
 
+// ---- mx.hip
+hipError_t mx_quantize(int batch, int rows, int cols, int bf16, const void* src, uint8_t* codes,
+                       uint8_t* scales, int block_major, hipStream_t st);
+hipError_t mx_dequantize(int batch, int rows, int cols, int bf16, const uint8_t* codes,
+                         const uint8_t* scales, void* dst, int block_major, hipStream_t st);
+size_t mx_ffn_ws_bytes(const Shape& s);
+hipError_t expert_ffn_mx(const Shape& s, const uint8_t* x, const uint8_t* xs,
+                         const int32_t* sorted_slot, const int32_t* offsets, const void* w_gate,
+                         const void* w_up, const void* w_down, const void* s_gate,
+                         const void* s_up, const void* s_down, const float* topk_w, void* y,
+                         void* ws, hipStream_t st);
+
 // Blocked layout of one stored expert weight matrix [Nout][K] (any weight
 // format but float32): [Nout/32][K/64][32 rows][64 K values], each 32 x 64
 // unit being the LDS image the expert GEMMs stage for that block (rows in

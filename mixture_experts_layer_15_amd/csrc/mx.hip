@@ -1,0 +1,741 @@
+// Microscaled 4-bit floating point (OCP MX, MXFP4): conversion, and the expert
+// network with activations and weights in 4 bits.
+//
+// "Serving MoE models with expert parallelism on 8xH200" (reviosa), section
+// "Quantization choices", weighs 4-bit expert weights; here the activations
+// are held in 4 bits too, so that the products run on the scaled matrix
+// instruction (v_mfma_scale_f32_32x32x64_f8f6f4, four times the bf16 rate).
+//
+//   conversion:  block of 32:  X = floor(log2 max|v|) - 2 (clamped to -127..125),
+//                code = the E2M1 value nearest to v / 2^X (ties to even, at most 6)
+//   gate/up:     h[p] = Q(silu(A_p Wg_j) * (A_p Wu_j)),  A_p = x[sorted_slot[p] / k]
+//   down:        y[p] = (h[p] Wd_j) * gate(p)
+//
+// Operand layout: lane l of an MFMA operand holds the 32 codes (16 bytes) of
+// row l % 32 and 32-value block l / 32 of a 64-deep step, and that block's
+// scale.  A step of 32 rows is therefore 1 KB of consecutive 16-byte pieces:
+// the unit of the blocked weight layout, of every LDS stage below and of the
+// intermediate h, which lies in the workspace as [group of 32 rows][F / 64]
+// units with scales [group][F / 128][32 rows][4 blocks].  Groups are counted
+// per expert (a group never holds rows of two), so h needs no gather.  Weights
+// are the A operand in the permuted row order (feature 16 (l / 32) + q in
+// register q), so a lane's 16 results are 16 consecutive features of a token.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "moe_device.h"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kNumXcd = 8;
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+// ---- conversion
+
+// The scale byte of a block whose largest magnitude has these float32 bits:
+// X + 127 = exponent field - 2, at least 0; 127 for a block of zeros; 255
+// (NaN) where the block holds an infinity or a NaN.  (The field of the largest
+// finite magnitude, 254, gives 252.)
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
+  const uint32_t e = amax_bits >> 23;
+  if (amax_bits == 0) return 127;
+  return e == 255 ? 255 : e < 2 ? 0 : e - 2;
+}
+
+// 2^(127 - byte): v times it is exact, or far below half of the smallest code.
+__device__ __forceinline__ float mx_inverse(uint32_t byte) {
+  return byte == 255 ? 0.0f : __uint_as_float((254u - byte) << 23);
+}
+
+// 8 values -> 8 codes, the first in the lowest nibble
+__device__ __forceinline__ uint32_t mx_codes8(const float* v, float inv) {
+  uint32_t q = 0;
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0] * inv, v[1] * inv, 1.0f, 0);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2] * inv, v[3] * inv, 1.0f, 1);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4] * inv, v[5] * inv, 1.0f, 2);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6] * inv, v[7] * inv, 1.0f, 3);
+  return q;
+}
+
+// Tiles of kTileCols columns and `rt` rows (a multiple of 8): 32 threads of 8
+// values for a row, 8 rows a pass.  Block-major scales pass through LDS, so
+// that they are written and read in runs of rt bytes.
+constexpr int kTileCols = 256;
+constexpr int kMaxTileRows = 64;
+
+struct ConvertArgs {
+  const void* src;
+  void* dst;
+  uint8_t* codes;
+  uint8_t* scales;
+  int rows, cols, rt;
+  int row_tiles, col_tiles;
+  long long tiles;
+};
+
+struct ConvertTile {
+  long long row0;  // first row of the batch element, in rows of the whole array
+  int r0, c0;      // first row and column of the tile
+};
+
+__device__ __forceinline__ ConvertTile convert_tile(const ConvertArgs& a, long long i) {
+  const long long rt = i / a.col_tiles;
+  return ConvertTile{rt / a.row_tiles * a.rows, (int)(rt % a.row_tiles) * a.rt,
+                     (int)(i % a.col_tiles) * kTileCols};
+}
+
+template <bool kBF16, bool kBlockMajor>
+__global__ __launch_bounds__(256) void mx_quantize_kernel(ConvertArgs a) {
+  __shared__ uint8_t lds[kBlockMajor ? (kTileCols / 32) * kMaxTileRows : 1];
+  const int cq = threadIdx.x % 32, rr = threadIdx.x / 32;
+  for (long long i = blockIdx.x; i < a.tiles; i += gridDim.x) {
+    const ConvertTile t = convert_tile(a, i);
+    const int c = t.c0 + cq * 8;
+    for (int r = rr; r < a.rt; r += 8) {
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      const bool in = t.r0 + r < a.rows && c < a.cols;
+      const long long at = (t.row0 + t.r0 + r) * a.cols + c;
+      if (in) {
+        if constexpr (kBF16) {
+          const u32x4_t u = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.src) + at);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[2 * q] = __uint_as_float(u[q] << 16);
+            v[2 * q + 1] = __uint_as_float(u[q] & 0xffff0000u);
+          }
+        } else {
+          const f32x4_t* p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.src) + at);
+          const f32x4_t lo = p[0], hi = p[1];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[q] = lo[q];
+            v[4 + q] = hi[q];
+          }
+        }
+      }
+      uint32_t top = 0;  // (as integers: a NaN is above an infinity, which is above the rest)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) top = max(top, __float_as_uint(v[q]) & 0x7fffffffu);
+      top = max(top, (uint32_t)__shfl_xor((int)top, 1, kWave));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 2, kWave));
+      const uint32_t byte = mx_scale_byte(top);
+      if (in) {
+        const uint32_t q = byte == 255 ? 0 : mx_codes8(v, mx_inverse(byte));
+        *reinterpret_cast<uint32_t*>(a.codes + at / 2) = q;
+        if (cq % 4 == 0) {
+          if constexpr (kBlockMajor) lds[(cq / 4) * a.rt + r] = (uint8_t)byte;
+          else a.scales[at / 32] = (uint8_t)byte;
+        }
+      }
+    }
+    if constexpr (kBlockMajor) {
+      __syncthreads();
+      const int n = min(a.rt, a.rows - t.r0), kb0 = t.c0 / 32;
+      const int kbs = min(kTileCols / 32, a.cols / 32 - kb0);
+      for (int j = threadIdx.x; j < kbs * a.rt; j += 256) {
+        const int kb = j / a.rt, r = j % a.rt;
+        if (r < n)
+          a.scales[t.row0 * (a.cols / 32) + (long long)(kb0 + kb) * a.rows + t.r0 + r] =
+              lds[kb * a.rt + r];
+      }
+      __syncthreads();
+    }
+  }
+}
+
+template <bool kBF16, bool kBlockMajor>
+__global__ __launch_bounds__(256) void mx_dequantize_kernel(ConvertArgs a) {
+  __shared__ uint8_t lds[kBlockMajor ? (kTileCols / 32) * kMaxTileRows : 1];
+  const int cq = threadIdx.x % 32, rr = threadIdx.x / 32;
+  for (long long i = blockIdx.x; i < a.tiles; i += gridDim.x) {
+    const ConvertTile t = convert_tile(a, i);
+    if constexpr (kBlockMajor) {
+      const int n = min(a.rt, a.rows - t.r0), kb0 = t.c0 / 32;
+      const int kbs = min(kTileCols / 32, a.cols / 32 - kb0);
+      for (int j = threadIdx.x; j < kbs * a.rt; j += 256) {
+        const int kb = j / a.rt, r = j % a.rt;
+        if (r < n)
+          lds[kb * a.rt + r] =
+              a.scales[t.row0 * (a.cols / 32) + (long long)(kb0 + kb) * a.rows + t.r0 + r];
+      }
+      __syncthreads();
+    }
+    const int c = t.c0 + cq * 8;
+    for (int r = rr; r < a.rt; r += 8) {
+      if (t.r0 + r >= a.rows || c >= a.cols) continue;
+      const long long at = (t.row0 + t.r0 + r) * a.cols + c;
+      const uint32_t q = *reinterpret_cast<const uint32_t*>(a.codes + at / 2);
+      uint32_t byte;
+      if constexpr (kBlockMajor) byte = lds[(cq / 4) * a.rt + r];
+      else byte = a.scales[at / 32];
+      u32x4_t w = __builtin_bit_cast(u32x4_t, e2m1x8_to_bf16x8(q, e8m0_to_f32(byte)));
+      if (byte == 255) w = u32x4_t{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
+      if constexpr (kBF16) {
+        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.dst) + at) = w;
+      } else {
+        u32x4_t* p = reinterpret_cast<u32x4_t*>(static_cast<float*>(a.dst) + at);
+        p[0] = u32x4_t{w[0] << 16, w[0] & 0xffff0000u, w[1] << 16, w[1] & 0xffff0000u};
+        p[1] = u32x4_t{w[2] << 16, w[2] & 0xffff0000u, w[3] << 16, w[3] & 0xffff0000u};
+      }
+    }
+    if constexpr (kBlockMajor) __syncthreads();
+  }
+}
+
+// ---- the expert network
+
+struct MxArgs {
+  const uint8_t* A;            // gate/up: x codes [T][K / 2]; down: h units
+  const uint8_t* AS;           // gate/up: x scales [T][K / 32]; down: h scales
+  uint32_t a_bytes, as_bytes;  // gate/up
+  const int32_t* sorted_slot;
+  const int32_t* offsets;      // [El + 1]
+  int k;
+  const uint8_t* W0;           // gate or down codes
+  const uint8_t* W1;           // up codes
+  const uint8_t* S0;           // their scales [K / 32][Nout] per expert
+  const uint8_t* S1;
+  const float* topk_w;         // down: gates or null
+  uint16_t* y;                 // down: [S][Nout]
+  uint8_t* h;                  // gate/up: h units
+  uint8_t* hs;                 // gate/up: h scales
+  int El, S;
+  int K, Nout;
+  int blocked;
+};
+
+// Raw buffer resource over `bytes` bytes at `base` (wave-uniform): loads at or
+// past `bytes` read zeros instead of faulting.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+
+// Segment bounds as the caller gives them, held inside [0, S] so that no row
+// of another array is touched whatever they are.
+__device__ __forceinline__ int bound(const MxArgs& a, int e) {
+  return max(0, min(a.offsets[e], a.S));
+}
+
+// groups[e] = number of groups of 32 rows of experts before e (groups[El]: of
+// all), each expert's counted up to a multiple of kUnit, by one workgroup of
+// kThreads threads.
+template <int kThreads, int kUnit>
+__device__ __forceinline__ void group_table(const MxArgs& a, int* groups) {
+  constexpr int kPer = kMaxExperts / kThreads;
+  __shared__ int waves[kThreads / kWave];
+  int n[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
+    n[i] = 0;
+    if (e < a.El) {
+      const int rows = max(0, bound(a, e + 1) - bound(a, e));
+      n[i] = rows / (32 * kUnit) * kUnit + (rows % (32 * kUnit) ? kUnit : 0);
+    }
+    sum += n[i];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int v = __shfl_up(incl, o, kWave);
+    if (lane_id() >= o) incl += v;
+  }
+  if (lane_id() == kWave - 1) waves[threadIdx.x / kWave] = incl;
+  __syncthreads();
+  int before = incl - sum;
+  for (int w = 0; w < (int)threadIdx.x / kWave; ++w) before += waves[w];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
+    if (e <= a.El) groups[e] = before;
+    before += n[i];
+  }
+  if (a.El == kMaxExperts && threadIdx.x == kThreads - 1) groups[kMaxExperts] = before;
+  __syncthreads();
+}
+
+// The expert that holds group `g` (the last e with groups[e] <= g).
+__device__ __forceinline__ int expert_of(const int* groups, int El, int g) {
+  int lo = 0, hi = El - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (groups[mid] <= g) lo = mid;
+    else hi = mid - 1;
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// permuted weight row of MFMA row r of a 32-row block
+__device__ __forceinline__ int feat(int r) {
+  return (((r >> 2) & 1) << 4) | (((r >> 3) & 3) << 2) | (r & 3);
+}
+
+__device__ __forceinline__ f32x16_t mfma_mx(u32x4_t a, u32x4_t b, f32x16_t c, uint32_t sa, uint32_t sb) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const i32x8_t av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8_t bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
+#else
+  (void)a;
+  (void)b;
+  (void)sa;
+  (void)sb;
+  return c;
+#endif
+}
+
+// Epilogue of a gate/up pair: 16 consecutive features of token row r of group
+// `grp` (lane half g), feature block fb: silu(gate) * up in float32, converted
+// to MXFP4 with the other half's 16 features.
+__device__ __forceinline__ void store_h(const MxArgs& a, const f32x16_t& gate, const f32x16_t& up,
+                                        int grp, int fb, int l) {
+  float h[16];
+  uint32_t top = 0;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    h[q] = silu_f32(gate[q]) * up[q];
+    top = max(top, __float_as_uint(h[q]) & 0x7fffffffu);
+  }
+  top = max(top, (uint32_t)__shfl_xor((int)top, 32, kWave));
+  const uint32_t byte = mx_scale_byte(top);
+  const float inv = mx_inverse(byte);
+  u32x2_t q = {mx_codes8(h, inv), mx_codes8(h + 8, inv)};
+  if (byte == 255) q = u32x2_t{0, 0};
+  const int F = a.Nout, r = l & 31, g = l >> 5;
+  *reinterpret_cast<u32x2_t*>(a.h + ((long long)grp * (F / 64) + (fb >> 1)) * 1024 +
+                              ((fb & 1) * 32 + r) * 16 + 8 * g) = q;
+  if (g == 0)
+    a.hs[((long long)grp * (F / 128) + (fb >> 2)) * 128 + r * 4 + (fb & 3)] = (uint8_t)byte;
+}
+
+// Epilogue of a down block: 16 consecutive columns of row p.
+__device__ __forceinline__ void store_y(const MxArgs& a, const f32x16_t& v, int p, int col, float gw) {
+  uint16_t* o = a.y + (long long)p * a.Nout + col;
+  float h[16];
+#pragma unroll
+  for (int q = 0; q < 16; ++q) h[q] = v[q] * gw;
+  *reinterpret_cast<u32x4_t*>(o) = u32x4_t{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]),
+                                           pack_bf16x2(h[4], h[5]), pack_bf16x2(h[6], h[7])};
+  *reinterpret_cast<u32x4_t*>(o + 8) = u32x4_t{pack_bf16x2(h[8], h[9]), pack_bf16x2(h[10], h[11]),
+                                               pack_bf16x2(h[12], h[13]), pack_bf16x2(h[14], h[15])};
+}
+
+// -- few rows per expert: weights streamed by each wave into registers.
+// An item is a group of 32 rows and kNB weight blocks of 32 rows (gate/up: two
+// gate blocks and the up blocks of the same features); the four waves of a
+// workgroup take a quarter of K each and add their results through LDS, so
+// that a handful of experts still fills the chip.  A wave keeps kD steps of
+// 64 K values in flight; nothing passes LDS before the results.
+constexpr int kNB = 4;
+constexpr int kD = 4;
+
+template <bool kGateUp>
+__global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxArgs a) {
+  constexpr int H = kGateUp ? 2 : 4;  // output blocks of an item
+  __shared__ int groups[kMaxExperts + 1];
+  __shared__ f32x4_t red[4][kNB][4][kWave];  // [wave][block][registers 4q ..][lane]
+  group_table<256, 1>(a, groups);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int l = lane_id(), g = l >> 5, r = l & 31;
+  const int nS = a.K / 64, ngrp = a.Nout / (32 * H);
+  const int n_items = groups[a.El] * ngrp;
+  const int per_xcd = (n_items + kNumXcd - 1) / kNumXcd;
+  const int xcd = blockIdx.x % kNumXcd, slots = gridDim.x / kNumXcd;
+  const int end = min(n_items, (xcd + 1) * per_xcd);
+  const int s0 = nS * wave / 4, s1 = nS * (wave + 1) / 4;
+  const uint32_t wrow = (uint32_t)a.K / 2, wmat = (uint32_t)a.Nout * wrow;
+  const uint32_t smat = (uint32_t)(a.K / 32) * a.Nout;
+  const uint32_t unit = a.blocked ? 1024u : 32u;
+  const uint32_t voffW = a.blocked ? 16u * l : (uint32_t)feat(r) * wrow + 16u * g;
+  const uint32_t voffS = (uint32_t)g * a.Nout + feat(r);
+  for (int it = xcd * per_xcd + (int)blockIdx.x / kNumXcd; it < end; it += slots) {
+    const int e = expert_of(groups, a.El, it / ngrp);
+    const int m_tiles = __builtin_amdgcn_readfirstlane(groups[e + 1] - groups[e]);
+    const int in = it - groups[e] * ngrp;
+    const int nb = __builtin_amdgcn_readfirstlane(in / m_tiles);       // feature group
+    const int mt = __builtin_amdgcn_readfirstlane(in % m_tiles);
+    const int grp = __builtin_amdgcn_readfirstlane(groups[e]) + mt;
+    const int row0 = __builtin_amdgcn_readfirstlane(bound(a, e)) + mt * 32;
+    const int rend = __builtin_amdgcn_readfirstlane(bound(a, e + 1));
+    const int p = min(row0 + r, rend - 1);
+    __amdgpu_buffer_rsrc_t rA, rAS;
+    uint32_t voffA, voffAS;
+    const int slot = a.sorted_slot[p];
+    if constexpr (kGateUp) {
+      const uint32_t t = (uint32_t)slot / (uint32_t)a.k;
+      rA = rsrc(a.A, a.a_bytes);
+      rAS = rsrc(a.AS, a.as_bytes);
+      voffA = t * wrow + 16u * g;
+      voffAS = t * (uint32_t)(a.K / 32) + g;
+    } else {
+      rA = rsrc(a.A + (long long)grp * nS * 1024, (uint32_t)nS * 1024u);
+      rAS = rsrc(a.AS + (long long)grp * (nS / 2) * 128, (uint32_t)(nS / 2) * 128u);
+      voffA = 16u * l;
+      voffAS = 4u * r + g;
+    }
+    const __amdgpu_buffer_rsrc_t rW0 = rsrc(a.W0 + (size_t)e * wmat, wmat);
+    const __amdgpu_buffer_rsrc_t rW1 = kGateUp ? rsrc(a.W1 + (size_t)e * wmat, wmat) : rW0;
+    const __amdgpu_buffer_rsrc_t rS0 = rsrc(a.S0 + (size_t)e * smat, smat);
+    const __amdgpu_buffer_rsrc_t rS1 = kGateUp ? rsrc(a.S1 + (size_t)e * smat, smat) : rS0;
+    u32x4_t wb[kD][kNB], tb[kD];
+    uint32_t ws[kD][kNB], ts[kD];
+    auto issue = [&](int s, int d) {
+#pragma unroll
+      for (int n = 0; n < kNB; ++n) {
+        const int fb = nb * H + n % H;
+        wb[d][n] = __builtin_amdgcn_raw_buffer_load_b128(n >= H ? rW1 : rW0, voffW,
+                                                         (uint32_t)fb * 32u * wrow + s * unit, 2);
+        ws[d][n] = __builtin_amdgcn_raw_buffer_load_b8(n >= H ? rS1 : rS0, voffS,
+                                                       (uint32_t)(2 * s) * a.Nout + fb * 32u, 0);
+      }
+      tb[d] = __builtin_amdgcn_raw_buffer_load_b128(rA, voffA, s * (kGateUp ? 32u : 1024u), 0);
+      ts[d] = __builtin_amdgcn_raw_buffer_load_b8(
+          rAS, voffAS, kGateUp ? 2u * s : (uint32_t)(s >> 1) * 128u + 2u * (s & 1), 0);
+    };
+    f32x16_t acc[kNB];
+#pragma unroll
+    for (int n = 0; n < kNB; ++n) acc[n] = f32x16_t{};
+#pragma unroll
+    for (int d = 0; d < kD; ++d)
+      if (s0 + d < s1) issue(s0 + d, d);
+    for (int s = s0; s < s1; s += kD) {
+#pragma unroll
+      for (int d = 0; d < kD; ++d) {
+        if (s + d < s1) {
+#pragma unroll
+          for (int n = 0; n < kNB; ++n) acc[n] = mfma_mx(wb[d][n], tb[d], acc[n], ws[d][n], ts[d]);
+          if (s + d + kD < s1) issue(s + d + kD, d);
+        }
+      }
+    }
+    const float gw = !kGateUp && a.topk_w ? a.topk_w[slot] : 1.0f;
+    // results of block n meet in wave n (gate/up: of pair n in wave n)
+    __syncthreads();  // the last item's sums have been read
+#pragma unroll
+    for (int n = 0; n < kNB; ++n) {
+      if (n % H == wave) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        red[wave][n][q][l] = f32x4_t{acc[n][4 * q], acc[n][4 * q + 1], acc[n][4 * q + 2], acc[n][4 * q + 3]};
+    }
+    __syncthreads();
+    if (wave < H) {
+      // in wave order whichever wave adds
+      f32x16_t sum[kNB / H];
+#pragma unroll
+      for (int i = 0; i < kNB / H; ++i) {
+        sum[i] = f32x16_t{};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+#pragma unroll
+          for (int n = 0; n < kNB; ++n) {
+            if (n != i * H + wave) continue;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f32x4_t v = w == wave ? f32x4_t{acc[n][4 * q], acc[n][4 * q + 1], acc[n][4 * q + 2], acc[n][4 * q + 3]}
+                                          : red[w][n][q][l];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) sum[i][4 * q + j] += v[j];
+            }
+          }
+        }
+      }
+      const int fb = nb * H + wave;
+      if constexpr (kGateUp) store_h(a, sum[0], sum[1], grp, fb, l);
+      else if (row0 + r < rend) store_y(a, sum[0], row0 + r, fb * 32 + 16 * g, gw);
+    }
+  }
+}
+
+// -- many rows per expert: tiles of 128 rows x 256 weight rows (gate/up: 128
+// gate and the up rows of the same features) through a ring of LDS stages of
+// 128 K values, filled by LDS-DMA in operand order.  Four waves of 64 x 128;
+// two workgroups a CU, so that the conversion of one's results runs beside the
+// other's products.
+constexpr int kBM = 4;        // groups of 32 rows of a tile
+constexpr int kStages = 3;
+constexpr int kStageA = kBM * 2 * 1024;
+constexpr int kStageW = 8 * 2 * 1024;
+constexpr int kStageAS = kBM * 32 * 4;
+constexpr int kStageWS = 4 * 256;
+constexpr int kStage = kStageA + kStageW + kStageAS + kStageWS;
+constexpr int kTileLds = kStages * kStage;
+
+// One LDS-DMA load per active lane: lane i's 16 (4) bytes, from voff + soff in
+// the buffer, land at lds + 16 i (4 i); lds is wave-uniform.
+__device__ __forceinline__ void lds_dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, unsigned char* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, soff, 0, 0);
+#else
+  (void)r, (void)voff, (void)soff, (void)lds;
+#endif
+}
+
+__device__ __forceinline__ void lds_dma4(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, unsigned char* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, voff, soff, 0, 0);
+#else
+  (void)r, (void)voff, (void)soff, (void)lds;
+#endif
+}
+
+// At most N vector-memory operations of this wave are outstanding, its LDS
+// reads have returned, and then so for the whole workgroup.  (No fence, which
+// would wait for every load in flight.)
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (0 << 8) | ((N >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <bool kGateUp>
+__global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  __shared__ int groups[kMaxExperts + 1];
+  group_table<256, kBM>(a, groups);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int l = lane_id(), g = l >> 5, r = l & 31;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int nK = a.K / 128;
+  const int cols = kGateUp ? 128 : 256;  // output columns of a tile
+  const int ntn = (a.Nout + cols - 1) / cols;
+  const uint32_t wrow = (uint32_t)a.K / 2, wmat = (uint32_t)a.Nout * wrow;
+  const uint32_t smat = (uint32_t)(a.K / 32) * a.Nout;
+  const uint32_t unit = a.blocked ? 1024u : 32u;
+  const uint32_t voffW = a.blocked ? 16u * l : (uint32_t)feat(r) * wrow + 16u * g;
+  const int n_items = groups[a.El] / kBM * ntn;
+  const int per_xcd = (n_items + kNumXcd - 1) / kNumXcd;
+  const int xcd = blockIdx.x % kNumXcd, slots = gridDim.x / kNumXcd;
+  const int end = min(n_items, (xcd + 1) * per_xcd);
+  for (int it = xcd * per_xcd + (int)blockIdx.x / kNumXcd; it < end; it += slots) {
+    const int e = expert_of(groups, a.El, it / ntn * kBM);
+    const int m_tiles = __builtin_amdgcn_readfirstlane(groups[e + 1] - groups[e]) / kBM;
+    const int in = it - groups[e] / kBM * ntn;
+    const int nt = __builtin_amdgcn_readfirstlane(in / m_tiles);
+    const int mt = __builtin_amdgcn_readfirstlane(in % m_tiles);
+    const int g0 = __builtin_amdgcn_readfirstlane(groups[e]) + mt * kBM;
+    const int row0 = __builtin_amdgcn_readfirstlane(bound(a, e)) + mt * kBM * 32;
+    const int rend = __builtin_amdgcn_readfirstlane(bound(a, e + 1));
+    // this wave's LDS-DMA: A blocks `wave` (both steps), W blocks wave and
+    // wave + 4 (both steps), rows' scales, and K block `wave` of the weights'
+    __amdgpu_buffer_rsrc_t rA, rAS;
+    uint32_t voffA, voffAS, stepA, stepAS;
+    if constexpr (kGateUp) {
+      const int slot = a.sorted_slot[min(row0 + wave * 32 + r, rend - 1)];
+      const uint32_t t = (uint32_t)slot / (uint32_t)a.k;
+      const int sslot = a.sorted_slot[min(row0 + (wave & 1) * 64 + l, rend - 1)];
+      rA = rsrc(a.A, a.a_bytes);
+      rAS = rsrc(a.AS, a.as_bytes);
+      voffA = t * wrow + 16u * g;
+      voffAS = (uint32_t)sslot / (uint32_t)a.k * (uint32_t)(a.K / 32);
+      stepA = 32;
+      stepAS = 4;
+    } else {
+      // (all kBM groups of the tile exist; rows behind the segment hold whatever
+      // was there and only reach results that are not stored)
+      rA = rsrc(a.A + (long long)(g0 + wave) * (2 * nK) * 1024, (uint32_t)nK * 2048u);
+      rAS = rsrc(a.AS + (long long)g0 * nK * 128, (uint32_t)(kBM * nK) * 128u);
+      voffA = 16u * l;
+      voffAS = (uint32_t)((wave & 1) * 2 + g) * nK * 128u + 4u * r;
+      stepA = 1024;
+      stepAS = 128;
+    }
+    const uint32_t f0 = (uint32_t)nt * cols;
+    const __amdgpu_buffer_rsrc_t rW0 = rsrc(a.W0 + (size_t)e * wmat, wmat);
+    const __amdgpu_buffer_rsrc_t rW1 = kGateUp ? rsrc(a.W1 + (size_t)e * wmat, wmat) : rW0;
+    // (down, 128 columns left: the second half repeats the first and is not stored)
+    const uint32_t sW0 = (f0 + 32u * wave) * wrow;
+    const uint32_t sW1 = kGateUp || f0 + 128u >= (uint32_t)a.Nout ? sW0 : sW0 + 128u * wrow;
+    // scales of one K block: 4 rows a lane (gate/up: 32 lanes for either matrix)
+    const __amdgpu_buffer_rsrc_t rS0 = rsrc(a.S0 + (size_t)e * smat, smat);
+    const __amdgpu_buffer_rsrc_t rS1 = kGateUp ? rsrc(a.S1 + (size_t)e * smat, smat) : rS0;
+    const uint32_t voffS = (uint32_t)wave * a.Nout + f0 + 4u * (kGateUp ? l & 31 : l);
+    auto issue = [&](int s, int slot) {
+      unsigned char* st = lds + slot * kStage;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        lds_dma16(rA, voffA, (uint32_t)(2 * s + q) * stepA, st + (wave * 2 + q) * 1024);
+        lds_dma16(rW0, voffW, sW0 + (uint32_t)(2 * s + q) * unit, st + kStageA + (wave * 2 + q) * 1024);
+        lds_dma16(rW1, voffW, sW1 + (uint32_t)(2 * s + q) * unit, st + kStageA + ((wave + 4) * 2 + q) * 1024);
+      }
+      unsigned char* sc = st + kStageA + kStageW;
+      lds_dma4(rAS, voffAS, (uint32_t)s * stepAS, sc + (wave & 1) * 256);
+      sc += kStageAS + wave * 256;
+      if constexpr (kGateUp) {
+        if (g == 0) {
+          lds_dma4(rS0, voffS, (uint32_t)(4 * s) * a.Nout, sc);
+          lds_dma4(rS1, voffS, (uint32_t)(4 * s) * a.Nout, sc + 128);
+        }
+      } else {
+        lds_dma4(rS0, voffS, (uint32_t)(4 * s) * a.Nout, sc);
+      }
+    };
+    f32x16_t acc[2][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) acc[m][n] = f32x16_t{};
+    // LDS-DMA instructions of a wave per stage
+    constexpr int kIssued = kGateUp ? 9 : 8;
+    static_assert(kStages == 3, "one stage is in flight behind the one waited for");
+    issue(0, 0);
+    if (nK > 1) issue(1, 1);
+    int slot = 0;
+    for (int s = 0; s < nK; ++s, slot = slot == kStages - 1 ? 0 : slot + 1) {
+      if (s + 1 < nK) stage_barrier<kIssued>();
+      else stage_barrier<0>();
+      // (every wave has read stage s - 1, whose place this one takes)
+      if (s + 2 < nK) issue(s + 2, slot == 0 ? 2 : slot - 1);
+      const unsigned char* st = lds + slot * kStage;
+      const unsigned char* sc = st + kStageA + kStageW;
+      uint32_t as[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        as[m] = *reinterpret_cast<const uint32_t*>(sc + ((wm * 2 + m) * 32 + r) * 4) >> (8 * g);
+      sc += kStageAS;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        u32x4_t av[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          av[m] = *reinterpret_cast<const u32x4_t*>(st + ((wm * 2 + m) * 2 + q) * 1024 + 16 * l);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int b = kGateUp ? (n >> 1) * 4 + wn * 2 + (n & 1) : wn * 4 + n;
+          const u32x4_t wv = *reinterpret_cast<const u32x4_t*>(st + kStageA + (b * 2 + q) * 1024 + 16 * l);
+          const uint32_t ws = sc[(2 * q + g) * 256 + b * 32 + feat(r)];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) acc[m][n] = mfma_mx(wv, av[m], acc[m][n], ws, as[m] >> (16 * q));
+        }
+      }
+    }
+    stage_barrier<0>();  // every wave has read its last stage
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int grp = g0 + wm * 2 + m;
+      if (row0 + (wm * 2 + m) * 32 >= rend) continue;
+      const int p = row0 + (wm * 2 + m) * 32 + r;
+      if constexpr (kGateUp) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) store_h(a, acc[m][n], acc[m][n + 2], grp, nt * 4 + wn * 2 + n, l);
+      } else if (p < rend) {
+        const float gw = a.topk_w ? a.topk_w[a.sorted_slot[p]] : 1.0f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int col = nt * 256 + wn * 128 + n * 32 + 16 * g;
+          if (col < a.Nout) store_y(a, acc[m][n], p, col, gw);
+        }
+      }
+    }
+  }
+}
+
+// Which kernel takes a problem.
+bool use_tiles(const Shape& s) { return s.S >= 64LL * s.El; }
+
+// Groups of 32 rows that the experts' segments can have.
+size_t max_groups(const Shape& s) {
+  return (size_t)(s.S / 32 + std::min<long long>(s.S, s.El) * (use_tiles(s) ? kBM : 1));
+}
+
+template <bool kGateUp>
+hipError_t launch_products(const Shape& s, const MxArgs& a, hipStream_t st) {
+  if (!use_tiles(s)) {
+    const long long items = (long long)max_groups(s) * (a.Nout / (kGateUp ? 64 : 128));
+    const int grid = (int)std::min(512LL, (items + 7) / 8 * 8);
+    hipLaunchKernelGGL(mx_stream_kernel<kGateUp>, dim3(grid), dim3(256), 0, st, a);
+    return hipGetLastError();
+  }
+  static std::atomic<uint64_t> done{0};
+  const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(mx_tile_kernel<kGateUp>), kTileLds, done);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(mx_tile_kernel<kGateUp>, dim3(512), dim3(256), kTileLds, st, a);
+  return hipGetLastError();
+}
+
+template <bool kQuantize>
+hipError_t convert(int batch, int rows, int cols, int bf16, const void* src, void* dst, uint8_t* codes,
+                   uint8_t* scales, int block_major, hipStream_t st) {
+  ConvertArgs a{src, dst, codes, scales, rows, cols, 8, 0, 0, 0};
+  a.col_tiles = (cols + kTileCols - 1) / kTileCols;
+  // block-major scales in runs of 64 bytes where that leaves work for the chip
+  if (block_major && (long long)batch * ((rows + 63) / 64) * a.col_tiles >= 1024) a.rt = kMaxTileRows;
+  a.row_tiles = (rows + a.rt - 1) / a.rt;
+  a.tiles = (long long)batch * a.row_tiles * a.col_tiles;
+  const unsigned grid = (unsigned)std::min(a.tiles, 1LL << 20);
+  auto go = [&](auto b, auto m) {
+    if constexpr (kQuantize)
+      hipLaunchKernelGGL((mx_quantize_kernel<b.value, m.value>), dim3(grid), dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((mx_dequantize_kernel<b.value, m.value>), dim3(grid), dim3(256), 0, st, a);
+  };
+  using std::false_type;
+  using std::true_type;
+  if (bf16) block_major ? go(true_type{}, true_type{}) : go(true_type{}, false_type{});
+  else block_major ? go(false_type{}, true_type{}) : go(false_type{}, false_type{});
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t mx_quantize(int batch, int rows, int cols, int bf16, const void* src, uint8_t* codes,
+                       uint8_t* scales, int block_major, hipStream_t st) {
+  return convert<true>(batch, rows, cols, bf16, src, nullptr, codes, scales, block_major, st);
+}
+
+hipError_t mx_dequantize(int batch, int rows, int cols, int bf16, const uint8_t* codes,
+                         const uint8_t* scales, void* dst, int block_major, hipStream_t st) {
+  return convert<false>(batch, rows, cols, bf16, nullptr, dst, const_cast<uint8_t*>(codes),
+                        const_cast<uint8_t*>(scales), block_major, st);
+}
+
+size_t mx_ffn_ws_bytes(const Shape& s) {
+  return align_up(max_groups(s) * (s.F / 64) * 1024) + align_up(max_groups(s) * (s.F / 128) * 128 + 256);
+}
+
+hipError_t expert_ffn_mx(const Shape& s, const uint8_t* x, const uint8_t* xs, const int32_t* sorted_slot,
+                         const int32_t* offsets, const void* w_gate, const void* w_up,
+                         const void* w_down, const void* s_gate, const void* s_up,
+                         const void* s_down, const float* topk_w, void* y, void* ws, hipStream_t st) {
+  uint8_t* h = static_cast<uint8_t*>(ws);
+  uint8_t* hs = h + align_up(max_groups(s) * (s.F / 64) * 1024);
+  MxArgs a{};
+  a.A = x;
+  a.AS = xs;
+  a.a_bytes = (uint32_t)((long long)s.T * s.d / 2);
+  a.as_bytes = (uint32_t)((long long)s.T * s.d / 32);
+  a.sorted_slot = sorted_slot;
+  a.offsets = offsets;
+  a.k = s.k;
+  a.W0 = static_cast<const uint8_t*>(w_gate);
+  a.W1 = static_cast<const uint8_t*>(w_up);
+  a.S0 = static_cast<const uint8_t*>(s_gate);
+  a.S1 = static_cast<const uint8_t*>(s_up);
+  a.h = h;
+  a.hs = hs;
+  a.El = s.El;
+  a.S = (int)s.S;
+  a.K = s.d;
+  a.Nout = s.F;
+  a.blocked = s.blocked;
+  hipError_t e = launch_products<true>(s, a, st);
+  if (e != hipSuccess) return e;
+  a.A = h;
+  a.AS = hs;
+  a.W0 = static_cast<const uint8_t*>(w_down);
+  a.W1 = nullptr;
+  a.S0 = static_cast<const uint8_t*>(s_down);
+  a.S1 = nullptr;
+  a.topk_w = topk_w;
+  a.y = static_cast<uint16_t*>(y);
+  a.K = s.F;
+  a.Nout = s.d;
+  return launch_products<false>(s, a, st);
+}
+
+}  // namespace moe

@@ -1,0 +1,246 @@
+"""4-bit conversion bit for bit against 64 bits, and the 4-bit expert network
+within the bounds of tests/mx_reference.py, on both of its kernels."""
+import pytest
+import torch
+
+import mx_reference as R
+from mixture_experts_layer_15_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+ACT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.load_library()
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _convert(v, layout):
+    """v [batch, rows, cols] -> codes, scales from the library, with a guard behind each."""
+    b, r, c = v.shape
+    n = b * r * c
+    codes = torch.full((n // 2 + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+    scales = torch.full((n // 32 + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+    B.moe_mx_quantize(v, codes[:n // 2], scales[:n // 32], layout)
+    assert (codes[n // 2:] == 0xA5).all() and (scales[n // 32:] == 0xA5).all()
+    shape = (b, c // 32, r) if layout == B.MOE_MX_SCALES_BLOCK else (b, r, c // 32)
+    return codes[:n // 2].view(b, r, c // 2), scales[:n // 32].view(shape)
+
+
+def _check(v):
+    b, r, c = v.shape
+    code, byte = R.quantize(v.reshape(b * r, c))
+    for layout in (B.MOE_MX_SCALES_ROW, B.MOE_MX_SCALES_BLOCK):
+        codes, scales = _convert(v, layout)
+        rows = scales.transpose(1, 2) if layout == B.MOE_MX_SCALES_BLOCK else scales
+        assert torch.equal(rows.reshape(b * r, -1), byte), "scales"
+        assert torch.equal(codes.reshape(b * r, -1), R.pack(code)), "codes"
+        want = R.values(codes, rows)
+        for t in (torch.float32, torch.bfloat16):
+            back = torch.full(v.shape, 9.0, dtype=t, device=DEV)
+            B.moe_mx_dequantize(codes.contiguous(), scales.contiguous(), back, layout)
+            assert torch.equal(back.double().nan_to_num(nan=1e30), want.nan_to_num(nan=1e30)), t
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("batch,rows,cols", [(1, 1, 32), (1, 7, 96), (3, 9, 288), (2, 65, 2048), (5, 64, 256), (1, 1000, 640), (129, 130, 2080),
+                                             (1, 3, 65536)])
+def test_conversion(act, batch, rows, cols):
+    g = _gen(rows * cols)
+    v = torch.randn(batch, rows, cols, generator=g, device=DEV) * torch.exp2(torch.randint(-20, 20, (batch, rows, cols), generator=g, device=DEV).float() / 4)
+    v[0, 0, :32] = 0
+    v[:, -1, -32:] *= -1e-30
+    _check(v.to(ACT[act]))
+
+
+def test_every_bfloat16_value_under_several_maxima():
+    """Each of the 65536 patterns beside a largest value that sets the block's scale: ties, subnormals, infinities, NaN."""
+    bits = torch.arange(65536, device=DEV, dtype=torch.int32)
+    v = (bits << 16).view(torch.float32)
+    for up in (0.0, 1.0, 1.75, 4.0, 100.0):
+        block = v[:, None].repeat(1, 32)
+        block[:, 1::2] = -block[:, 1::2]
+        block[:, 31] = v * up if up else v
+        _check(block.to(torch.bfloat16)[None])
+
+
+def test_values_at_and_beside_every_border():
+    """float32 values at each border between two codes, one step below and above, at many scales."""
+    edges = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0, 7.9999], device=DEV)
+    near = torch.cat([edges, torch.nextafter(edges, torch.zeros_like(edges)), torch.nextafter(edges, torch.full_like(edges, 9.0))])
+    row = torch.zeros(32, device=DEV)
+    row[:30] = near
+    row[31] = 4.0
+    e = torch.arange(-149, 126, device=DEV, dtype=torch.float64)
+    v = (row.double()[None] * torch.exp2(e)[:, None])
+    v = torch.where(v.abs() > 3.4e38, 0.0, v).float()
+    v[:, 1::2] *= -1
+    _check(v[None])
+
+
+def test_infinities_and_nan():
+    v = torch.ones(1, 6, 64, device=DEV)
+    v[0, 0, 3], v[0, 1, 40], v[0, 2, 31], v[0, 3, 32] = float("inf"), -float("inf"), float("nan"), -float("nan")
+    v[0, 4] = -0.0
+    for t in ACT.values():
+        _check(v.to(t))
+        _, s = _convert(v.to(t), B.MOE_MX_SCALES_ROW)
+        assert (s[0] == 255).sum() == 4 and s[0, 4].tolist() == [127, 127]
+
+
+def _weights(El, F, d, g, spread=2):
+    w = {}
+    for n, rows, K in (("gate", F, d), ("up", F, d), ("down", d, F)):
+        w["w_" + n] = torch.randint(0, 256, (El, rows, K // 2), generator=g, device=DEV, dtype=torch.uint8)
+        top = 127 - int(round(torch.log2(torch.tensor(2.9 * K ** 0.5)).item()))
+        w["s_" + n] = torch.randint(top - spread, top + spread, (El, K // 32, rows), generator=g, device=DEV, dtype=torch.uint8)
+    return w
+
+
+def _packed(p, w):
+    out = dict(w)
+    for which, n in ((0, "gate"), (0, "up"), (1, "down")):
+        out["w_" + n] = torch.empty_like(w["w_" + n])
+        B.moe_pack_weights(p, which, w["w_" + n], out["w_" + n])
+    return out
+
+
+def _dispatch(p, idx):
+    counts = torch.empty(p.num_local, dtype=torch.int32, device=DEV)
+    offsets = torch.empty(p.num_local + 1, dtype=torch.int32, device=DEV)
+    order, pos = torch.empty_like(idx).view(-1), torch.empty_like(idx).view(-1)
+    B.moe_permute(p, idx, counts, offsets, order, pos, B.workspace(p, B.MOE_CALL_PERMUTE, DEV))
+    return offsets, order
+
+
+def _ids(T, E, k, g, skew):
+    logits = torch.randn(T, E, generator=g, device=DEV)
+    logits -= skew * torch.arange(E, device=DEV)
+    return torch.topk(logits, k, dim=1).indices.to(torch.int32).contiguous()
+
+
+# T, d, E, k, F, first local expert, local experts, skew of the load
+CASES = [
+    (1, 128, 4, 2, 128, 0, 4, 0.0), (1, 2048, 128, 8, 768, 0, 128, 0.0), (5, 256, 8, 8, 384, 2, 3, 0.0), (33, 640, 20, 3, 384, 0, 20, 0.3),
+    (64, 128, 512, 1, 256, 0, 512, 0.0), (31, 384, 512, 4, 128, 100, 400, 0.0), (200, 256, 4, 1, 128, 0, 4, 3.0),
+    # tiles of 128 rows
+    (128, 128, 2, 1, 128, 0, 2, 0.0), (300, 384, 4, 2, 640, 0, 4, 0.5), (257, 640, 6, 3, 384, 1, 4, 1.0), (1001, 128, 20, 3, 128, 0, 20, 0.2),
+    (513, 2048, 2, 1, 768, 0, 1, 0.0), (700, 256, 512, 100, 128, 3, 509, 0.05),
+]
+
+
+@pytest.mark.parametrize("blocked", [False, True])
+@pytest.mark.parametrize("T,d,E,k,F,e0,El,skew", CASES)
+def test_expert_network(T, d, E, k, F, e0, El, skew, blocked):
+    g = _gen(T * d + E)
+    p = B.problem(T, d, E, k, F, e0, El, "bf16", "mxfp4", blocked)
+    w = _weights(El, F, d, g)
+    kept = _packed(p, w) if blocked else w
+    offsets, order = _dispatch(p, _ids(T, E, k, g, skew))
+    x = (torch.randn(T, d, generator=g, device=DEV) * torch.exp(torch.randn(d, generator=g, device=DEV))).to(torch.bfloat16)
+    codes, scales = _convert(x[None], B.MOE_MX_SCALES_ROW)
+    gates = torch.rand(T * k, generator=g, device=DEV)
+    ws = B.workspace(p, B.MOE_CALL_EXPERT_FFN_MX, DEV).fill_(0xFF)
+    rows = R.values(codes[0], scales[0])
+    off = offsets.tolist()
+    for tw in (gates, None):
+        y = torch.full((T * k, d), 7.0, dtype=torch.bfloat16, device=DEV)
+        B.moe_expert_ffn_mx(p, codes.contiguous(), scales.contiguous(), order, offsets, kept["w_gate"], kept["w_up"], kept["w_down"],
+                            w["s_gate"], w["s_up"], w["s_down"], tw, y, ws)
+        assert (y[off[-1]:] == 7.0).all()
+        step = max(1, El // 25)    # a sample of the experts where there are many, the fullest among them
+        full = max(range(El), key=lambda j: off[j + 1] - off[j])
+        for j in sorted(set(range(0, El, step)) | {full, El - 1}):
+            lo, hi = off[j], off[j + 1]
+            if lo == hi:
+                continue
+            slot = order[lo:hi].long()
+            m = [R.values(w["w_" + n][j], w["s_" + n][j].t()) for n in ("gate", "up", "down")]
+            want, err = R.expert(rows[slot // k], *m)
+            if tw is not None:
+                want, err = want * tw[slot, None].double(), err * tw[slot, None].double()
+            got = y[lo:hi].double()
+            assert torch.isfinite(got).all()
+            over = (got - want).abs() - (err + (want.abs() + err) * (2.0 ** -8 + 2 * R.U))
+            assert float(over.max()) <= 0, (j, float(over.max()), float((got - want).abs().max()), float(want.abs().max()))
+            # and as a whole, where a border met by chance cannot hide anything
+            rel = float((got - want).norm() / want.norm())
+            assert rel < 2.0 ** -8, (j, rel)
+
+
+@pytest.mark.parametrize("T", [8, 300])
+def test_wide_scales_and_nan(T):
+    """Scales over the whole range that float32 sums hold, and a token with a NaN: its rows alone are NaN."""
+    d, E, k, F = 256, 4, 2, 256
+    g = _gen(T)
+    p = B.problem(T, d, E, k, F, 0, E, "bf16", "mxfp4")
+    w = _weights(E, F, d, g, spread=12)
+    offsets, order = _dispatch(p, _ids(T, E, k, g, 0.0))
+    x = torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16)
+    x[T // 2, 5] = float("nan")
+    x[T // 3, 7] = float("inf")
+    codes, scales = _convert(x[None], B.MOE_MX_SCALES_ROW)
+    scales[0, 0, 0] = 60         # a block far below the others of its row
+    rows = R.values(codes[0], scales[0])
+    y = torch.zeros(T * k, d, dtype=torch.bfloat16, device=DEV)
+    B.moe_expert_ffn_mx(p, codes.contiguous(), scales.contiguous(), order, offsets, w["w_gate"], w["w_up"], w["w_down"], w["s_gate"], w["s_up"],
+                        w["s_down"], None, y, B.workspace(p, B.MOE_CALL_EXPERT_FFN_MX, DEV).fill_(0xFF))
+    off = offsets.tolist()
+    for j in range(E):
+        slot = order[off[j]:off[j + 1]].long()
+        t = slot // k
+        got = y[off[j]:off[j + 1]].double()
+        bad = (t == T // 2) | (t == T // 3)
+        assert torch.isnan(got[bad]).all()
+        m = [R.values(w["w_" + n][j], w["s_" + n][j].t()) for n in ("gate", "up", "down")]
+        want, err = R.expert(rows[t[~bad]], *m)
+        over = (got[~bad] - want).abs() - (err + (want.abs() + err) * (2.0 ** -8 + 2 * R.U))
+        assert not over.numel() or float(over.max()) <= 0
+
+
+def test_rows_and_blocked_layouts_agree_and_captured():
+    """Both layouts give the same bits; a captured graph with the conversion replays on new tokens as the eager calls do."""
+    for T in (16, 400):
+        d, E, k, F = 640, 8, 4, 384
+        g = _gen(T)
+        p, pb = (B.problem(T, d, E, k, F, 0, E, "bf16", "mxfp4", b) for b in (False, True))
+        w = _weights(E, F, d, g)
+        kept = _packed(pb, w)
+        offsets, order = _dispatch(p, _ids(T, E, k, g, 0.2))
+        x = torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16)
+        codes = torch.empty(T, d // 2, dtype=torch.uint8, device=DEV)
+        scales = torch.empty(T, d // 32, dtype=torch.uint8, device=DEV)
+        ws = B.workspace(p, B.MOE_CALL_EXPERT_FFN_MX, DEV)
+
+        def step(prob, mats, y, wsp, stream=None):
+            B.moe_mx_quantize(x, codes, scales, stream=stream)
+            B.moe_expert_ffn_mx(prob, codes, scales, order, offsets, mats["w_gate"], mats["w_up"], mats["w_down"], w["s_gate"], w["s_up"],
+                                w["s_down"], None, y, wsp, stream=stream)
+        y = torch.zeros(T * k, d, dtype=torch.bfloat16, device=DEV)
+        step(p, w, y, ws)
+        yb = torch.zeros_like(y)
+        step(pb, kept, yb, ws)
+        assert torch.equal(y, yb)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(p, w, y, ws)
+        side = torch.cuda.Stream()
+        for _ in range(3):
+            x.copy_(torch.randn(T, d, generator=g, device=DEV))
+            y.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            again = torch.zeros_like(y)
+            torch.cuda.synchronize()
+            step(pb, kept, again, B.workspace(p, B.MOE_CALL_EXPERT_FFN_MX, DEV), stream=side)
+            side.synchronize()
+            assert torch.equal(again, y)
