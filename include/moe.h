@@ -126,7 +126,8 @@ typedef enum {
   MOE_CALL_ROUTE_BACKWARD = 5,
   MOE_CALL_NORM_BACKWARD = 6,
   MOE_CALL_COMBINE_NORM_BACKWARD = 7,
-  MOE_CALL_EXPERT_FFN_MX = 8
+  MOE_CALL_EXPERT_FFN_MX = 8,
+  MOE_CALL_FORWARD_FEW = 9
 } moe_call_t;
 
 /* Layout of the expert weight matrices. */
@@ -290,6 +291,34 @@ moe_status_t moe_forward(const moe_problem_t* p, const moe_forward_args_t* a, vo
 
 moe_status_t moe_forward_noalloc(const moe_problem_t* p, const moe_forward_args_t* a,
                                  void* stream);
+
+/* ---- The whole layer for a few tokens ----
+ *
+ * moe_forward for at most MOE_FEW_MAX_TOKENS tokens and MOE_FEW_MAX_SLOTS
+ * slots (T*k), in two kernels: one forms the logits, one does the rest, every
+ * touched expert's weights read once ("Serving MoE models with expert
+ * parallelism on 8xH200" (reviosa), section "Batching: MoE needs bigger
+ * batches than you think": such batches stream weights).  Same formulas,
+ * formats, layouts and arguments as moe_forward, with these differences:
+ *  - counts, offsets, sorted_slot, slot_pos and events must be NULL: no
+ *    dispatch order is formed (MOE_ERR_INVALID_ARGUMENT).
+ *  - the experts' rows are not rounded before they are added, and sums run in
+ *    another order, so results agree within rounding, not bit for bit (the
+ *    selection is taken on the logits this call writes).  FP8 block scales
+ *    are applied to the sum of each 128-deep block: they need not lie within
+ *    2^32 of each other.
+ *  - T above MOE_FEW_MAX_TOKENS or T*k above MOE_FEW_MAX_SLOTS is
+ *    MOE_ERR_UNSUPPORTED.  Arrays are 16-byte aligned (checked).
+ *  - the logits, where given, are written (or read) in place; they are
+ *    distinct from the other arrays.
+ *  ws, ws_bytes: scratch of moe_workspace_size(p, MOE_CALL_FORWARD_FEW).  The
+ *  workgroups of the second kernel wait for each other's results only where
+ *  those are under way, so the call needs no share of the device to itself. */
+#define MOE_FEW_MAX_TOKENS 16
+#define MOE_FEW_MAX_SLOTS 256
+
+moe_status_t moe_forward_few(const moe_problem_t* p, const moe_forward_args_t* a, void* ws,
+                             size_t ws_bytes, void* stream);
 
 /* ---- Expert-parallel load balancing (EPLB) ----
  *

@@ -24,7 +24,8 @@ MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_MXFP4 = range(4)
 MOE_CALL_PERMUTE, MOE_CALL_EXPERT_FFN, MOE_CALL_FORWARD, MOE_CALL_ROUTE = range(4)
 MOE_CALL_BALANCE_LOSS, MOE_CALL_ROUTE_BACKWARD = 4, 5
 MOE_CALL_NORM_BACKWARD, MOE_CALL_COMBINE_NORM_BACKWARD = 6, 7
-MOE_CALL_EXPERT_FFN_MX = 8
+MOE_CALL_EXPERT_FFN_MX, MOE_CALL_FORWARD_FEW = 8, 9
+MOE_FEW_MAX_TOKENS, MOE_FEW_MAX_SLOTS = 16, 256   # include/moe.h
 MOE_MX_SCALES_ROW, MOE_MX_SCALES_BLOCK = range(2)
 MOE_GRAD_MAX_TENSORS = 4096   # include/moe.h
 MOE_FORWARD_EVENTS = 7
@@ -119,6 +120,7 @@ def load_library() -> ctypes.CDLL:
     lib.moe_norm_backward.argtypes = [P, ctypes.POINTER(NormBackwardArgs), vp, sz, vp]
     lib.moe_combine_norm.argtypes = [P, ctypes.POINTER(CombineNormArgs), vp]
     lib.moe_combine_norm_backward.argtypes = [P, ctypes.POINTER(CombineNormBackwardArgs), vp, sz, vp]
+    lib.moe_forward_few.argtypes = [P, ctypes.POINTER(ForwardArgs), vp, sz, vp]
     lib.moe_mx_quantize.argtypes = [i32, i32, i32, i32, vp, vp, vp, i32, vp]
     lib.moe_mx_dequantize.argtypes = [i32, i32, i32, i32, vp, vp, vp, i32, vp]
     lib.moe_expert_ffn_mx.argtypes = [P] + [vp] * 13 + [sz, vp]
@@ -127,7 +129,7 @@ def load_library() -> ctypes.CDLL:
               "moe_balance_loss", "moe_route_backward", "moe_combine_backward", "moe_grad_norm",
               "moe_grad_clip", "moe_norm", "moe_norm_backward", "moe_combine_norm",
               "moe_combine_norm_backward", "moe_mx_quantize", "moe_mx_dequantize",
-              "moe_expert_ffn_mx"):
+              "moe_expert_ffn_mx", "moe_forward_few"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -521,6 +523,46 @@ def moe_combine_norm_backward(p, *, dout, y, weight, rstd, ws, slot_pos=None, to
         _arg(c, "dgate", dgate, f32, p.d, dev))
     wp, wn = _ws_arg(c, ws, dev)
     _check(c, load_library().moe_combine_norm_backward(ctypes.byref(p), ctypes.byref(a), wp, wn, st))
+
+
+# ---- the layer for a few tokens (tensors checked as above)
+
+_WEIGHT_DTYPE = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
+
+
+def _weight_arg(call: str, name: str, w, p: Problem, device: int):
+    n = p.num_local * p.F * p.d
+    if p.weight in _WEIGHT_DTYPE:
+        return _arg(call, name, w, _WEIGHT_DTYPE[p.weight], n, device)
+    # FP8 codes as bytes or as torch's type
+    dtype = torch.uint8
+    if isinstance(w, torch.Tensor) and p.weight == MOE_FP8_E4M3 and w.dtype is torch.float8_e4m3fn:
+        dtype = w.dtype
+    return _arg(call, name, w, dtype, n if p.weight == MOE_FP8_E4M3 else n // 2, device)
+
+
+def moe_forward_few(p, *, x, w_router, w_gate, w_up, w_down, out, ws, router_bias=None, s_gate=None,
+                    s_up=None, s_down=None, logits=None, topk_idx=None, topk_w=None, stream=None) -> None:
+    """The whole layer for at most 16 tokens, in two kernels (see moe.h)."""
+    c = "moe_forward_few"
+    dev, st = _current(c, stream)
+    f32, act, n, S, El = torch.float32, _act(c, p), p.T * p.d, p.T * p.k, p.num_local
+    scale = {}
+    for name, s in (("s_gate", s_gate), ("s_up", s_up), ("s_down", s_down)):
+        if p.weight == MOE_FP8_E4M3:
+            scale[name] = _arg(c, name, s, f32, El * (p.F // 128) * (p.d // 128), dev)
+        elif p.weight == MOE_MXFP4:
+            scale[name] = _arg(c, name, s, torch.uint8, El * p.F * p.d // 32, dev)
+    a = ForwardArgs(
+        x=_arg(c, "x", x, act, n, dev), w_router=_arg(c, "w_router", w_router, act, p.d * p.E, dev),
+        router_bias=_arg(c, "router_bias", router_bias, f32, p.E, dev),
+        w_gate=_weight_arg(c, "w_gate", w_gate, p, dev), w_up=_weight_arg(c, "w_up", w_up, p, dev),
+        w_down=_weight_arg(c, "w_down", w_down, p, dev), out=_arg(c, "out", out, act, n, dev),
+        logits=_arg(c, "logits", logits, f32, p.T * p.E, dev),
+        topk_idx=_arg(c, "topk_idx", topk_idx, torch.int32, S, dev),
+        topk_w=_arg(c, "topk_w", topk_w, f32, S, dev), **scale)
+    wp, wn = _ws_arg(c, ws, dev)
+    _check(c, load_library().moe_forward_few(ctypes.byref(p), ctypes.byref(a), wp, wn, st))
 
 
 # ---- 4-bit activations (tensors checked as above)

@@ -56,6 +56,8 @@ moe_status_t check_problem(const moe_problem_t* p, Shape* s) {
   return MOE_OK;
 }
 
+bool few_tokens(const Shape& s) { return s.T <= MOE_FEW_MAX_TOKENS && s.S <= MOE_FEW_MAX_SLOTS; }
+
 moe_status_t from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -191,6 +193,8 @@ size_t moe_workspace_size(const moe_problem_t* p, int32_t call) {
       return moe::norm_grad_ws_bytes(s);
     case MOE_CALL_EXPERT_FFN_MX:
       return s.weight == MOE_MXFP4 ? moe::mx_ffn_ws_bytes(s) : 0;
+    case MOE_CALL_FORWARD_FEW:
+      return few_tokens(s) ? moe::few_ws_bytes(s) : 0;
     default:
       return 0;
   }
@@ -331,6 +335,34 @@ moe_status_t moe_forward(const moe_problem_t* p, const moe_forward_args_t* a, vo
   if (e == hipSuccess) e = moe::combine(s, y, pos, nullptr, a->out, strm);
   if (e == hipSuccess) e = mark(6);
   return from_hip(e);
+}
+
+moe_status_t moe_forward_few(const moe_problem_t* p, const moe_forward_args_t* a, void* ws,
+                             size_t ws_bytes, void* stream) {
+  Shape s;
+  moe_status_t st = check_problem(p, &s);
+  if (st != MOE_OK) return st;
+  if (a == nullptr) return MOE_ERR_INVALID_ARGUMENT;
+  if (!few_tokens(s)) return MOE_ERR_UNSUPPORTED;
+  if (a->counts != nullptr || a->offsets != nullptr || a->sorted_slot != nullptr ||
+      a->slot_pos != nullptr || a->events != nullptr)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!all_aligned16(a->x, a->w_router, a->router_bias, a->w_gate, a->w_up, a->w_down, a->s_gate,
+                     a->s_up, a->s_down, a->out, a->logits, a->topk_idx, a->topk_w, ws))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (a->w_gate == nullptr || a->w_up == nullptr || a->w_down == nullptr)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if ((s.weight == MOE_FP8_E4M3 || s.weight == MOE_MXFP4) &&
+      (a->s_gate == nullptr || a->s_up == nullptr || a->s_down == nullptr))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (s.T > 0 && (a->x == nullptr || a->out == nullptr ||
+                  (a->w_router == nullptr && a->logits == nullptr)))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (s.T > 0 && (a->out == a->x || (a->logits != nullptr && a->logits == a->topk_w)))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (ws == nullptr || ws_bytes < moe::few_ws_bytes(s)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (s.T == 0) return MOE_OK;
+  return from_hip(moe::forward_few(s, *a, ws, static_cast<hipStream_t>(stream)));
 }
 
 moe_status_t moe_balance_loss(const moe_problem_t* p, const float* logits, const int32_t* topk_idx,

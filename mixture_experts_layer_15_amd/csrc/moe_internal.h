@@ -156,6 +156,10 @@ hipError_t combine_norm(const Shape& s, const moe_combine_norm_args_t& g, hipStr
 hipError_t combine_norm_backward(const Shape& s, const moe_combine_norm_backward_args_t& g,
                                  void* ws, hipStream_t st);
 
+// ---- few.hip
+size_t few_ws_bytes(const Shape& s);
+hipError_t forward_few(const Shape& s, const moe_forward_args_t& f, void* ws, hipStream_t st);
+
 // ---- mx.hip
 hipError_t mx_quantize(int batch, int rows, int cols, int bf16, const void* src, uint8_t* codes,
                        uint8_t* scales, int block_major, hipStream_t st);
