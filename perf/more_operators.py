@@ -341,8 +341,8 @@ def _own(s):
         return dict(values=s["values"])
     if s["op"] == "few":
         p = B.problem(s["T"], s["d"], s["E"], s["k"], s["F"], 0, s["local"], "f32" if s["weight"] == "f32" else "bf16", s["weight"], s["blocked"])
-        B.moe_forward_few(p, x=s["x"], w_router=s["w_router"], router_bias=None, w_gate=s["kept_gate"], w_up=s["kept_up"],
-                          w_down=s["kept_down"], s_gate=s["s_gate"], s_up=s["s_up"], s_down=s["s_down"], out=s["out"], logits=s["logits"],
+        w_gate, w_up, w_down = (s["kept_" + n].view(s["w_" + n].dtype) for n in ("gate", "up", "down"))
+        B.moe_forward_few(p, x=s["x"], w_router=s["w_router"], router_bias=None, w_gate=w_gate, w_up=w_up, w_down=w_down, s_gate=s["s_gate"], s_up=s["s_up"], s_down=s["s_down"], out=s["out"], logits=s["logits"],
                           topk_w=s["topk_w"], ws=_workspace(B.moe_workspace_size(p, B.MOE_CALL_FORWARD_FEW), s["x"].device))
         return dict(out=s["out"], logits=s["logits"], topk_w=s["topk_w"])
     if s["op"] == "mx":
