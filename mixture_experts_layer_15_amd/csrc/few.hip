@@ -7,8 +7,9 @@
 // drained chips of a kernel per stage, so here one kernel forms the logits and
 // a second does the rest:
 //
-//  router   a workgroup forms the logits of four experts (all of K; no partial
-//           sums leave it) and clears the counters of the second kernel.
+//  router   a workgroup forms the logits of four experts for up to four tokens
+//           (all of K; no partial sums leave it); the counters of the second
+//           kernel are cleared.
 //  layer    every workgroup selects the top k of every token (a few hundred
 //           logits) and lists the touched experts for itself.  The gate/up
 //           items (expert, 32 features) are cut into a share per workgroup, and
@@ -49,7 +50,8 @@ constexpr int kPad = 16;        // words between counters: a cache line each
 constexpr int kRowPad = 36;     // floats of a token's 32 results in LDS
 constexpr int kThreads = 256;
 constexpr int kGrid = 512;      // workgroups of the layer kernel: two a compute unit
-constexpr int kRouterThreads = 512;
+constexpr int kRouterThreads = 1024;
+constexpr int kRouterTokens = 4;  // most tokens of a workgroup of the router
 static_assert(kMaxTokens <= 16, "an item's rows are half of a 32-row operand");
 static_assert(kMaxSlots <= kThreads, "a thread per slot");
 
@@ -110,9 +112,10 @@ template <bool kBF16, int TT>
 __global__ __launch_bounds__(kRouterThreads) void few_router_kernel(FewArgs a) {
   __shared__ float part[kRouterThreads / kWave][TT * 4];
   const int tid = threadIdx.x;
-  for (int i = blockIdx.x * kRouterThreads + tid; i < a.n_ctr; i += gridDim.x * kRouterThreads) a.ctr[i] = 0;
+  if (blockIdx.y == 0)
+    for (int i = blockIdx.x * kRouterThreads + tid; i < a.n_ctr; i += gridDim.x * kRouterThreads) a.ctr[i] = 0;
   if (a.w_router == nullptr) return;
-  const int e0 = blockIdx.x * 4;
+  const int e0 = blockIdx.x * 4, t0 = blockIdx.y * TT;
   const bool whole = a.E % 4 == 0;
   float acc[TT * 4];
 #pragma unroll
@@ -147,7 +150,7 @@ __global__ __launch_bounds__(kRouterThreads) void few_router_kernel(FewArgs a) {
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-      const long long at = (long long)min(t, a.T - 1) * a.d + c;
+      const long long at = (long long)min(t0 + t, a.T - 1) * a.d + c;
       if constexpr (kBF16) {
         const u32x2_t u = *reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(a.x) + at);
 #pragma unroll
@@ -172,7 +175,7 @@ __global__ __launch_bounds__(kRouterThreads) void few_router_kernel(FewArgs a) {
     float s = part[0][tid];
 #pragma unroll
     for (int w = 1; w < kRouterThreads / kWave; ++w) s += part[w][tid];
-    const int t = tid / 4, e = e0 + tid % 4;
+    const int t = t0 + tid / 4, e = e0 + tid % 4;
     if (t < a.T && e < a.E) a.logits[t * a.E + e] = a.bias ? s + a.bias[e] : s;
   }
 }
@@ -230,8 +233,10 @@ __device__ __forceinline__ void select_by_waves(const FewArgs& a, Plan& p) {
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
     id[j] = l * kV + j;
-    key[j] = id[j] < a.E ? logit_key(a.logits[t * a.E + id[j]]) : 0;
+    key[j] = __float_as_uint(a.logits[t * a.E + min(id[j], a.E - 1)]);  // (all loads before any use)
   }
+#pragma unroll
+  for (int j = 0; j < kV; ++j) key[j] = id[j] < a.E ? logit_key(__uint_as_float(key[j])) : 0;
 #pragma unroll
   for (int j = 1; j < kV; ++j)  // insertion: stable
 #pragma unroll
@@ -278,9 +283,10 @@ __device__ __forceinline__ void select_by_rows(const FewArgs& a, Plan& p) {
   uint32_t key[kV];
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
-    const int e = j * 16 + r;
-    key[j] = t < a.T && e < a.E ? logit_key(a.logits[t * a.E + e]) : 0;
+    key[j] = __float_as_uint(a.logits[min(t, a.T - 1) * a.E + min(j * 16 + r, a.E - 1)]);
   }
+#pragma unroll
+  for (int j = 0; j < kV; ++j) key[j] = t < a.T && j * 16 + r < a.E ? logit_key(__uint_as_float(key[j])) : 0;
   for (int i = 0; i < a.k; ++i) {
     uint32_t best = key[0];
     int at = 0;
@@ -915,13 +921,13 @@ hipError_t forward_few(const Shape& s, const moe_forward_args_t& f, void* ws, hi
   a.e0 = s.e0;
   a.El = s.El;
   auto router = [&](auto bf16, auto tt) {
-    hipLaunchKernelGGL((few_router_kernel<bf16.value, tt.value>), dim3((s.E + 3) / 4), dim3(kRouterThreads), 0, st, a);
+    const dim3 grid((s.E + 3) / 4, f.w_router ? (s.T + tt.value - 1) / tt.value : 1);
+    hipLaunchKernelGGL((few_router_kernel<bf16.value, tt.value>), grid, dim3(kRouterThreads), 0, st, a);
   };
   using std::integral_constant;
   auto by_tokens = [&](auto bf16) {
     if (s.T == 1) router(bf16, integral_constant<int, 1>{});
-    else if (s.T <= 4) router(bf16, integral_constant<int, 4>{});
-    else router(bf16, integral_constant<int, kMaxTokens>{});
+    else router(bf16, integral_constant<int, kRouterTokens>{});
   };
   if (s.act == kBF16) by_tokens(std::true_type{});
   else by_tokens(std::false_type{});
