@@ -14,10 +14,10 @@
 // Operand layout: lane l of an MFMA operand holds the 32 codes (16 bytes) of
 // row l % 32 and 32-value block l / 32 of a 64-deep step, and that block's
 // scale.  A step of 32 rows is therefore 1 KB of consecutive 16-byte pieces:
-// the unit of the blocked weight layout, of every LDS stage below and of the
-// intermediate h, which lies in the workspace as [group of 32 rows][F / 64]
-// units with scales [group][F / 128][32 rows][4 blocks].  Groups are counted
-// per expert (a group never holds rows of two), so h needs no gather.  Weights
+// the unit of the blocked weight layout and of the intermediate h, which lies
+// in the workspace as [group of 32 rows][F / 64] units with scales
+// [group][32 rows][F / 32].  Groups are counted per expert (a group never holds
+// rows of two), so h needs no gather.  Weights
 // are the A operand in the permuted row order (feature 16 (l / 32) + q in
 // register q), so a lane's 16 results are 16 consecutive features of a token.
 #include <algorithm>
@@ -287,6 +287,14 @@ __device__ __forceinline__ f32x16_t mfma_mx(u32x4_t a, u32x4_t b, f32x16_t c, ui
 #endif
 }
 
+// Offset in two units (a stage of 128 K values of 32 rows) of the 16 bytes that
+// lane l moves of half block h: row 16 h + l % 16, chunk l / 16 (half chunk % 2
+// of unit chunk / 2).
+__device__ __forceinline__ uint32_t unit_offset(int h, int l) {
+  const int c = l >> 4;
+  return (c >> 1) * 1024 + ((c & 1) * 32 + 16 * h + (l & 15)) * 16;
+}
+
 // Epilogue of a gate/up pair: 16 consecutive features of token row r of group
 // `grp` (lane half g), feature block fb: silu(gate) * up in float32, converted
 // to MXFP4 with the other half's 16 features.
@@ -308,7 +316,7 @@ __device__ __forceinline__ void store_h(const MxArgs& a, const f32x16_t& gate, c
   *reinterpret_cast<u32x2_t*>(a.h + ((long long)grp * (F / 64) + (fb >> 1)) * 1024 +
                               ((fb & 1) * 32 + r) * 16 + 8 * g) = q;
   if (g == 0)
-    a.hs[((long long)grp * (F / 128) + (fb >> 2)) * 128 + r * 4 + (fb & 3)] = (uint8_t)byte;
+    a.hs[((long long)grp * 32 + r) * (F / 32) + fb] = (uint8_t)byte;
 }
 
 // Epilogue of a down block: 16 consecutive columns of row p.
@@ -372,9 +380,9 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxArgs a) {
       voffAS = t * (uint32_t)(a.K / 32) + g;
     } else {
       rA = rsrc(a.A + (long long)grp * nS * 1024, (uint32_t)nS * 1024u);
-      rAS = rsrc(a.AS + (long long)grp * (nS / 2) * 128, (uint32_t)(nS / 2) * 128u);
+      rAS = rsrc(a.AS + (long long)grp * nS * 64, (uint32_t)nS * 64u);
       voffA = 16u * l;
-      voffAS = 4u * r + g;
+      voffAS = (uint32_t)(r * 2 * nS) + g;
     }
     const __amdgpu_buffer_rsrc_t rW0 = rsrc(a.W0 + (size_t)e * wmat, wmat);
     const __amdgpu_buffer_rsrc_t rW1 = kGateUp ? rsrc(a.W1 + (size_t)e * wmat, wmat) : rW0;
@@ -392,8 +400,7 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxArgs a) {
                                                        (uint32_t)(2 * s) * a.Nout + fb * 32u, 0);
       }
       tb[d] = __builtin_amdgcn_raw_buffer_load_b128(rA, voffA, s * (kGateUp ? 32u : 1024u), 0);
-      ts[d] = __builtin_amdgcn_raw_buffer_load_b8(
-          rAS, voffAS, kGateUp ? 2u * s : (uint32_t)(s >> 1) * 128u + 2u * (s & 1), 0);
+      ts[d] = __builtin_amdgcn_raw_buffer_load_b8(rAS, voffAS, 2u * s, 0);
     };
     f32x16_t acc[kNB];
 #pragma unroll
@@ -452,17 +459,21 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxArgs a) {
 
 // -- many rows per expert: tiles of 128 rows x 256 weight rows (gate/up: 128
 // gate and the up rows of the same features) through a ring of LDS stages of
-// 128 K values, filled by LDS-DMA in operand order.  Four waves of 64 x 128;
-// two workgroups a CU, so that the conversion of one's results runs beside the
-// other's products.
+// 128 K values, filled by LDS-DMA.  Four waves of 64 x 128; two workgroups a
+// CU, so that the conversion of one's results runs beside the other's products.
+// In a stage a 32-row block is [row / 16][16-byte chunk][row % 16]: a DMA
+// instruction takes 64 bytes of each of 16 rows (the cache counts lines, not
+// bytes: 32 bytes of 32 rows made it the bottleneck), and an operand read is
+// two runs of 256 bytes.  The rows' scales come 16 bytes (four stages) at a
+// time, for the same reason, and are read into registers.
 constexpr int kBM = 4;        // groups of 32 rows of a tile
 constexpr int kStages = 3;
-constexpr int kStageA = kBM * 2 * 1024;
-constexpr int kStageW = 8 * 2 * 1024;
-constexpr int kStageAS = kBM * 32 * 4;
-constexpr int kStageWS = 4 * 256;
-constexpr int kStage = kStageA + kStageW + kStageAS + kStageWS;
-constexpr int kTileLds = kStages * kStage;
+constexpr int kBlock = 2048;  // of 32 rows
+constexpr int kStageW = kBM * kBlock;              // weight rows behind the tile's rows
+constexpr int kStageWS = kStageW + 8 * kBlock;     // their scales [4 K blocks][256]
+constexpr int kStage = kStageWS + 4 * 256;
+constexpr int kRowScales = kStages * kStage;       // [128 rows][16]
+constexpr int kTileLds = kRowScales + kBM * 32 * 16;
 
 // One LDS-DMA load per active lane: lane i's 16 (4) bytes, from voff + soff in
 // the buffer, land at lds + 16 i (4 i); lds is wave-uniform.
@@ -506,8 +517,11 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
   const int ntn = (a.Nout + cols - 1) / cols;
   const uint32_t wrow = (uint32_t)a.K / 2, wmat = (uint32_t)a.Nout * wrow;
   const uint32_t smat = (uint32_t)(a.K / 32) * a.Nout;
-  const uint32_t unit = a.blocked ? 1024u : 32u;
-  const uint32_t voffW = a.blocked ? 16u * l : (uint32_t)feat(r) * wrow + 16u * g;
+  const uint32_t stepW = a.blocked ? 2048u : 64u;  // of a stage
+  uint32_t voffW[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    voffW[h] = a.blocked ? unit_offset(h, l) : (uint32_t)feat(16 * h + (l & 15)) * wrow + 16u * (l >> 4);
   const int n_items = groups[a.El] / kBM * ntn;
   const int per_xcd = (n_items + kNumXcd - 1) / kNumXcd;
   const int xcd = blockIdx.x % kNumXcd, slots = gridDim.x / kNumXcd;
@@ -521,29 +535,31 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
     const int g0 = __builtin_amdgcn_readfirstlane(groups[e]) + mt * kBM;
     const int row0 = __builtin_amdgcn_readfirstlane(bound(a, e)) + mt * kBM * 32;
     const int rend = __builtin_amdgcn_readfirstlane(bound(a, e + 1));
-    // this wave's LDS-DMA: A blocks `wave` (both steps), W blocks wave and
-    // wave + 4 (both steps), rows' scales, and K block `wave` of the weights'
+    // this wave's LDS-DMA: A block `wave`, W blocks wave and wave + 4, the
+    // scales of A block `wave`, and K block `wave` of the weights' scales.
+    // Lane l: row l % 16 of a half block, chunk l / 16.
     __amdgpu_buffer_rsrc_t rA, rAS;
-    uint32_t voffA, voffAS, stepA, stepAS;
+    uint32_t voffA[2], voffAS, stepA;
     if constexpr (kGateUp) {
-      const int slot = a.sorted_slot[min(row0 + wave * 32 + r, rend - 1)];
-      const uint32_t t = (uint32_t)slot / (uint32_t)a.k;
-      const int sslot = a.sorted_slot[min(row0 + (wave & 1) * 64 + l, rend - 1)];
+      uint32_t t[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        t[h] = (uint32_t)a.sorted_slot[min(row0 + wave * 32 + 16 * h + (l & 15), rend - 1)] / (uint32_t)a.k;
+        voffA[h] = t[h] * wrow + 16u * (l >> 4);
+      }
       rA = rsrc(a.A, a.a_bytes);
       rAS = rsrc(a.AS, a.as_bytes);
-      voffA = t * wrow + 16u * g;
-      voffAS = (uint32_t)sslot / (uint32_t)a.k * (uint32_t)(a.K / 32);
-      stepA = 32;
-      stepAS = 4;
+      voffAS = (l & 16 ? t[1] : t[0]) * (uint32_t)(a.K / 32);  // lanes 0 .. 31: their rows
+      stepA = 64;
     } else {
       // (all kBM groups of the tile exist; rows behind the segment hold whatever
       // was there and only reach results that are not stored)
       rA = rsrc(a.A + (long long)(g0 + wave) * (2 * nK) * 1024, (uint32_t)nK * 2048u);
-      rAS = rsrc(a.AS + (long long)g0 * nK * 128, (uint32_t)(kBM * nK) * 128u);
-      voffA = 16u * l;
-      voffAS = (uint32_t)((wave & 1) * 2 + g) * nK * 128u + 4u * r;
-      stepA = 1024;
-      stepAS = 128;
+      rAS = rsrc(a.AS + (long long)(g0 + wave) * (4 * nK) * 32, (uint32_t)nK * 128u);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) voffA[h] = unit_offset(h, l);
+      voffAS = (uint32_t)r * (4 * nK);
+      stepA = 2048;
     }
     const uint32_t f0 = (uint32_t)nt * cols;
     const __amdgpu_buffer_rsrc_t rW0 = rsrc(a.W0 + (size_t)e * wmat, wmat);
@@ -558,14 +574,12 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
     auto issue = [&](int s, int slot) {
       unsigned char* st = lds + slot * kStage;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        lds_dma16(rA, voffA, (uint32_t)(2 * s + q) * stepA, st + (wave * 2 + q) * 1024);
-        lds_dma16(rW0, voffW, sW0 + (uint32_t)(2 * s + q) * unit, st + kStageA + (wave * 2 + q) * 1024);
-        lds_dma16(rW1, voffW, sW1 + (uint32_t)(2 * s + q) * unit, st + kStageA + ((wave + 4) * 2 + q) * 1024);
+      for (int h = 0; h < 2; ++h) {
+        lds_dma16(rA, voffA[h], (uint32_t)s * stepA, st + wave * kBlock + h * 1024);
+        lds_dma16(rW0, voffW[h], sW0 + (uint32_t)s * stepW, st + kStageW + wave * kBlock + h * 1024);
+        lds_dma16(rW1, voffW[h], sW1 + (uint32_t)s * stepW, st + kStageW + (wave + 4) * kBlock + h * 1024);
       }
-      unsigned char* sc = st + kStageA + kStageW;
-      lds_dma4(rAS, voffAS, (uint32_t)s * stepAS, sc + (wave & 1) * 256);
-      sc += kStageAS + wave * 256;
+      unsigned char* sc = st + kStageWS + wave * 256;
       if constexpr (kGateUp) {
         if (g == 0) {
           lds_dma4(rS0, voffS, (uint32_t)(4 * s) * a.Nout, sc);
@@ -575,44 +589,65 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
         lds_dma4(rS0, voffS, (uint32_t)(4 * s) * a.Nout, sc);
       }
     };
+    // row scales of stages s .. s + 3 (s a multiple of 4; behind the row's end
+    // come others' or zeros, not used)
+    auto issue_row_scales = [&](int s) {
+      if (g == 0) lds_dma16(rAS, voffAS, 4u * s, lds + kRowScales + wave * 512);
+    };
     f32x16_t acc[2][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int n = 0; n < 4; ++n) acc[m][n] = f32x16_t{};
-    // LDS-DMA instructions of a wave per stage
-    constexpr int kIssued = kGateUp ? 9 : 8;
+    constexpr int kIssued = kGateUp ? 8 : 7;  // LDS-DMA instructions of issue()
     static_assert(kStages == 3, "one stage is in flight behind the one waited for");
+    issue_row_scales(0);
     issue(0, 0);
     if (nK > 1) issue(1, 1);
     int slot = 0;
+    u32x4_t rs[2];  // row scales of this stage (word 0) and the next ones
     for (int s = 0; s < nK; ++s, slot = slot == kStages - 1 ? 0 : slot + 1) {
       if (s + 1 < nK) stage_barrier<kIssued>();
       else stage_barrier<0>();
-      // (every wave has read stage s - 1, whose place this one takes)
+      // (every wave has read stage s - 1, whose place stage s + 2 takes, and in
+      // s = 4 n + 1 the row scales of stages 4 n .. 4 n + 3)
+      if (s % 4 == 1 && s + 3 < nK) issue_row_scales(s + 3);
       if (s + 2 < nK) issue(s + 2, slot == 0 ? 2 : slot - 1);
       const unsigned char* st = lds + slot * kStage;
-      const unsigned char* sc = st + kStageA + kStageW;
-      uint32_t as[2];
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-        as[m] = *reinterpret_cast<const uint32_t*>(sc + ((wm * 2 + m) * 32 + r) * 4) >> (8 * g);
-      sc += kStageAS;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        u32x4_t av[2];
+      if (s % 4 == 0) {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
-          av[m] = *reinterpret_cast<const u32x4_t*>(st + ((wm * 2 + m) * 2 + q) * 1024 + 16 * l);
+          rs[m] = *reinterpret_cast<const u32x4_t*>(lds + kRowScales + ((wm * 2 + m) * 32 + r) * 16);
+      }
+      // both steps' operands are on their way before the first product
+      uint32_t ws[2][4];
+      u32x4_t av[2][2], wv[2][4];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const unsigned char* at = st + (r >> 4) * 1024 + (2 * q + g) * 256 + (r & 15) * 16;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) av[q][m] = *reinterpret_cast<const u32x4_t*>(at + (wm * 2 + m) * kBlock);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           const int b = kGateUp ? (n >> 1) * 4 + wn * 2 + (n & 1) : wn * 4 + n;
-          const u32x4_t wv = *reinterpret_cast<const u32x4_t*>(st + kStageA + (b * 2 + q) * 1024 + 16 * l);
-          const uint32_t ws = sc[(2 * q + g) * 256 + b * 32 + feat(r)];
-#pragma unroll
-          for (int m = 0; m < 2; ++m) acc[m][n] = mfma_mx(wv, av[m], acc[m][n], ws, as[m] >> (16 * q));
+          wv[q][n] = *reinterpret_cast<const u32x4_t*>(at + kStageW + b * kBlock);
+          ws[q][n] = st[kStageWS + (2 * q + g) * 256 + b * 32 + feat(r)];
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
+      uint32_t as[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        as[m] = rs[m][0] >> (8 * g);
+        rs[m] = u32x4_t{rs[m][1], rs[m][2], rs[m][3], 0};
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            acc[m][n] = mfma_mx(wv[q][n], av[q][m], acc[m][n], ws[q][n], as[m] >> (16 * q));
     }
     stage_barrier<0>();  // every wave has read its last stage
 #pragma unroll
