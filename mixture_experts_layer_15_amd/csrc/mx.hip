@@ -297,9 +297,9 @@ __device__ __forceinline__ uint32_t unit_offset(int h, int l) {
 
 // Epilogue of a gate/up pair: 16 consecutive features of token row r of group
 // `grp` (lane half g), feature block fb: silu(gate) * up in float32, converted
-// to MXFP4 with the other half's 16 features.
-__device__ __forceinline__ void store_h(const MxArgs& a, const f32x16_t& gate, const f32x16_t& up,
-                                        int grp, int fb, int l) {
+// to MXFP4 with the other half's 16 features.  Returns the scale byte.
+__device__ __forceinline__ uint32_t store_h(const MxArgs& a, const f32x16_t& gate, const f32x16_t& up,
+                                            int grp, int fb, int l) {
   float h[16];
   uint32_t top = 0;
 #pragma unroll
@@ -312,11 +312,14 @@ __device__ __forceinline__ void store_h(const MxArgs& a, const f32x16_t& gate, c
   const float inv = mx_inverse(byte);
   u32x2_t q = {mx_codes8(h, inv), mx_codes8(h + 8, inv)};
   if (byte == 255) q = u32x2_t{0, 0};
-  const int F = a.Nout, r = l & 31, g = l >> 5;
-  *reinterpret_cast<u32x2_t*>(a.h + ((long long)grp * (F / 64) + (fb >> 1)) * 1024 +
+  const int r = l & 31, g = l >> 5;
+  *reinterpret_cast<u32x2_t*>(a.h + ((long long)grp * (a.Nout / 64) + (fb >> 1)) * 1024 +
                               ((fb & 1) * 32 + r) * 16 + 8 * g) = q;
-  if (g == 0)
-    a.hs[((long long)grp * 32 + r) * (F / 32) + fb] = (uint8_t)byte;
+  return byte;
+}
+
+__device__ __forceinline__ uint8_t* h_scale(const MxArgs& a, int grp, int r, int fb) {
+  return a.hs + ((long long)grp * 32 + r) * (a.Nout / 32) + fb;
 }
 
 // Epilogue of a down block: 16 consecutive columns of row p.
@@ -451,8 +454,12 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxArgs a) {
         }
       }
       const int fb = nb * H + wave;
-      if constexpr (kGateUp) store_h(a, sum[0], sum[1], grp, fb, l);
-      else if (row0 + r < rend) store_y(a, sum[0], row0 + r, fb * 32 + 16 * g, gw);
+      if constexpr (kGateUp) {
+        const uint32_t byte = store_h(a, sum[0], sum[1], grp, fb, l);
+        if (g == 0) *h_scale(a, grp, r, fb) = (uint8_t)byte;
+      } else if (row0 + r < rend) {
+        store_y(a, sum[0], row0 + r, fb * 32 + 16 * g, gw);
+      }
     }
   }
 }
@@ -472,8 +479,10 @@ constexpr int kBlock = 2048;  // of 32 rows
 constexpr int kStageW = kBM * kBlock;              // weight rows behind the tile's rows
 constexpr int kStageWS = kStageW + 8 * kBlock;     // their scales [4 K blocks][256]
 constexpr int kStage = kStageWS + 4 * 256;
-constexpr int kRowScales = kStages * kStage;       // [128 rows][16]
-constexpr int kTileLds = kRowScales + kBM * 32 * 16;
+constexpr int kRowScales = kStages * kStage;       // [2][128 rows][16]
+constexpr int kTileTable = kRowScales + 2 * kBM * 512;  // groups before each expert, El + 1
+// (up to 251 experts two workgroups fit a compute unit)
+inline int tile_lds(int El) { return kTileTable + (El + 1) * 4; }
 
 // One LDS-DMA load per active lane: lane i's 16 (4) bytes, from voff + soff in
 // the buffer, land at lds + 16 i (4 i); lds is wave-uniform.
@@ -504,10 +513,12 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// The ring runs on across items: the next item's first stages and addresses are
+// under way before the present one's results are converted and stored.
 template <bool kGateUp>
 __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  __shared__ int groups[kMaxExperts + 1];
+  int* groups = reinterpret_cast<int*>(lds + kTileTable);
   group_table<256, kBM>(a, groups);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int l = lane_id(), g = l >> 5, r = l & 31;
@@ -526,112 +537,191 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
   const int per_xcd = (n_items + kNumXcd - 1) / kNumXcd;
   const int xcd = blockIdx.x % kNumXcd, slots = gridDim.x / kNumXcd;
   const int end = min(n_items, (xcd + 1) * per_xcd);
-  for (int it = xcd * per_xcd + (int)blockIdx.x / kNumXcd; it < end; it += slots) {
-    const int e = expert_of(groups, a.El, it / ntn * kBM);
-    const int m_tiles = __builtin_amdgcn_readfirstlane(groups[e + 1] - groups[e]) / kBM;
-    const int in = it - groups[e] / kBM * ntn;
-    const int nt = __builtin_amdgcn_readfirstlane(in / m_tiles);
-    const int mt = __builtin_amdgcn_readfirstlane(in % m_tiles);
-    const int g0 = __builtin_amdgcn_readfirstlane(groups[e]) + mt * kBM;
-    const int row0 = __builtin_amdgcn_readfirstlane(bound(a, e)) + mt * kBM * 32;
-    const int rend = __builtin_amdgcn_readfirstlane(bound(a, e + 1));
-    // this wave's LDS-DMA: A block `wave`, W blocks wave and wave + 4, the
-    // scales of A block `wave`, and K block `wave` of the weights' scales.
-    // Lane l: row l % 16 of a half block, chunk l / 16.
-    __amdgpu_buffer_rsrc_t rA, rAS;
-    uint32_t voffA[2], voffAS, stepA;
+  int it = xcd * per_xcd + (int)blockIdx.x / kNumXcd;
+  if (it >= end) return;
+
+  // An item: tile nt of the columns, rows row0 .. rend - 1 (up to 128) in groups
+  // g0 .. of expert e.  Found from the one before, `in` being its number among
+  // its expert's items (M tiles fastest).
+  struct Item {
+    int e, in, nt, g0, row0, rend;
+  };
+  auto place = [&](int e, int in) {
+    Item t;
+    int first = __builtin_amdgcn_readfirstlane(groups[e]);
+    int m_tiles = __builtin_amdgcn_readfirstlane(groups[e + 1]) / kBM - first / kBM;
+    while (in >= m_tiles * ntn) {
+      in -= m_tiles * ntn;
+      ++e;
+      first = __builtin_amdgcn_readfirstlane(groups[e]);
+      m_tiles = __builtin_amdgcn_readfirstlane(groups[e + 1]) / kBM - first / kBM;
+    }
+    t.e = e;
+    t.in = in;
+    t.nt = __builtin_amdgcn_readfirstlane(in / m_tiles);
+    const int mt = in - t.nt * m_tiles;
+    t.g0 = first + mt * kBM;
+    t.row0 = __builtin_amdgcn_readfirstlane(bound(a, e)) + mt * kBM * 32;
+    t.rend = __builtin_amdgcn_readfirstlane(bound(a, e + 1));
+    return t;
+  };
+  // This lane's slots of an item: gate/up: of the two rows that it moves, row
+  // l % 16 of a half block; down: of the two rows whose results it has.
+  auto load_slots = [&](const Item& t, int (&slot)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = kGateUp ? wave * 32 + 16 * h + (l & 15) : (wm * 2 + h) * 32 + r;
+      slot[h] = a.sorted_slot[min(t.row0 + row, t.rend - 1)];
+    }
+  };
+
+  // This wave's LDS-DMA of an item: A block `wave`, W blocks wave and wave + 4,
+  // the scales of A block `wave`, and K block `wave` of the weights' scales.
+  // Lane l: row l % 16 of a half block, chunk l / 16.
+  __amdgpu_buffer_rsrc_t rA, rAS, rW0, rW1, rS0, rS1;
+  uint32_t voffA[2], voffAS, voffS, sW0, sW1;
+  constexpr uint32_t stepA = kGateUp ? 64 : 2048;
+  auto aim = [&](const Item& t, const int (&slot)[2]) {
     if constexpr (kGateUp) {
-      uint32_t t[2];
+      uint32_t tok[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        t[h] = (uint32_t)a.sorted_slot[min(row0 + wave * 32 + 16 * h + (l & 15), rend - 1)] / (uint32_t)a.k;
-        voffA[h] = t[h] * wrow + 16u * (l >> 4);
+        tok[h] = (uint32_t)slot[h] / (uint32_t)a.k;
+        voffA[h] = tok[h] * wrow + 16u * (l >> 4);
       }
       rA = rsrc(a.A, a.a_bytes);
       rAS = rsrc(a.AS, a.as_bytes);
-      voffAS = (l & 16 ? t[1] : t[0]) * (uint32_t)(a.K / 32);  // lanes 0 .. 31: their rows
-      stepA = 64;
+      voffAS = (l & 16 ? tok[1] : tok[0]) * (uint32_t)(a.K / 32);  // lanes 0 .. 31: their rows
     } else {
       // (all kBM groups of the tile exist; rows behind the segment hold whatever
       // was there and only reach results that are not stored)
-      rA = rsrc(a.A + (long long)(g0 + wave) * (2 * nK) * 1024, (uint32_t)nK * 2048u);
-      rAS = rsrc(a.AS + (long long)(g0 + wave) * (4 * nK) * 32, (uint32_t)nK * 128u);
+      rA = rsrc(a.A + (long long)(t.g0 + wave) * (2 * nK) * 1024, (uint32_t)nK * 2048u);
+      rAS = rsrc(a.AS + (long long)(t.g0 + wave) * (4 * nK) * 32, (uint32_t)nK * 128u);
 #pragma unroll
       for (int h = 0; h < 2; ++h) voffA[h] = unit_offset(h, l);
       voffAS = (uint32_t)r * (4 * nK);
-      stepA = 2048;
     }
-    const uint32_t f0 = (uint32_t)nt * cols;
-    const __amdgpu_buffer_rsrc_t rW0 = rsrc(a.W0 + (size_t)e * wmat, wmat);
-    const __amdgpu_buffer_rsrc_t rW1 = kGateUp ? rsrc(a.W1 + (size_t)e * wmat, wmat) : rW0;
+    const uint32_t f0 = (uint32_t)t.nt * cols;
+    rW0 = rsrc(a.W0 + (size_t)t.e * wmat, wmat);
+    rW1 = kGateUp ? rsrc(a.W1 + (size_t)t.e * wmat, wmat) : rW0;
     // (down, 128 columns left: the second half repeats the first and is not stored)
-    const uint32_t sW0 = (f0 + 32u * wave) * wrow;
-    const uint32_t sW1 = kGateUp || f0 + 128u >= (uint32_t)a.Nout ? sW0 : sW0 + 128u * wrow;
+    sW0 = (f0 + 32u * wave) * wrow;
+    sW1 = kGateUp || f0 + 128u >= (uint32_t)a.Nout ? sW0 : sW0 + 128u * wrow;
     // scales of one K block: 4 rows a lane (gate/up: 32 lanes for either matrix)
-    const __amdgpu_buffer_rsrc_t rS0 = rsrc(a.S0 + (size_t)e * smat, smat);
-    const __amdgpu_buffer_rsrc_t rS1 = kGateUp ? rsrc(a.S1 + (size_t)e * smat, smat) : rS0;
-    const uint32_t voffS = (uint32_t)wave * a.Nout + f0 + 4u * (kGateUp ? l & 31 : l);
-    auto issue = [&](int s, int slot) {
-      unsigned char* st = lds + slot * kStage;
+    rS0 = rsrc(a.S0 + (size_t)t.e * smat, smat);
+    rS1 = kGateUp ? rsrc(a.S1 + (size_t)t.e * smat, smat) : rS0;
+    voffS = (uint32_t)wave * a.Nout + f0 + 4u * (kGateUp ? l & 31 : l);
+  };
+  // this lane's operands in a stage
+  const int first_w = wn * (kGateUp ? 2 : 4);
+  const int read_a = (r >> 4) * 1024 + g * 256 + (r & 15) * 16 + wm * 2 * kBlock;
+  const int read_w = (r >> 4) * 1024 + g * 256 + (r & 15) * 16 + kStageW + first_w * kBlock;
+  const int read_ws = kStageWS + g * 256 + first_w * 32 + feat(r);
+  int put = 0;  // the ring's next place
+  auto issue = [&](int s) {
+    unsigned char* st = lds + put * kStage;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        lds_dma16(rA, voffA[h], (uint32_t)s * stepA, st + wave * kBlock + h * 1024);
-        lds_dma16(rW0, voffW[h], sW0 + (uint32_t)s * stepW, st + kStageW + wave * kBlock + h * 1024);
-        lds_dma16(rW1, voffW[h], sW1 + (uint32_t)s * stepW, st + kStageW + (wave + 4) * kBlock + h * 1024);
-      }
-      unsigned char* sc = st + kStageWS + wave * 256;
-      if constexpr (kGateUp) {
-        if (g == 0) {
-          lds_dma4(rS0, voffS, (uint32_t)(4 * s) * a.Nout, sc);
-          lds_dma4(rS1, voffS, (uint32_t)(4 * s) * a.Nout, sc + 128);
-        }
-      } else {
+    for (int h = 0; h < 2; ++h) {
+      lds_dma16(rA, voffA[h], (uint32_t)s * stepA, st + wave * kBlock + h * 1024);
+      lds_dma16(rW0, voffW[h], sW0 + (uint32_t)s * stepW, st + kStageW + wave * kBlock + h * 1024);
+      lds_dma16(rW1, voffW[h], sW1 + (uint32_t)s * stepW, st + kStageW + (wave + 4) * kBlock + h * 1024);
+    }
+    unsigned char* sc = st + kStageWS + wave * 256;
+    if constexpr (kGateUp) {
+      if (g == 0) {
         lds_dma4(rS0, voffS, (uint32_t)(4 * s) * a.Nout, sc);
+        lds_dma4(rS1, voffS, (uint32_t)(4 * s) * a.Nout, sc + 128);
       }
-    };
-    // row scales of stages s .. s + 3 (s a multiple of 4; behind the row's end
-    // come others' or zeros, not used)
-    auto issue_row_scales = [&](int s) {
-      if (g == 0) lds_dma16(rAS, voffAS, 4u * s, lds + kRowScales + wave * 512);
-    };
+    } else {
+      lds_dma4(rS0, voffS, (uint32_t)(4 * s) * a.Nout, sc);
+    }
+    put = put == kStages - 1 ? 0 : put + 1;
+  };
+  constexpr int kIssued = kGateUp ? 8 : 7;  // LDS-DMA instructions of issue()
+  // Row scales of stages s .. s + 3 (s a multiple of 4) into the two buffers in
+  // turn.  (Behind the row's end come others' or zeros, not used.)
+  int put_rs = 0, get_rs = 0;
+  auto issue_row_scales = [&](int s) {
+    if (g == 0) lds_dma16(rAS, voffAS, 4u * s, lds + kRowScales + put_rs * (kBM * 512) + wave * 512);
+    put_rs ^= 1;
+  };
+
+  // stages that are under way beside the one that is multiplied: two, of which
+  // one may still be when the next one's turn comes (K = 128: one, none)
+  const int ahead = nK == 1 ? 1 : 2;
+  static_assert(kStages == 3, "a place for the stage being read and two ahead");
+  const int e0 = expert_of(groups, a.El, it / ntn * kBM);
+  Item cur = place(e0, it - groups[e0] / kBM * ntn);
+  int slot[2] = {0, 0};
+  if (kGateUp || a.topk_w) load_slots(cur, slot);
+  aim(cur, slot);
+  float gw[2] = {1.0f, 1.0f};
+  if (!kGateUp && a.topk_w) {
+    gw[0] = a.topk_w[slot[0]];
+    gw[1] = a.topk_w[slot[1]];
+  }
+  issue_row_scales(0);
+  issue(0);
+  if (ahead == 2) issue(1);
+  int get = 0;
+  if (ahead == 2) stage_barrier<kIssued>();
+  else stage_barrier<0>();
+  for (;;) {
+    const bool more = it + slots < end;
+    Item next = cur;
+    if (more) {
+      next = place(cur.e, cur.in + slots);
+      if (kGateUp || a.topk_w) load_slots(next, slot);
+    }
+    float gn[2] = {1.0f, 1.0f};
     f32x16_t acc[2][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int n = 0; n < 4; ++n) acc[m][n] = f32x16_t{};
-    constexpr int kIssued = kGateUp ? 8 : 7;  // LDS-DMA instructions of issue()
-    static_assert(kStages == 3, "one stage is in flight behind the one waited for");
-    issue_row_scales(0);
-    issue(0, 0);
-    if (nK > 1) issue(1, 1);
-    int slot = 0;
     u32x4_t rs[2];  // row scales of this stage (word 0) and the next ones
-    for (int s = 0; s < nK; ++s, slot = slot == kStages - 1 ? 0 : slot + 1) {
-      if (s + 1 < nK) stage_barrier<kIssued>();
-      else stage_barrier<0>();
-      // (every wave has read stage s - 1, whose place stage s + 2 takes, and in
-      // s = 4 n + 1 the row scales of stages 4 n .. 4 n + 3)
+    for (int s = 0; s < nK; ++s) {
+      // (stage 0 was waited for before the last item's results were stored)
+      if (s > 0) {
+        if (s + 1 < nK || more) stage_barrier<kIssued>();
+        else stage_barrier<0>();
+      }
+      // Every wave has read the stage before this one, whose place the new one
+      // takes, and the row scales before the present ones.
       if (s % 4 == 1 && s + 3 < nK) issue_row_scales(s + 3);
-      if (s + 2 < nK) issue(s + 2, slot == 0 ? 2 : slot - 1);
-      const unsigned char* st = lds + slot * kStage;
+      if (s + ahead < nK) {
+        issue(s + ahead);
+      } else if (more) {
+        if (s + ahead == nK) {
+          aim(next, slot);
+          if (!kGateUp && a.topk_w) {
+            gn[0] = a.topk_w[slot[0]];
+            gn[1] = a.topk_w[slot[1]];
+          }
+          issue_row_scales(0);
+        }
+        issue(s + ahead - nK);
+      }
+      const unsigned char* st = lds + get * kStage;
+      get = get == kStages - 1 ? 0 : get + 1;
       if (s % 4 == 0) {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
-          rs[m] = *reinterpret_cast<const u32x4_t*>(lds + kRowScales + ((wm * 2 + m) * 32 + r) * 16);
+          rs[m] = *reinterpret_cast<const u32x4_t*>(lds + kRowScales + get_rs * (kBM * 512) + ((wm * 2 + m) * 32 + r) * 16);
+        get_rs ^= 1;
       }
       // both steps' operands are on their way before the first product
       uint32_t ws[2][4];
       u32x4_t av[2][2], wv[2][4];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const unsigned char* at = st + (r >> 4) * 1024 + (2 * q + g) * 256 + (r & 15) * 16;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) av[q][m] = *reinterpret_cast<const u32x4_t*>(at + (wm * 2 + m) * kBlock);
+        for (int m = 0; m < 2; ++m) av[q][m] = *reinterpret_cast<const u32x4_t*>(st + read_a + q * 512 + m * kBlock);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const int b = kGateUp ? (n >> 1) * 4 + wn * 2 + (n & 1) : wn * 4 + n;
-          wv[q][n] = *reinterpret_cast<const u32x4_t*>(at + kStageW + b * kBlock);
-          ws[q][n] = st[kStageWS + (2 * q + g) * 256 + b * 32 + feat(r)];
+          const int b = kGateUp ? (n >> 1) * 4 + (n & 1) : n;  // of the wave's weight blocks
+          wv[q][n] = *reinterpret_cast<const u32x4_t*>(st + read_w + q * 512 + b * kBlock);
+          ws[q][n] = st[read_ws + q * 512 + b * 32];
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -649,24 +739,57 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
           for (int m = 0; m < 2; ++m)
             acc[m][n] = mfma_mx(wv[q][n], av[q][m], acc[m][n], ws[q][n], as[m] >> (16 * q));
     }
-    stage_barrier<0>();  // every wave has read its last stage
+    // the next item's first stage, before the stores that follow are counted
+    if (more) {
+      if (ahead == 2) stage_barrier<kIssued>();
+      else stage_barrier<0>();
+    }
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      const int grp = g0 + wm * 2 + m;
-      if (row0 + (wm * 2 + m) * 32 >= rend) continue;
-      const int p = row0 + (wm * 2 + m) * 32 + r;
+      const int grp = cur.g0 + wm * 2 + m, p0 = cur.row0 + (wm * 2 + m) * 32;
+      if (p0 >= cur.rend) continue;
       if constexpr (kGateUp) {
+        const int fb = cur.nt * 4 + wn * 2;
+        const uint32_t lo = store_h(a, acc[m][0], acc[m][2], grp, fb, l);
+        const uint32_t hi = store_h(a, acc[m][1], acc[m][3], grp, fb + 1, l);
+        if (g == 0) *reinterpret_cast<uint16_t*>(h_scale(a, grp, r, fb)) = (uint16_t)(lo | hi << 8);
+      } else {
+        // 32 rows x 64 columns at a time through LDS, so that a store takes whole
+        // lines: the place of the stage that was read last, the part of it that
+        // this wave alone fills (its weight blocks; 16-byte chunk c of row i at
+        // c ^ i % 8).
+        unsigned char* tmp = lds + put * kStage + kStageW + wave * kBlock;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) store_h(a, acc[m][n], acc[m][n + 2], grp, nt * 4 + wn * 2 + n, l);
-      } else if (p < rend) {
-        const float gw = a.topk_w ? a.topk_w[a.sorted_slot[p]] : 1.0f;
+        for (int n = 0; n < 4; n += 2) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int col = nt * 256 + wn * 128 + n * 32 + 16 * g;
-          if (col < a.Nout) store_y(a, acc[m][n], p, col, gw);
+          for (int b = 0; b < 2; ++b) {
+            float v[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] = acc[m][n + b][q] * gw[m];
+            unsigned char* row = tmp + (r >> 4) * (4 * kBlock) + (r & 15) * 128;
+            const int c = b * 4 + g * 2;
+            *reinterpret_cast<u32x4_t*>(row + ((c ^ (r & 7)) << 4)) =
+                u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+            *reinterpret_cast<u32x4_t*>(row + (((c + 1) ^ (r & 7)) << 4)) =
+                u32x4_t{pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15])};
+          }
+          const int col = cur.nt * 256 + wn * 128 + n * 32 + (l & 7) * 8;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int i = q * 8 + (l >> 3);
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(tmp + (i >> 4) * (4 * kBlock) + (i & 15) * 128 +
+                                                                (((l & 7) ^ (i & 7)) << 4));
+            if (p0 + i < cur.rend && col < a.Nout)
+              *reinterpret_cast<u32x4_t*>(a.y + (long long)(p0 + i) * a.Nout + col) = v;
+          }
         }
       }
     }
+    if (!more) return;
+    it += slots;
+    cur = next;
+    gw[0] = gn[0];
+    gw[1] = gn[1];
   }
 }
 
@@ -687,9 +810,9 @@ hipError_t launch_products(const Shape& s, const MxArgs& a, hipStream_t st) {
     return hipGetLastError();
   }
   static std::atomic<uint64_t> done{0};
-  const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(mx_tile_kernel<kGateUp>), kTileLds, done);
+  const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(mx_tile_kernel<kGateUp>), tile_lds(kMaxExperts), done);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(mx_tile_kernel<kGateUp>, dim3(512), dim3(256), kTileLds, st, a);
+  hipLaunchKernelGGL(mx_tile_kernel<kGateUp>, dim3(512), dim3(256), tile_lds(s.El), st, a);
   return hipGetLastError();
 }
 

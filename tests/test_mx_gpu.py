@@ -133,7 +133,8 @@ CASES = [
     (64, 128, 512, 1, 256, 0, 512, 0.0), (31, 384, 512, 4, 128, 100, 400, 0.0), (200, 256, 4, 1, 128, 0, 4, 3.0),
     # tiles of 128 rows
     (128, 128, 2, 1, 128, 0, 2, 0.0), (300, 384, 4, 2, 640, 0, 4, 0.5), (257, 640, 6, 3, 384, 1, 4, 1.0), (1001, 128, 20, 3, 128, 0, 20, 0.2),
-    (513, 2048, 2, 1, 768, 0, 1, 0.0), (700, 256, 512, 100, 128, 3, 509, 0.05),
+    (513, 2048, 2, 1, 768, 0, 1, 0.0), (4099, 1152, 8, 4, 896, 0, 8, 0.1), (20000, 128, 8, 4, 128, 0, 8, 0.1), (9000, 256, 8, 8, 256, 0, 8, 0.0),
+    (700, 256, 512, 100, 128, 3, 509, 0.05),
 ]
 
 
