@@ -111,6 +111,27 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* lds, int turn) {
   }
 }
 
+// Sums of the first N of v (a power of two) over the wave: lane l ends with one
+// of them in v[0], the one whose number it returns.  A step halves the values:
+// N + 5 exchanges rather than 6 N.
+template <int N, int O = 1, int M>
+__device__ __forceinline__ int wave_sums(float (&v)[M]) {
+  if constexpr (N > 1) {
+    const bool up = lane_id() & O;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float keep = up ? v[i + N / 2] : v[i], send = up ? v[i] : v[i + N / 2];
+      v[i] = keep + __shfl_xor(send, O, kWave);
+    }
+    return (up ? N / 2 : 0) + wave_sums<N / 2, O * 2>(v);
+  } else if constexpr (O < kWave) {
+    v[0] += __shfl_xor(v[0], O, kWave);
+    return wave_sums<1, O * 2>(v);
+  } else {
+    return 0;
+  }
+}
+
 __device__ __forceinline__ float inv_norm(float sum, int d, float eps) {
   return 1.0f / sqrtf(sum / (float)d + eps);
 }
@@ -407,11 +428,17 @@ struct CombineNormGradArgs {
 //    <dc, y_i> = r (<u, y_i> - r mean(n u) <c, y_i>)
 // needs no second look at y.  More slots read y twice, the second time from a
 // cache.
+// Narrow bfloat16 rows keep to 128 registers: four workgroups of 256 a compute
+// unit, which hide each other's loads (4099 x 2048, k = 8, of 286 MB: 75 -> 64.6
+// us).  Wider rows do not fit there: held to 168 registers 8192 x 4096, k = 4
+// takes 190 us rather than 154.
 template <bool kBF16, int L, int V, bool kOne>
-__global__ __launch_bounds__(L) void combine_norm_backward_kernel(CombineNormGradArgs a) {
-  constexpr int kN = kOne ? 1 + 2 * kBatch : 1;
-  constexpr int kSums = kOne ? kN : kBatch;
-  __shared__ float lds[2 * (L / kWave) * kSums];
+__global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine_norm_backward_kernel(
+    CombineNormGradArgs a) {
+  constexpr int kPairs = 2 * kBatch;  // <u, y_i> and <c, y_i>
+  constexpr int kSums = kOne ? 1 + kPairs : kBatch;
+  constexpr int kW = L / kWave;
+  __shared__ float lds[2 * kW * kSums];
   float acc[V][8];  // column sums over the workgroup's rows
 #pragma unroll
   for (int j = 0; j < V; ++j)
@@ -422,9 +449,9 @@ __global__ __launch_bounds__(L) void combine_norm_backward_kernel(CombineNormGra
     const long long row = t * a.d;
     const float r = a.rstd[t];
     float cc[V][8], u[V][8];
-    float s[kN];
+    float s[1] = {0.0f}, e[kOne ? kPairs : 1];
 #pragma unroll
-    for (int n = 0; n < kN; ++n) s[n] = 0.0f;
+    for (int n = 0; n < (kOne ? kPairs : 1); ++n) e[n] = 0.0f;
     int p[kBatch];
     float g[kBatch];
     if constexpr (kOne) slots8(a.pos, a.topk_w, t, a.k, 0, a.S, p, g);
@@ -464,26 +491,47 @@ __global__ __launch_bounds__(L) void combine_norm_backward_kernel(CombineNormGra
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
                 const float v = at8(raw[b], q);
-                s[1 + 2 * b] = fmaf(u[j][q], v, s[1 + 2 * b]);
-                s[2 + 2 * b] = fmaf(cc[j][q], v, s[2 + 2 * b]);
+                e[2 * b] = fmaf(u[j][q], v, e[2 * b]);
+                e[2 * b + 1] = fmaf(cc[j][q], v, e[2 * b + 1]);
               }
             }
           }
         }
       }
     }
-    group_sum<L, kSums>(s, lds, turn);
-    turn ^= 1;
+    if constexpr (kOne) {
+      float* at = lds + turn * (kW * kSums);
+      const int wave = threadIdx.x / kWave;
+      s[0] = wave_sum(s[0]);
+      if (lane_id() == 0) at[wave * kSums] = s[0];
+      if (a.dtopk_w) {
+        const int i = wave_sums<kPairs>(e);
+        if (lane_id() < kPairs) at[wave * kSums + 1 + i] = e[0];
+      }
+      __syncthreads();
+      s[0] = at[0];
+#pragma unroll
+      for (int w = 1; w < kW; ++w) s[0] += at[w * kSums];
+    } else {
+      group_sum<L, kSums>(s, lds, turn);
+    }
     const float m = s[0] / (float)a.d;
     if constexpr (kOne) {
       if (a.dtopk_w && (int)threadIdx.x < a.k) {
-        float v = 0.0f;
+        const float* at = lds + turn * (kW * kSums) + 1 + 2 * threadIdx.x;
+        float uy = at[0], cy = at[1], v = 0.0f;
+#pragma unroll
+        for (int w = 1; w < kW; ++w) {
+          uy += at[w * kSums];
+          cy += at[w * kSums + 1];
+        }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
-          if ((int)threadIdx.x == b && p[b] >= 0) v = r * (s[1 + 2 * b] - r * m * s[2 + 2 * b]);
+          if ((int)threadIdx.x == b && p[b] >= 0) v = r * (uy - r * m * cy);
         a.dtopk_w[t * a.k + threadIdx.x] = v;
       }
     }
+    turn ^= 1;
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
@@ -549,21 +597,29 @@ __global__ __launch_bounds__(L) void combine_norm_backward_kernel(CombineNormGra
 }
 
 // ---- column sums: out0 = f0 * sum of n rows of part, out1 = f1 * that
-// (f null: 1; out null: not wanted).  A workgroup takes 64 columns: 16 threads
-// of 4 columns, 16 of them over the rows.
+// (f null: 1; out null: not wanted).  A workgroup takes 16 columns: 4 threads of
+// 4 columns, 64 of them over the rows.
 __global__ __launch_bounds__(256) void column_sum_kernel(const float* part, int n, int d,
                                                          const float* f0, float* out0,
                                                          const float* f1, float* out1) {
-  __shared__ f32x4_t lds[16][16];
-  const int cq = threadIdx.x % 16, rr = threadIdx.x / 16;
-  const int c = blockIdx.x * 64 + cq * 4;  // d is a multiple of 128
+  __shared__ f32x4_t lds[64][4];
+  const int cq = threadIdx.x % 4, rr = threadIdx.x / 4;
+  const int c = blockIdx.x * 16 + cq * 4;  // d is a multiple of 128
   f32x4_t s = {0, 0, 0, 0};
 #pragma unroll 8
-  for (int i = rr; i < n; i += 16) s += *reinterpret_cast<const f32x4_t*>(part + (long long)i * d + c);
+  for (int i = rr; i < n; i += 64) s += *reinterpret_cast<const f32x4_t*>(part + (long long)i * d + c);
   lds[rr][cq] = s;
   __syncthreads();
+  if (rr >= 8) return;
+#pragma unroll
+  for (int i = 8; i < 64; i += 8) s += lds[rr + i][cq];
+  // (the eight partial sums are lanes 4 apart of the first half wave)
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] += __shfl_xor(s[j], o, kWave);
+  }
   if (rr > 0) return;
-  for (int i = 1; i < 16; ++i) s += lds[i][cq];
   if (out0) {
     f32x4_t f = {1, 1, 1, 1};
     if (f0) f = *reinterpret_cast<const f32x4_t*>(f0 + c);
@@ -578,13 +634,15 @@ __global__ __launch_bounds__(256) void column_sum_kernel(const float* part, int 
 
 hipError_t column_sum(const float* part, int n, int d, const float* f0, float* out0,
                       const float* f1, float* out1, hipStream_t st) {
-  hipLaunchKernelGGL(column_sum_kernel, dim3(d / 64), dim3(256), 0, st, part, n, d, f0, out0, f1,
+  hipLaunchKernelGGL(column_sum_kernel, dim3(d / 16), dim3(256), 0, st, part, n, d, f0, out0, f1,
                      out1);
   return hipGetLastError();
 }
 
 // Threads of a row's group and chunks a thread: a wave up to 1024 columns, 256
-// threads up to 8192, 1024 beyond.
+// threads up to 4096, 512 up to 8192, 1024 beyond.  (norm_backward at 8192 x
+// 7168: 256 threads of four chunks 195 us, 512 of two 181, 1024 of one 184;
+// combine_norm_backward at 8192 x 4096: 256 of two 154, 512 of one 186.)
 template <typename F>
 void with_group(int d, F&& f) {
   using std::integral_constant;
@@ -594,13 +652,15 @@ void with_group(int d, F&& f) {
   else if (chunks <= 128) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
   else if (chunks <= 256) go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
   else if (chunks <= 512) go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  else if (chunks <= 1024) go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  else if (chunks <= 1024) go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
   else if (chunks <= 2048) go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
   else if (chunks <= 4096) go(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
   else go(integral_constant<int, 1024>{}, integral_constant<int, 8>{});
 }
 
-// Workgroups of a backward kernel: what fills the chip.
+// Workgroups of a backward kernel: what fills the chip, and no more: each leaves
+// a row of partial sums (norm_backward at 8192 x 7168: 512 workgroups 181 + 6 us
+// of column sums, 1024 185 + 11).
 int grad_blocks(const Shape& s) {
   const int most = s.d <= 1024 ? 2048 : s.d <= 4096 ? 1024 : s.d <= 8192 ? 512 : 256;
   return std::max(1, std::min(most, s.T));

@@ -36,7 +36,7 @@ def _problem(T, d, k=1, act="bf16", E=64):
     return B.problem(T, d, E, k, 128, act=act, weight=act)
 
 
-# a row group of every kind: a wave of one and two chunks, 256 threads of one, two and four, 1024 of two, four, eight
+# a row group of every kind: a wave of one and two chunks, 256 threads of one and two, 512 of two, 1024 of two, four, eight
 WIDTHS = [128, 640, 1152, 2048, 2176, 7168, 9216, 17408, 65536]
 
 
