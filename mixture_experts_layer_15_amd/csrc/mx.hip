@@ -219,6 +219,17 @@ __device__ __forceinline__ int bound(const MxArgs& a, int e) {
   return max(0, min(a.offsets[e], a.S));
 }
 
+// The same for a wave-uniform e, by a scalar load: one through the vector
+// pipe would be waited for behind every load in flight.
+__device__ __forceinline__ int uniform_bound(const MxArgs& a, int e) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const auto* p = (const __attribute__((address_space(4))) int32_t*)(a.offsets + __builtin_amdgcn_readfirstlane(e));
+  return max(0, min((int)*p, a.S));
+#else
+  return bound(a, e);
+#endif
+}
+
 // groups[e] = number of groups of 32 rows of experts before e (groups[El]: of
 // all), each expert's counted up to a multiple of kUnit, by one workgroup of
 // kThreads threads.
@@ -273,11 +284,13 @@ __device__ __forceinline__ int feat(int r) {
   return (((r >> 2) & 1) << 4) | (((r >> 3) & 3) << 2) | (r & 3);
 }
 
+// The product of 32 x 64 by 64 x 32; byte kByte of sb is b's scale, byte 0 of sa a's.
+template <int kByte>
 __device__ __forceinline__ f32x16_t mfma_mx(u32x4_t a, u32x4_t b, f32x16_t c, uint32_t sa, uint32_t sb) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const i32x8_t av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
   const i32x8_t bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, kByte, (int)sb);
 #else
   (void)a;
   (void)b;
@@ -287,12 +300,32 @@ __device__ __forceinline__ f32x16_t mfma_mx(u32x4_t a, u32x4_t b, f32x16_t c, ui
 #endif
 }
 
-// Offset in two units (a stage of 128 K values of 32 rows) of the 16 bytes that
-// lane l moves of half block h: row 16 h + l % 16, chunk l / 16 (half chunk % 2
-// of unit chunk / 2).
+// How a block of 32 rows of a stage (128 K values: 64 bytes, 4 chunks of 16)
+// lies in LDS, and what lane l moves there as half block h.  Consecutive lanes
+// write consecutive places, and four of them have to read 64 consecutive bytes:
+// 16 rows' first chunks, then their second ones and so on pass the cache at
+// 9.7 TB/s on all compute units, 64 bytes of one row after the other at 34.
+// From units: lane l takes row 16 h + l % 16, chunk l / 16 (half chunk % 2 of
+// unit chunk / 2); offset in the two units of the stage, and a chunk's place.
 __device__ __forceinline__ uint32_t unit_offset(int h, int l) {
   const int c = l >> 4;
   return (c >> 1) * 1024 + ((c & 1) * 32 + 16 * h + (l & 15)) * 16;
+}
+
+__device__ __forceinline__ int unit_place(int row, int chunk) {
+  return (row >> 4) * 1024 + chunk * 256 + (row & 15) * 16;
+}
+
+// From rows: lane l takes row 16 h + l / 4.  The chunks of a row change places,
+// so that any 8 or 16 consecutive rows' places of one chunk are in different banks.
+__device__ __forceinline__ int row_turn(int row) {
+  return ((row >> 1) & 2) | (((row >> 1) ^ (row >> 3)) & 1);
+}
+
+__device__ __forceinline__ uint32_t row_chunk(int l) { return 16u * ((l & 3) ^ row_turn(l >> 2)); }
+
+__device__ __forceinline__ int row_place(int row, int chunk) {
+  return row * 64 + ((chunk ^ row_turn(row & 15)) << 4);
 }
 
 // Epilogue of a gate/up pair: 16 consecutive features of token row r of group
@@ -341,7 +374,7 @@ __device__ __forceinline__ void store_y(const MxArgs& a, const f32x16_t& v, int 
 // that a handful of experts still fills the chip.  A wave keeps kD steps of
 // 64 K values in flight; nothing passes LDS before the results.
 constexpr int kNB = 4;
-constexpr int kD = 4;
+constexpr int kD = 3;
 
 template <bool kGateUp>
 __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxArgs a) {
@@ -361,96 +394,128 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxArgs a) {
   const uint32_t smat = (uint32_t)(a.K / 32) * a.Nout;
   const uint32_t unit = a.blocked ? 1024u : 32u;
   const uint32_t voffW = a.blocked ? 16u * l : (uint32_t)feat(r) * wrow + 16u * g;
-  const uint32_t voffS = (uint32_t)g * a.Nout + feat(r);
-  for (int it = xcd * per_xcd + (int)blockIdx.x / kNumXcd; it < end; it += slots) {
-    const int e = expert_of(groups, a.El, it / ngrp);
-    const int m_tiles = __builtin_amdgcn_readfirstlane(groups[e + 1] - groups[e]);
-    const int in = it - groups[e] * ngrp;
-    const int nb = __builtin_amdgcn_readfirstlane(in / m_tiles);       // feature group
+  // Scales of a step: a lane loads four columns of a K block (down: 128 columns in
+  // a load, gate/up: 64 a matrix) and each block's are fetched from the lane that
+  // holds them; a byte a lane and block was a fifth of the time of the loads.
+  const uint32_t voffS = kGateUp ? (uint32_t)((l >> 4) & 1) * a.Nout + 4u * (l & 15)
+                                 : (uint32_t)g * a.Nout + 4u * r;
+  const int from = 4 * (g * (8 * H) + feat(r) / 4), shift = 8 * (r & 3);
+  struct Item {
+    int e, nb, grp, row0, rend, slot;  // feature group, row group, rows; slot of the lane's row
+  };
+  auto decode = [&](int it) {
+    Item i;
+    i.e = expert_of(groups, a.El, it / ngrp);
+    const int m_tiles = __builtin_amdgcn_readfirstlane(groups[i.e + 1] - groups[i.e]);
+    const int in = it - groups[i.e] * ngrp;
+    i.nb = __builtin_amdgcn_readfirstlane(in / m_tiles);
     const int mt = __builtin_amdgcn_readfirstlane(in % m_tiles);
-    const int grp = __builtin_amdgcn_readfirstlane(groups[e]) + mt;
-    const int row0 = __builtin_amdgcn_readfirstlane(bound(a, e)) + mt * 32;
-    const int rend = __builtin_amdgcn_readfirstlane(bound(a, e + 1));
-    const int p = min(row0 + r, rend - 1);
-    __amdgpu_buffer_rsrc_t rA, rAS;
-    uint32_t voffA, voffAS;
-    const int slot = a.sorted_slot[p];
-    if constexpr (kGateUp) {
-      const uint32_t t = (uint32_t)slot / (uint32_t)a.k;
-      rA = rsrc(a.A, a.a_bytes);
-      rAS = rsrc(a.AS, a.as_bytes);
-      voffA = t * wrow + 16u * g;
-      voffAS = t * (uint32_t)(a.K / 32) + g;
-    } else {
-      rA = rsrc(a.A + (long long)grp * nS * 1024, (uint32_t)nS * 1024u);
-      rAS = rsrc(a.AS + (long long)grp * nS * 64, (uint32_t)nS * 64u);
-      voffA = 16u * l;
-      voffAS = (uint32_t)(r * 2 * nS) + g;
-    }
-    const __amdgpu_buffer_rsrc_t rW0 = rsrc(a.W0 + (size_t)e * wmat, wmat);
-    const __amdgpu_buffer_rsrc_t rW1 = kGateUp ? rsrc(a.W1 + (size_t)e * wmat, wmat) : rW0;
-    const __amdgpu_buffer_rsrc_t rS0 = rsrc(a.S0 + (size_t)e * smat, smat);
-    const __amdgpu_buffer_rsrc_t rS1 = kGateUp ? rsrc(a.S1 + (size_t)e * smat, smat) : rS0;
-    u32x4_t wb[kD][kNB], tb[kD];
-    uint32_t ws[kD][kNB], ts[kD];
-    auto issue = [&](int s, int d) {
+    i.grp = __builtin_amdgcn_readfirstlane(groups[i.e]) + mt;
+    i.row0 = uniform_bound(a, i.e) + mt * 32;
+    i.rend = uniform_bound(a, i.e + 1);
+    i.slot = a.sorted_slot[min(i.row0 + r, i.rend - 1)];
+    return i;
+  };
+  u32x4_t wb[kD][kNB], tb[kD];
+  uint32_t ws[kD][kGateUp ? 2 : 1];
+  uint8_t ts[kD];
+  // Step s of item i into place d.  A step that the wave does not have (or an
+  // item that is not there) reads zeros, without a branch: the number of loads
+  // in flight is then the same on every path, and the waits for them are exact.
+  auto issue = [&](const Item& i, bool there, int s, int d) {
+    const bool on = there && s < s1;
+    const uint32_t wn = on ? wmat : 0, sn = on ? smat : 0;
+    const __amdgpu_buffer_rsrc_t rW0 = rsrc(a.W0 + (size_t)i.e * wmat, wn);
+    const __amdgpu_buffer_rsrc_t rW1 = kGateUp ? rsrc(a.W1 + (size_t)i.e * wmat, wn) : rW0;
+    const __amdgpu_buffer_rsrc_t rS0 = rsrc(a.S0 + (size_t)i.e * smat, sn);
+    const __amdgpu_buffer_rsrc_t rS1 = kGateUp ? rsrc(a.S1 + (size_t)i.e * smat, sn) : rS0;
 #pragma unroll
-      for (int n = 0; n < kNB; ++n) {
-        const int fb = nb * H + n % H;
-        wb[d][n] = __builtin_amdgcn_raw_buffer_load_b128(n >= H ? rW1 : rW0, voffW,
-                                                         (uint32_t)fb * 32u * wrow + s * unit, 2);
-        ws[d][n] = __builtin_amdgcn_raw_buffer_load_b8(n >= H ? rS1 : rS0, voffS,
-                                                       (uint32_t)(2 * s) * a.Nout + fb * 32u, 0);
-      }
-      tb[d] = __builtin_amdgcn_raw_buffer_load_b128(rA, voffA, s * (kGateUp ? 32u : 1024u), 0);
-      ts[d] = __builtin_amdgcn_raw_buffer_load_b8(rAS, voffAS, 2u * s, 0);
-    };
+    for (int n = 0; n < kNB; ++n) {
+      const int fb = i.nb * H + n % H;
+      wb[d][n] = __builtin_amdgcn_raw_buffer_load_b128(n >= H ? rW1 : rW0, voffW,
+                                                       (uint32_t)fb * 32u * wrow + s * unit, 2);
+    }
+    const uint32_t at = (uint32_t)(2 * s) * a.Nout + i.nb * (32u * H);
+    ws[d][0] = __builtin_amdgcn_raw_buffer_load_b32(rS0, voffS, at, 0);
+    if constexpr (kGateUp) ws[d][1] = __builtin_amdgcn_raw_buffer_load_b32(rS1, voffS, at, 0);
+    if constexpr (kGateUp) {
+      const uint32_t t = (uint32_t)i.slot / (uint32_t)a.k;
+      tb[d] = __builtin_amdgcn_raw_buffer_load_b128(rsrc(a.A, on ? a.a_bytes : 0), t * wrow + 16u * g, s * 32u, 0);
+      ts[d] = __builtin_amdgcn_raw_buffer_load_b8(rsrc(a.AS, on ? a.as_bytes : 0), t * (uint32_t)(a.K / 32) + g,
+                                                  2u * s, 0);
+    } else {
+      tb[d] = __builtin_amdgcn_raw_buffer_load_b128(
+          rsrc(a.A + (long long)i.grp * nS * 1024, on ? (uint32_t)nS * 1024u : 0), 16u * l, s * 1024u, 0);
+      ts[d] = __builtin_amdgcn_raw_buffer_load_b8(
+          rsrc(a.AS + (long long)i.grp * nS * 64, on ? (uint32_t)nS * 64u : 0), (uint32_t)(r * 2 * nS) + g, 2u * s, 0);
+    }
+  };
+  auto multiply = [&](f32x16_t(&acc)[kNB], int d) {
+#pragma unroll
+    for (int n = 0; n < kNB; ++n) {
+      const int v = __builtin_amdgcn_ds_bpermute(from + 32 * (n % H), (int)ws[d][n / H]);
+      acc[n] = mfma_mx<0>(wb[d][n], tb[d], acc[n], (uint32_t)v >> shift, ts[d]);
+    }
+  };
+  const __amdgpu_buffer_rsrc_t rG = rsrc(a.topk_w, !kGateUp && a.topk_w ? (uint32_t)a.S * 4u : 0);
+  auto gate_of = [&](const Item& i) { return __builtin_amdgcn_raw_buffer_load_b32(rG, 4u * i.slot, 0, 0); };
+  int it = xcd * per_xcd + (int)blockIdx.x / kNumXcd;
+  if (it >= end) return;
+  auto at_most = [&](int i) { return i < end ? i : it; };
+  Item cur = decode(it), next = decode(at_most(it + slots));
+  uint32_t gw = gate_of(cur);
+#pragma unroll
+  for (int d = 0; d < kD; ++d) {
+    issue(cur, true, s0 + d, d);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  while (true) {
+    const bool more = it + slots < end;
+    // (two items ahead: a wait for its slots waits for nothing later)
+    const Item third = decode(at_most(it + 2 * slots));
     f32x16_t acc[kNB];
 #pragma unroll
     for (int n = 0; n < kNB; ++n) acc[n] = f32x16_t{};
-#pragma unroll
-    for (int d = 0; d < kD; ++d)
-      if (s0 + d < s1) issue(s0 + d, d);
-    for (int s = s0; s < s1; s += kD) {
+    int s = s0;
+    for (; s + kD < s1; s += kD) {
 #pragma unroll
       for (int d = 0; d < kD; ++d) {
-        if (s + d < s1) {
-#pragma unroll
-          for (int n = 0; n < kNB; ++n) acc[n] = mfma_mx(wb[d][n], tb[d], acc[n], ws[d][n], ts[d]);
-          if (s + d + kD < s1) issue(s + d + kD, d);
-        }
+        multiply(acc, d);
+        __builtin_amdgcn_sched_barrier(0);
+        issue(cur, true, s + d + kD, d);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    const float gw = !kGateUp && a.topk_w ? a.topk_w[slot] : 1.0f;
+    // the next item's first steps fly while this one's results are joined
+    const uint32_t next_gw = gate_of(next);
+#pragma unroll
+    for (int d = 0; d < kD; ++d) {
+      multiply(acc, d);
+      __builtin_amdgcn_sched_barrier(0);
+      issue(next, more, s0 + d, d);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const int row0 = cur.row0, rend = cur.rend, nb = cur.nb, grp = cur.grp;
     // results of block n meet in wave n (gate/up: of pair n in wave n)
     __syncthreads();  // the last item's sums have been read
 #pragma unroll
     for (int n = 0; n < kNB; ++n) {
-      if (n % H == wave) continue;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         red[wave][n][q][l] = f32x4_t{acc[n][4 * q], acc[n][4 * q + 1], acc[n][4 * q + 2], acc[n][4 * q + 3]};
     }
     __syncthreads();
     if (wave < H) {
-      // in wave order whichever wave adds
       f32x16_t sum[kNB / H];
 #pragma unroll
       for (int i = 0; i < kNB / H; ++i) {
-        sum[i] = f32x16_t{};
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int q = 0; q < 4; ++q) {
+          f32x4_t v = red[0][i * H + wave][q][l];
 #pragma unroll
-          for (int n = 0; n < kNB; ++n) {
-            if (n != i * H + wave) continue;
+          for (int w = 1; w < 4; ++w) v += red[w][i * H + wave][q][l];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const f32x4_t v = w == wave ? f32x4_t{acc[n][4 * q], acc[n][4 * q + 1], acc[n][4 * q + 2], acc[n][4 * q + 3]}
-                                          : red[w][n][q][l];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) sum[i][4 * q + j] += v[j];
-            }
-          }
+          for (int j = 0; j < 4; ++j) sum[i][4 * q + j] = v[j];
         }
       }
       const int fb = nb * H + wave;
@@ -458,9 +523,14 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxArgs a) {
         const uint32_t byte = store_h(a, sum[0], sum[1], grp, fb, l);
         if (g == 0) *h_scale(a, grp, r, fb) = (uint8_t)byte;
       } else if (row0 + r < rend) {
-        store_y(a, sum[0], row0 + r, fb * 32 + 16 * g, gw);
+        store_y(a, sum[0], row0 + r, fb * 32 + 16 * g, a.topk_w ? __uint_as_float(gw) : 1.0f);
       }
     }
+    if (!more) break;
+    it += slots;
+    cur = next;
+    next = third;
+    gw = next_gw;
   }
 }
 
@@ -468,11 +538,10 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxArgs a) {
 // gate and the up rows of the same features) through a ring of LDS stages of
 // 128 K values, filled by LDS-DMA.  Four waves of 64 x 128; two workgroups a
 // CU, so that the conversion of one's results runs beside the other's products.
-// In a stage a 32-row block is [row / 16][16-byte chunk][row % 16]: a DMA
-// instruction takes 64 bytes of each of 16 rows (the cache counts lines, not
-// bytes: 32 bytes of 32 rows made it the bottleneck), and an operand read is
-// two runs of 256 bytes.  The rows' scales come 16 bytes (four stages) at a
-// time, for the same reason, and are read into registers.
+// A DMA instruction takes 64 bytes of each of 16 rows (the cache counts lines,
+// not bytes: 32 bytes of 32 rows made it the bottleneck).  The rows' scales come
+// 16 bytes (four stages) at a time, for the same reason, and are read into
+// registers.
 constexpr int kBM = 4;        // groups of 32 rows of a tile
 constexpr int kStages = 3;
 constexpr int kBlock = 2048;  // of 32 rows
@@ -514,8 +583,10 @@ __device__ __forceinline__ void stage_barrier() {
 }
 
 // The ring runs on across items: the next item's first stages and addresses are
-// under way before the present one's results are converted and stored.
-template <bool kGateUp>
+// under way before the present one's results are converted and stored.  kAhead
+// stages are under way beside the one that is multiplied, of which all but the
+// newest have arrived when their turn comes (K = 128 has one stage only).
+template <bool kGateUp, int kAhead>
 __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   int* groups = reinterpret_cast<int*>(lds + kTileTable);
@@ -532,7 +603,7 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
   uint32_t voffW[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    voffW[h] = a.blocked ? unit_offset(h, l) : (uint32_t)feat(16 * h + (l & 15)) * wrow + 16u * (l >> 4);
+    voffW[h] = a.blocked ? unit_offset(h, l) : (uint32_t)feat(16 * h + (l >> 2)) * wrow + row_chunk(l);
   const int n_items = groups[a.El] / kBM * ntn;
   const int per_xcd = (n_items + kNumXcd - 1) / kNumXcd;
   const int xcd = blockIdx.x % kNumXcd, slots = gridDim.x / kNumXcd;
@@ -561,63 +632,71 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
     t.nt = __builtin_amdgcn_readfirstlane(in / m_tiles);
     const int mt = in - t.nt * m_tiles;
     t.g0 = first + mt * kBM;
-    t.row0 = __builtin_amdgcn_readfirstlane(bound(a, e)) + mt * kBM * 32;
-    t.rend = __builtin_amdgcn_readfirstlane(bound(a, e + 1));
+    t.row0 = uniform_bound(a, e) + mt * kBM * 32;
+    t.rend = uniform_bound(a, e + 1);
     return t;
   };
   // This lane's slots of an item: gate/up: of the two rows that it moves, row
-  // l % 16 of a half block; down: of the two rows whose results it has.
+  // l / 4 of a half block; down: of the two rows whose results it has.
   auto load_slots = [&](const Item& t, int (&slot)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int row = kGateUp ? wave * 32 + 16 * h + (l & 15) : (wm * 2 + h) * 32 + r;
+      const int row = kGateUp ? wave * 32 + 16 * h + (l >> 2) : (wm * 2 + h) * 32 + r;
       slot[h] = a.sorted_slot[min(t.row0 + row, t.rend - 1)];
     }
   };
 
   // This wave's LDS-DMA of an item: A block `wave`, W blocks wave and wave + 4,
   // the scales of A block `wave`, and K block `wave` of the weights' scales.
-  // Lane l: row l % 16 of a half block, chunk l / 16.
   __amdgpu_buffer_rsrc_t rA, rAS, rW0, rW1, rS0, rS1;
   uint32_t voffA[2], voffAS, voffS, sW0, sW1;
   constexpr uint32_t stepA = kGateUp ? 64 : 2048;
-  auto aim = [&](const Item& t, const int (&slot)[2]) {
+  auto aim = [&](const Item& t, const int (&slot)[2], bool there) {
+    const uint32_t on = there ? ~0u : 0u;  // (of the buffers' sizes)
     if constexpr (kGateUp) {
       uint32_t tok[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         tok[h] = (uint32_t)slot[h] / (uint32_t)a.k;
-        voffA[h] = tok[h] * wrow + 16u * (l >> 4);
+        voffA[h] = tok[h] * wrow + row_chunk(l);
       }
-      rA = rsrc(a.A, a.a_bytes);
-      rAS = rsrc(a.AS, a.as_bytes);
-      voffAS = (l & 16 ? tok[1] : tok[0]) * (uint32_t)(a.K / 32);  // lanes 0 .. 31: their rows
+      rA = rsrc(a.A, a.a_bytes & on);
+      rAS = rsrc(a.AS, a.as_bytes & on);
+      // lanes 0 .. 31: their rows, which other lanes move
+      const uint32_t lo = __shfl((int)tok[0], 4 * (l & 15), kWave), hi = __shfl((int)tok[1], 4 * (l & 15), kWave);
+      voffAS = (l & 16 ? hi : lo) * (uint32_t)(a.K / 32);
     } else {
       // (all kBM groups of the tile exist; rows behind the segment hold whatever
       // was there and only reach results that are not stored)
-      rA = rsrc(a.A + (long long)(t.g0 + wave) * (2 * nK) * 1024, (uint32_t)nK * 2048u);
-      rAS = rsrc(a.AS + (long long)(t.g0 + wave) * (4 * nK) * 32, (uint32_t)nK * 128u);
+      rA = rsrc(a.A + (long long)(t.g0 + wave) * (2 * nK) * 1024, (uint32_t)nK * 2048u & on);
+      rAS = rsrc(a.AS + (long long)(t.g0 + wave) * (4 * nK) * 32, (uint32_t)nK * 128u & on);
 #pragma unroll
       for (int h = 0; h < 2; ++h) voffA[h] = unit_offset(h, l);
       voffAS = (uint32_t)r * (4 * nK);
     }
     const uint32_t f0 = (uint32_t)t.nt * cols;
-    rW0 = rsrc(a.W0 + (size_t)t.e * wmat, wmat);
-    rW1 = kGateUp ? rsrc(a.W1 + (size_t)t.e * wmat, wmat) : rW0;
+    rW0 = rsrc(a.W0 + (size_t)t.e * wmat, wmat & on);
+    rW1 = kGateUp ? rsrc(a.W1 + (size_t)t.e * wmat, wmat & on) : rW0;
     // (down, 128 columns left: the second half repeats the first and is not stored)
-    sW0 = (f0 + 32u * wave) * wrow;
-    sW1 = kGateUp || f0 + 128u >= (uint32_t)a.Nout ? sW0 : sW0 + 128u * wrow;
+    sW0 = __builtin_amdgcn_readfirstlane((f0 + 32u * wave) * wrow);
+    sW1 = __builtin_amdgcn_readfirstlane(kGateUp || f0 + 128u >= (uint32_t)a.Nout ? sW0 : sW0 + 128u * wrow);
     // scales of one K block: 4 rows a lane (gate/up: 32 lanes for either matrix)
-    rS0 = rsrc(a.S0 + (size_t)t.e * smat, smat);
-    rS1 = kGateUp ? rsrc(a.S1 + (size_t)t.e * smat, smat) : rS0;
+    rS0 = rsrc(a.S0 + (size_t)t.e * smat, smat & on);
+    rS1 = kGateUp ? rsrc(a.S1 + (size_t)t.e * smat, smat & on) : rS0;
     voffS = (uint32_t)wave * a.Nout + f0 + 4u * (kGateUp ? l & 31 : l);
   };
   // this lane's operands in a stage
   const int first_w = wn * (kGateUp ? 2 : 4);
-  const int read_a = (r >> 4) * 1024 + g * 256 + (r & 15) * 16 + wm * 2 * kBlock;
-  const int read_w = (r >> 4) * 1024 + g * 256 + (r & 15) * 16 + kStageW + first_w * kBlock;
+  int read_a[2], read_w[2];  // of either step
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    read_a[q] = wm * 2 * kBlock + (kGateUp ? row_place(r, 2 * q + g) : unit_place(r, 2 * q + g));
+    read_w[q] = kStageW + first_w * kBlock + (a.blocked ? unit_place(r, 2 * q + g) : row_place(r, 2 * q + g));
+  }
   const int read_ws = kStageWS + g * 256 + first_w * 32 + feat(r);
   int put = 0;  // the ring's next place
+  // (an aim without memory writes zeros into places that no stage will be read
+  // from, and keeps the number of loads in flight what the waits count on)
   auto issue = [&](int s) {
     unsigned char* st = lds + put * kStage;
 #pragma unroll
@@ -646,62 +725,45 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
     put_rs ^= 1;
   };
 
-  // stages that are under way beside the one that is multiplied: two, of which
-  // one may still be when the next one's turn comes (K = 128: one, none)
-  const int ahead = nK == 1 ? 1 : 2;
-  static_assert(kStages == 3, "a place for the stage being read and two ahead");
+  static_assert(kStages >= kAhead + 1, "a place for the stage being read and those ahead");
   const int e0 = expert_of(groups, a.El, it / ntn * kBM);
   Item cur = place(e0, it - groups[e0] / kBM * ntn);
+  // (slots and gates are fetched an item ahead, and taken behind a wait that covers
+  // them: a wait for their own sake would be one for the whole ring)
   int slot[2] = {0, 0};
-  if (kGateUp || a.topk_w) load_slots(cur, slot);
-  aim(cur, slot);
-  float gw[2] = {1.0f, 1.0f};
-  if (!kGateUp && a.topk_w) {
-    gw[0] = a.topk_w[slot[0]];
-    gw[1] = a.topk_w[slot[1]];
-  }
+  float gw[2] = {1.0f, 1.0f}, gn[2] = {1.0f, 1.0f};
+  const bool use_slots = kGateUp || a.topk_w;
+  auto load_gates = [&](float (&w)[2]) {
+    if (kGateUp || !a.topk_w) return;
+    w[0] = a.topk_w[slot[0]];
+    w[1] = a.topk_w[slot[1]];
+  };
+  auto after = [&](const Item& t, bool there) { return there ? place(t.e, t.in + slots) : t; };
+  if (use_slots) load_slots(cur, slot);
+  aim(cur, slot, true);
+  load_gates(gw);
+  Item next = after(cur, it + slots < end);
+  if (use_slots) load_slots(next, slot);
   issue_row_scales(0);
-  issue(0);
-  if (ahead == 2) issue(1);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) issue(i);
+  // The next stage is there for every wave, and what was asked for before the
+  // newest stage.
+  auto arrive = [&] {
+    stage_barrier<kIssued*(kAhead - 1)>();
+    asm volatile("" : "+v"(slot[0]), "+v"(slot[1]), "+v"(gw[0]), "+v"(gw[1]), "+v"(gn[0]), "+v"(gn[1]));
+  };
+  arrive();
   int get = 0;
-  if (ahead == 2) stage_barrier<kIssued>();
-  else stage_barrier<0>();
   for (;;) {
     const bool more = it + slots < end;
-    Item next = cur;
-    if (more) {
-      next = place(cur.e, cur.in + slots);
-      if (kGateUp || a.topk_w) load_slots(next, slot);
-    }
-    float gn[2] = {1.0f, 1.0f};
     f32x16_t acc[2][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int n = 0; n < 4; ++n) acc[m][n] = f32x16_t{};
     u32x4_t rs[2];  // row scales of this stage (word 0) and the next ones
-    for (int s = 0; s < nK; ++s) {
-      // (stage 0 was waited for before the last item's results were stored)
-      if (s > 0) {
-        if (s + 1 < nK || more) stage_barrier<kIssued>();
-        else stage_barrier<0>();
-      }
-      // Every wave has read the stage before this one, whose place the new one
-      // takes, and the row scales before the present ones.
-      if (s % 4 == 1 && s + 3 < nK) issue_row_scales(s + 3);
-      if (s + ahead < nK) {
-        issue(s + ahead);
-      } else if (more) {
-        if (s + ahead == nK) {
-          aim(next, slot);
-          if (!kGateUp && a.topk_w) {
-            gn[0] = a.topk_w[slot[0]];
-            gn[1] = a.topk_w[slot[1]];
-          }
-          issue_row_scales(0);
-        }
-        issue(s + ahead - nK);
-      }
+    auto multiply = [&](int s) {
       const unsigned char* st = lds + get * kStage;
       get = get == kStages - 1 ? 0 : get + 1;
       if (s % 4 == 0) {
@@ -716,11 +778,11 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
 #pragma unroll
-        for (int m = 0; m < 2; ++m) av[q][m] = *reinterpret_cast<const u32x4_t*>(st + read_a + q * 512 + m * kBlock);
+        for (int m = 0; m < 2; ++m) av[q][m] = *reinterpret_cast<const u32x4_t*>(st + read_a[q] + m * kBlock);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           const int b = kGateUp ? (n >> 1) * 4 + (n & 1) : n;  // of the wave's weight blocks
-          wv[q][n] = *reinterpret_cast<const u32x4_t*>(st + read_w + q * 512 + b * kBlock);
+          wv[q][n] = *reinterpret_cast<const u32x4_t*>(st + read_w[q] + b * kBlock);
           ws[q][n] = st[read_ws + q * 512 + b * 32];
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -732,18 +794,33 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
         rs[m] = u32x4_t{rs[m][1], rs[m][2], rs[m][3], 0};
       }
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int m = 0; m < 2; ++m) acc[m][n] = mfma_mx<0>(wv[0][n], av[0][m], acc[m][n], ws[0][n], as[m]);
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
-            acc[m][n] = mfma_mx(wv[q][n], av[q][m], acc[m][n], ws[q][n], as[m] >> (16 * q));
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) acc[m][n] = mfma_mx<2>(wv[1][n], av[1][m], acc[m][n], ws[1][n], as[m]);
+    };
+    Item third = next;
+    for (int s = 0; s < nK; ++s) {
+      // Every wave has read the stage before this one, whose place the new one
+      // takes, and the row scales before the present ones.  (Stage 0 was waited for
+      // before the last item's results were stored.)
+      if (s > 0) stage_barrier<kIssued*(kAhead - 1)>();
+      int at = s + kAhead;
+      if (at == nK) {  // the next item's first stages follow
+        aim(next, slot, more);
+        load_gates(gn);
+        third = after(next, it + 2 * slots < end);
+        if (use_slots) load_slots(third, slot);
+      }
+      if (at >= nK) at -= nK;
+      if (at == 0 || (s % 4 == 1 && s + 3 < nK)) issue_row_scales(at == 0 ? 0 : s + 3);
+      issue(at);
+      multiply(s);
     }
-    // the next item's first stage, before the stores that follow are counted
-    if (more) {
-      if (ahead == 2) stage_barrier<kIssued>();
-      else stage_barrier<0>();
-    }
+    arrive();  // the next item's first stage, before the stores that follow are counted
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const int grp = cur.g0 + wm * 2 + m, p0 = cur.row0 + (wm * 2 + m) * 32;
@@ -785,12 +862,14 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
         }
       }
     }
-    if (!more) return;
+    if (!more) break;
     it += slots;
     cur = next;
+    next = third;
     gw[0] = gn[0];
     gw[1] = gn[1];
   }
+  __builtin_amdgcn_s_waitcnt((0 & 15) | (7 << 4) | (15 << 8));  // no LDS-DMA outlives the workgroup
 }
 
 // Which kernel takes a problem.
@@ -809,11 +888,14 @@ hipError_t launch_products(const Shape& s, const MxArgs& a, hipStream_t st) {
     hipLaunchKernelGGL(mx_stream_kernel<kGateUp>, dim3(grid), dim3(256), 0, st, a);
     return hipGetLastError();
   }
-  static std::atomic<uint64_t> done{0};
-  const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(mx_tile_kernel<kGateUp>), tile_lds(kMaxExperts), done);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(mx_tile_kernel<kGateUp>, dim3(512), dim3(256), tile_lds(s.El), st, a);
-  return hipGetLastError();
+  auto launch = [&](auto kern, std::atomic<uint64_t>& done) {
+    const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(kern), tile_lds(kMaxExperts), done);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, dim3(512), dim3(256), tile_lds(s.El), st, a);
+    return hipGetLastError();
+  };
+  static std::atomic<uint64_t> done_one{0}, done_two{0};
+  return a.K == 128 ? launch(mx_tile_kernel<kGateUp, 1>, done_one) : launch(mx_tile_kernel<kGateUp, 2>, done_two);
 }
 
 template <bool kQuantize>
