@@ -554,7 +554,7 @@ constexpr int kTileTable = kRowScales + 2 * kBM * 512;  // groups before each ex
 inline int tile_lds(int El) { return kTileTable + (El + 1) * 4; }
 
 // One LDS-DMA load per active lane: lane i's 16 (4) bytes, from voff + soff in
-// the buffer, land at lds + 16 i (4 i); lds is wave-uniform.
+// the buffer (from), land at lds + 16 i (4 i); lds is wave-uniform.
 __device__ __forceinline__ void lds_dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, unsigned char* lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, soff, 0, 0);
@@ -563,11 +563,12 @@ __device__ __forceinline__ void lds_dma16(__amdgpu_buffer_rsrc_t r, uint32_t vof
 #endif
 }
 
-__device__ __forceinline__ void lds_dma4(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, unsigned char* lds) {
+__device__ __forceinline__ void lds_dma4(const uint8_t* from, unsigned char* lds) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, voff, soff, 0, 0);
+  __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)const_cast<uint8_t*>(from),
+                                   (__attribute__((address_space(3))) void*)lds, 4, 0, 0);
 #else
-  (void)r, (void)voff, (void)soff, (void)lds;
+  (void)from, (void)lds;
 #endif
 }
 
@@ -583,10 +584,13 @@ __device__ __forceinline__ void stage_barrier() {
 }
 
 // The ring runs on across items: the next item's first stages and addresses are
-// under way before the present one's results are converted and stored.  kAhead
-// stages are under way beside the one that is multiplied, of which all but the
-// newest have arrived when their turn comes (K = 128 has one stage only).
-template <bool kGateUp, int kAhead>
+// under way before the present one's results are converted and stored.  A stage is
+// two steps of 64 K values: the operands of one are read while the other's
+// products run, across stages and items, so that a wave's matrix instructions
+// do not stand behind its reads, and the loads of the stage after next go out
+// between them.  (Reads and loads in front of the products: 158 us for the
+// Qwen3 prefill gate/up.)
+template <bool kGateUp>
 __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   int* groups = reinterpret_cast<int*>(lds + kTileTable);
@@ -594,7 +598,7 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int l = lane_id(), g = l >> 5, r = l & 31;
   const int wm = wave >> 1, wn = wave & 1;
-  const int nK = a.K / 128;
+  const int nK = a.K / 128, nS = max(nK, 2);  // (a lone stage is followed by one of zeros)
   const int cols = kGateUp ? 128 : 256;  // output columns of a tile
   const int ntn = (a.Nout + cols - 1) / cols;
   const uint32_t wrow = (uint32_t)a.K / 2, wmat = (uint32_t)a.Nout * wrow;
@@ -648,8 +652,9 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
 
   // This wave's LDS-DMA of an item: A block `wave`, W blocks wave and wave + 4,
   // the scales of A block `wave`, and K block `wave` of the weights' scales.
-  __amdgpu_buffer_rsrc_t rA, rAS, rW0, rW1, rS0, rS1;
-  uint32_t voffA[2], voffAS, voffS, sW0, sW1;
+  __amdgpu_buffer_rsrc_t rA, rAS, rW0, rW1;
+  uint32_t voffA[2], voffAS, sW0, sW1;
+  const uint8_t* ps;  // this lane's four scales of stage 0
   constexpr uint32_t stepA = kGateUp ? 64 : 2048;
   auto aim = [&](const Item& t, const int (&slot)[2], bool there) {
     const uint32_t on = there ? ~0u : 0u;  // (of the buffers' sizes)
@@ -680,10 +685,12 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
     // (down, 128 columns left: the second half repeats the first and is not stored)
     sW0 = __builtin_amdgcn_readfirstlane((f0 + 32u * wave) * wrow);
     sW1 = __builtin_amdgcn_readfirstlane(kGateUp || f0 + 128u >= (uint32_t)a.Nout ? sW0 : sW0 + 128u * wrow);
-    // scales of one K block: 4 rows a lane (gate/up: 32 lanes for either matrix)
-    rS0 = rsrc(a.S0 + (size_t)t.e * smat, smat & on);
-    rS1 = kGateUp ? rsrc(a.S1 + (size_t)t.e * smat, smat & on) : rS0;
-    voffS = (uint32_t)wave * a.Nout + f0 + 4u * (kGateUp ? l & 31 : l);
+    // scales of one K block: 4 rows a lane (gate/up: 32 lanes for either matrix).
+    // These loads have no bounds of their own: columns behind the matrix repeat its
+    // last ones, and the zeros behind a lone stage take that stage's (a row that
+    // a NaN among them spoils is NaN already).
+    const uint32_t f = kGateUp ? f0 + 4u * (l & 31) : min(f0 + 4u * l, (uint32_t)a.Nout - 4u);
+    ps = (kGateUp && g ? a.S1 : a.S0) + (size_t)t.e * smat + (uint32_t)wave * a.Nout + f;
   };
   // this lane's operands in a stage
   const int first_w = wn * (kGateUp ? 2 : 4);
@@ -697,35 +704,30 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
   int put = 0;  // the ring's next place
   // (an aim without memory writes zeros into places that no stage will be read
   // from, and keeps the number of loads in flight what the waits count on)
-  auto issue = [&](int s) {
+  constexpr int kIssued = 7;  // LDS-DMA instructions of a stage
+  auto issue_one = [&](int s, int i) {
     unsigned char* st = lds + put * kStage;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    const int h = i & 1;
+    if (i < 2) {
       lds_dma16(rA, voffA[h], (uint32_t)s * stepA, st + wave * kBlock + h * 1024);
+    } else if (i < 4) {
       lds_dma16(rW0, voffW[h], sW0 + (uint32_t)s * stepW, st + kStageW + wave * kBlock + h * 1024);
+    } else if (i < 6) {
       lds_dma16(rW1, voffW[h], sW1 + (uint32_t)s * stepW, st + kStageW + (wave + 4) * kBlock + h * 1024);
-    }
-    unsigned char* sc = st + kStageWS + wave * 256;
-    if constexpr (kGateUp) {
-      if (g == 0) {
-        lds_dma4(rS0, voffS, (uint32_t)(4 * s) * a.Nout, sc);
-        lds_dma4(rS1, voffS, (uint32_t)(4 * s) * a.Nout, sc + 128);
-      }
     } else {
-      lds_dma4(rS0, voffS, (uint32_t)(4 * s) * a.Nout, sc);
+      lds_dma4(ps + (uint32_t)(4 * min(s, nK - 1)) * a.Nout, st + kStageWS + wave * 256);
     }
-    put = put == kStages - 1 ? 0 : put + 1;
+    if (i == kIssued - 1) put = put == kStages - 1 ? 0 : put + 1;
   };
-  constexpr int kIssued = kGateUp ? 8 : 7;  // LDS-DMA instructions of issue()
   // Row scales of stages s .. s + 3 (s a multiple of 4) into the two buffers in
   // turn.  (Behind the row's end come others' or zeros, not used.)
-  int put_rs = 0, get_rs = 0;
+  int put_rs = 0, get_rs = 1;
   auto issue_row_scales = [&](int s) {
     if (g == 0) lds_dma16(rAS, voffAS, 4u * s, lds + kRowScales + put_rs * (kBM * 512) + wave * 512);
     put_rs ^= 1;
   };
 
-  static_assert(kStages >= kAhead + 1, "a place for the stage being read and those ahead");
+  static_assert(kStages == 3, "a place for the stage being read and two ahead");
   const int e0 = expert_of(groups, a.El, it / ntn * kBM);
   Item cur = place(e0, it - groups[e0] / kBM * ntn);
   // (slots and gates are fetched an item ahead, and taken behind a wait that covers
@@ -745,16 +747,40 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
   Item next = after(cur, it + slots < end);
   if (use_slots) load_slots(next, slot);
   issue_row_scales(0);
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    if (i == nK) aim(cur, slot, false);
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) issue(i);
-  // The next stage is there for every wave, and what was asked for before the
-  // newest stage.
-  auto arrive = [&] {
-    stage_barrier<kIssued*(kAhead - 1)>();
-    asm volatile("" : "+v"(slot[0]), "+v"(slot[1]), "+v"(gw[0]), "+v"(gw[1]), "+v"(gn[0]), "+v"(gn[1]));
-  };
-  arrive();
+    for (int j = 0; j < kIssued; ++j) issue_one(i, j);
+  }
   int get = 0;
+  uint32_t rs[2];  // row scales of the stage
+  uint32_t ws[2][4];
+  u32x4_t av[2][2], wv[2][4];
+  auto read = [&](int q) {
+    const unsigned char* st = lds + get * kStage;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) av[q][m] = *reinterpret_cast<const u32x4_t*>(st + read_a[q] + m * kBlock);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const int b = kGateUp ? (n >> 1) * 4 + (n & 1) : n;  // of the wave's weight blocks
+      wv[q][n] = *reinterpret_cast<const u32x4_t*>(st + read_w[q] + b * kBlock);
+      ws[q][n] = st[read_ws + q * 512 + b * 32];
+    }
+  };
+  // The next stage is there for every wave, with all that was asked for before the
+  // newest stage, and every wave has read the present one; its first operands.
+  auto arrive = [&](int s) {
+    stage_barrier<kIssued>();
+    asm volatile("" : "+v"(slot[0]), "+v"(slot[1]), "+v"(gw[0]), "+v"(gw[1]), "+v"(gn[0]), "+v"(gn[1]));
+    if (s % 4 == 0) get_rs ^= 1;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+      rs[m] = *reinterpret_cast<const uint32_t*>(lds + kRowScales + get_rs * (kBM * 512) + ((wm * 2 + m) * 32 + r) * 16 + 4 * (s % 4));
+    read(0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  arrive(0);
   for (;;) {
     const bool more = it + slots < end;
     f32x16_t acc[2][4];
@@ -762,65 +788,44 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int n = 0; n < 4; ++n) acc[m][n] = f32x16_t{};
-    u32x4_t rs[2];  // row scales of this stage (word 0) and the next ones
-    auto multiply = [&](int s) {
-      const unsigned char* st = lds + get * kStage;
-      get = get == kStages - 1 ? 0 : get + 1;
-      if (s % 4 == 0) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-          rs[m] = *reinterpret_cast<const u32x4_t*>(lds + kRowScales + get_rs * (kBM * 512) + ((wm * 2 + m) * 32 + r) * 16);
-        get_rs ^= 1;
-      }
-      // both steps' operands are on their way before the first product
-      uint32_t ws[2][4];
-      u32x4_t av[2][2], wv[2][4];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m) av[q][m] = *reinterpret_cast<const u32x4_t*>(st + read_a[q] + m * kBlock);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int b = kGateUp ? (n >> 1) * 4 + (n & 1) : n;  // of the wave's weight blocks
-          wv[q][n] = *reinterpret_cast<const u32x4_t*>(st + read_w[q] + b * kBlock);
-          ws[q][n] = st[read_ws + q * 512 + b * 32];
+    Item third = next;
+    for (int s = 0; s < nS; ++s) {
+      // every wave has read the stage before this one, whose place the new one takes,
+      // and the row scales before the present ones
+      int at = s + 2;
+      if (at >= nS) at -= nS;
+      if (at == 0 || at == nK) {  // the next item's first stages follow (or zeros)
+        aim(next, slot, more && at == 0);
+        if (at == 0) {
+          load_gates(gn);
+          third = after(next, it + 2 * slots < end);
+          if (use_slots) load_slots(third, slot);
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
+      if (at == 0 || (s % 4 == 1 && s + 3 < nK)) issue_row_scales(at == 0 ? 0 : s + 3);
       uint32_t as[2];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        as[m] = rs[m][0] >> (8 * g);
-        rs[m] = u32x4_t{rs[m][1], rs[m][2], rs[m][3], 0};
+      for (int m = 0; m < 2; ++m) as[m] = s < nK ? rs[m] >> (8 * g) : 0;
+      read(1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int n = i >> 1, m = i & 1;
+        acc[m][n] = mfma_mx<0>(wv[0][n], av[0][m], acc[m][n], ws[0][n], as[m]);
+        if (i < kIssued) {
+          issue_one(at, i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) acc[m][n] = mfma_mx<0>(wv[0][n], av[0][m], acc[m][n], ws[0][n], as[m]);
+      __builtin_amdgcn_sched_barrier(0);
+      get = get == kStages - 1 ? 0 : get + 1;
+      arrive(s + 1 == nS ? 0 : s + 1);
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int m = 0; m < 2; ++m) acc[m][n] = mfma_mx<2>(wv[1][n], av[1][m], acc[m][n], ws[1][n], as[m]);
-    };
-    Item third = next;
-    for (int s = 0; s < nK; ++s) {
-      // Every wave has read the stage before this one, whose place the new one
-      // takes, and the row scales before the present ones.  (Stage 0 was waited for
-      // before the last item's results were stored.)
-      if (s > 0) stage_barrier<kIssued*(kAhead - 1)>();
-      int at = s + kAhead;
-      if (at == nK) {  // the next item's first stages follow
-        aim(next, slot, more);
-        load_gates(gn);
-        third = after(next, it + 2 * slots < end);
-        if (use_slots) load_slots(third, slot);
-      }
-      if (at >= nK) at -= nK;
-      if (at == 0 || (s % 4 == 1 && s + 3 < nK)) issue_row_scales(at == 0 ? 0 : s + 3);
-      issue(at);
-      multiply(s);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    arrive();  // the next item's first stage, before the stores that follow are counted
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const int grp = cur.g0 + wm * 2 + m, p0 = cur.row0 + (wm * 2 + m) * 32;
@@ -888,14 +893,11 @@ hipError_t launch_products(const Shape& s, const MxArgs& a, hipStream_t st) {
     hipLaunchKernelGGL(mx_stream_kernel<kGateUp>, dim3(grid), dim3(256), 0, st, a);
     return hipGetLastError();
   }
-  auto launch = [&](auto kern, std::atomic<uint64_t>& done) {
-    const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(kern), tile_lds(kMaxExperts), done);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3(512), dim3(256), tile_lds(s.El), st, a);
-    return hipGetLastError();
-  };
-  static std::atomic<uint64_t> done_one{0}, done_two{0};
-  return a.K == 128 ? launch(mx_tile_kernel<kGateUp, 1>, done_one) : launch(mx_tile_kernel<kGateUp, 2>, done_two);
+  static std::atomic<uint64_t> done{0};
+  const hipError_t e = set_lds_attr(reinterpret_cast<const void*>(mx_tile_kernel<kGateUp>), tile_lds(kMaxExperts), done);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(mx_tile_kernel<kGateUp>, dim3(512), dim3(256), tile_lds(s.El), st, a);
+  return hipGetLastError();
 }
 
 template <bool kQuantize>
