@@ -29,6 +29,14 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return uint32_t(f32_to_bf16(lo)) | (uint32_t(f32_to_bf16(hi)) << 16);
 }
 
+// The same bits by one instruction for the pair (taken apart, a conversion each,
+// a shift and an or).
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 // Four OCP E4M3FN codes (one dword) -> four bfloat16 (two dwords), exactly:
 // every finite E4M3FN value has at most 4 significant bits and an exponent
 // inside bfloat16's normal range, so the conversion with unit scale rounds

@@ -361,10 +361,10 @@ __device__ __forceinline__ void store_y(const MxArgs& a, const f32x16_t& v, int 
   float h[16];
 #pragma unroll
   for (int q = 0; q < 16; ++q) h[q] = v[q] * gw;
-  *reinterpret_cast<u32x4_t*>(o) = u32x4_t{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]),
-                                           pack_bf16x2(h[4], h[5]), pack_bf16x2(h[6], h[7])};
-  *reinterpret_cast<u32x4_t*>(o + 8) = u32x4_t{pack_bf16x2(h[8], h[9]), pack_bf16x2(h[10], h[11]),
-                                               pack_bf16x2(h[12], h[13]), pack_bf16x2(h[14], h[15])};
+  *reinterpret_cast<u32x4_t*>(o) = u32x4_t{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3]),
+                                           bf16_pair(h[4], h[5]), bf16_pair(h[6], h[7])};
+  *reinterpret_cast<u32x4_t*>(o + 8) = u32x4_t{bf16_pair(h[8], h[9]), bf16_pair(h[10], h[11]),
+                                               bf16_pair(h[12], h[13]), bf16_pair(h[14], h[15])};
 }
 
 // -- few rows per expert: weights streamed by each wave into registers.
@@ -851,9 +851,9 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
             unsigned char* row = tmp + (r >> 4) * (4 * kBlock) + (r & 15) * 128;
             const int c = b * 4 + g * 2;
             *reinterpret_cast<u32x4_t*>(row + ((c ^ (r & 7)) << 4)) =
-                u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+                u32x4_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
             *reinterpret_cast<u32x4_t*>(row + (((c + 1) ^ (r & 7)) << 4)) =
-                u32x4_t{pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15])};
+                u32x4_t{bf16_pair(v[8], v[9]), bf16_pair(v[10], v[11]), bf16_pair(v[12], v[13]), bf16_pair(v[14], v[15])};
           }
           const int col = cur.nt * 256 + wn * 128 + n * 32 + (l & 7) * 8;
 #pragma unroll

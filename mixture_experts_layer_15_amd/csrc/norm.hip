@@ -56,8 +56,8 @@ template <bool kBF16>
 __device__ __forceinline__ Chunk<kBF16> pack8(const float* f) {
   Chunk<kBF16> c;
   if constexpr (kBF16) {
-    c.v[0] = u32x4_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                     pack_bf16x2(f[6], f[7])};
+    c.v[0] = u32x4_t{bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
+                     bf16_pair(f[6], f[7])};
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q) c.v[q >> 2][q & 3] = __float_as_uint(f[q]);
