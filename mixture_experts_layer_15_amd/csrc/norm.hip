@@ -334,6 +334,8 @@ struct CombineNormArgs {
   float eps, res_scale;
 };
 
+// (8192 x 2048, k = 8, 369 MB: 68 us, 5.4 TB/s; with stores into the cache, where
+// they displace the expert rows still to be read, 73.)
 template <bool kBF16, int L, int V>
 __global__ __launch_bounds__(L) void combine_norm_kernel(CombineNormArgs a) {
   __shared__ float lds[2 * (L / kWave)];
@@ -386,7 +388,7 @@ __global__ __launch_bounds__(L) void combine_norm_kernel(CombineNormArgs a) {
 #pragma unroll
       for (int q = 0; q < 8; ++q) o[q] = fmaf(a.res_scale, at8(h[j], q), o[q]);
       h[j] = pack8<kBF16>(o);
-      store8(a.out, row + c, h[j]);
+      store8<kBF16, true>(a.out, row + c, h[j]);
 #pragma unroll
       for (int q = 0; q < 8; ++q) s[0] = fmaf(at8(h[j], q), at8(h[j], q), s[0]);
     }
@@ -403,7 +405,7 @@ __global__ __launch_bounds__(L) void combine_norm_kernel(CombineNormArgs a) {
       vec8(a.next_weight, c, w);
 #pragma unroll
       for (int q = 0; q < 8; ++q) o[q] = at8(h[j], q) * rn * w[q];
-      store8(a.next_x, row + c, pack8<kBF16>(o));
+      store8<kBF16, true>(a.next_x, row + c, pack8<kBF16>(o));
     }
   }
 }
