@@ -1,0 +1,246 @@
+"""The operators of a block together, as a model runs them: norm, router,
+dispatch, 4-bit conversion and experts, combine with the next block's norm (or
+the layer for a few tokens between two norms), eagerly on a stream of their
+own and replayed from a captured graph; and the backward pass of the norms
+around the router's."""
+import pytest
+import torch
+
+import few_reference as FR
+import mx_reference as MR
+import norm_reference as NR
+from mixture_experts_layer_15_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+EPS = 1e-5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.load_library()
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _within(got, want, err, what):
+    assert torch.isfinite(got).all(), what
+    over = (got.double() - want).abs() - err
+    assert float(over.max()) <= 0, (what, float(over.max()))
+
+
+def _mxfp4(El, F, d, g):
+    out = {}
+    for n, rows, K in (("gate", F, d), ("up", F, d), ("down", d, F)):
+        w = torch.randn(El, rows, K, generator=g, device=DEV) / K ** 0.5
+        codes = torch.empty(El, rows, K // 2, dtype=torch.uint8, device=DEV)
+        scales = torch.empty(El, K // 32, rows, dtype=torch.uint8, device=DEV)
+        B.moe_mx_quantize(w, codes, scales, B.MOE_MX_SCALES_BLOCK)
+        out["w_" + n], out["s_" + n] = codes, scales
+    return out
+
+
+class Blocks:
+    """Two blocks: x = norm(h); experts of x; h <- h + gate * norm(combined), whose norm is the next x."""
+
+    def __init__(self, T, d, E, k, F, e0, El, seed):
+        g = _gen(seed)
+        self.shape = (T, d, E, k, F, e0, El)
+        self.p = B.problem(T, d, E, k, F, e0, El, "bf16", "mxfp4", True)
+        bf = torch.bfloat16
+        self.h0 = torch.randn(T, d, generator=g, device=DEV).to(bf)
+        e = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device=DEV)  # noqa: E731
+        self.layers = []
+        for _ in range(2):
+            raw = _mxfp4(El, F, d, g)
+            kept = dict(raw)
+            for which, n in ((0, "gate"), (0, "up"), (1, "down")):
+                kept["w_" + n] = torch.empty_like(raw["w_" + n])
+                B.moe_pack_weights(self.p, which, raw["w_" + n], kept["w_" + n])
+            self.layers.append(dict(
+                raw=raw, kept=kept, before=1 + 0.1 * torch.randn(d, generator=g, device=DEV),
+                after=1 + 0.1 * torch.randn(d, generator=g, device=DEV), channel=torch.rand(d, generator=g, device=DEV),
+                w_router=(torch.randn(d, E, generator=g, device=DEV) / d ** 0.5).to(bf),
+                x=e(T, d, t=bf), logits=e(T, E), idx=e(T, k, t=torch.int32), gates=e(T, k), counts=e(El, t=torch.int32),
+                offsets=e(El + 1, t=torch.int32), order=e(T * k, t=torch.int32), pos=e(T, k, t=torch.int32),
+                codes=e(T, d // 2, t=torch.uint8), scales=e(T, d // 32, t=torch.uint8), y=e(T * k, d, t=bf), out=e(T, d, t=bf)))
+        self.ws = {c: B.workspace(self.p, c, DEV) for c in (B.MOE_CALL_ROUTE, B.MOE_CALL_PERMUTE, B.MOE_CALL_EXPERT_FFN_MX,
+                                                           B.MOE_CALL_FORWARD_FEW)}
+
+    def tensors(self):
+        return [L[n] for L in self.layers for n in ("x", "logits", "idx", "gates", "offsets", "codes", "scales", "out")]
+
+    def run(self, few, stream=None):
+        p, h = self.p, self.h0
+        B.moe_norm(p, h, self.layers[0]["before"], EPS, self.layers[0]["x"], stream=stream)
+        for i, L in enumerate(self.layers):
+            after = self.layers[i + 1] if i + 1 < len(self.layers) else None
+            kept = L["kept"]
+            if few:
+                B.moe_forward_few(p, x=L["x"], w_router=L["w_router"], w_gate=kept["w_gate"], w_up=kept["w_up"], w_down=kept["w_down"],
+                                  s_gate=kept["s_gate"], s_up=kept["s_up"], s_down=kept["s_down"], logits=L["logits"], topk_idx=L["idx"],
+                                  topk_w=L["gates"], out=L["y"][:h.shape[0]], ws=self.ws[B.MOE_CALL_FORWARD_FEW], stream=stream)
+                rows = dict(y=L["y"][:h.shape[0]])     # row t is token t's
+                q = B.problem(p.T, p.d, p.E, 1, p.F, act="bf16", weight="mxfp4")
+            else:
+                B.moe_route(p, L["x"], L["w_router"], None, L["logits"], L["idx"], L["gates"], self.ws[B.MOE_CALL_ROUTE], stream=stream)
+                B.moe_permute(p, L["idx"], L["counts"], L["offsets"], L["order"], L["pos"], self.ws[B.MOE_CALL_PERMUTE], stream=stream)
+                B.moe_mx_quantize(L["x"], L["codes"], L["scales"], stream=stream)
+                B.moe_expert_ffn_mx(p, L["codes"], L["scales"], L["order"], L["offsets"], kept["w_gate"], kept["w_up"], kept["w_down"],
+                                    kept["s_gate"], kept["s_up"], kept["s_down"], None, L["y"], self.ws[B.MOE_CALL_EXPERT_FFN_MX],
+                                    stream=stream)
+                rows = dict(y=L["y"], slot_pos=L["pos"], topk_w=L["gates"])
+                q = p
+            following = {} if after is None else dict(next_weight=after["before"], next_x=after["x"])
+            B.moe_combine_norm(q, h=h, weight=L["after"], eps=EPS, gate=L["channel"], out=L["out"], stream=stream, **rows, **following)
+            h = L["out"]
+
+    def check(self, few):
+        T, d, E, k, F, e0, El = self.shape
+        h = self.h0
+        want, err, _, _ = NR.norm(h.double(), self.layers[0]["before"].double(), EPS)
+        _within(self.layers[0]["x"], want, NR.stored(want, err, torch.bfloat16), "first norm")
+        for i, L in enumerate(self.layers):
+            x, raw = L["x"], L["raw"]
+            want, err = FR.logits(x, L["w_router"], None)
+            if few:
+                _within(L["logits"], want, err, "logits")
+            idx, gates = FR.selection(L["logits"], k)
+            assert torch.equal(L["idx"], idx)
+            assert torch.allclose(L["gates"].double(), gates, rtol=(k + 16) * 2.0 ** -23, atol=1e-38)
+            mats = [raw["w_gate"], raw["w_up"], raw["w_down"]]
+            scales = [raw["s_gate"], raw["s_up"], raw["s_down"]]
+            if few:
+                want, err = FR.layer(x, idx, L["gates"], mats, scales, "mxfp4", torch.bfloat16, e0, El)
+                _within(L["y"][:T], want, err, "layer")
+                y, pos, w = L["y"][:T].double(), torch.arange(T, device=DEV)[:, None], None
+            else:
+                code, byte = MR.quantize(x)
+                assert torch.equal(L["codes"], MR.pack(code)) and torch.equal(L["scales"], byte)
+                rows, off = MR.values(L["codes"], L["scales"]), L["offsets"].tolist()
+                for j in range(0, El, max(1, El // 6)):
+                    slot = L["order"][off[j]:off[j + 1]].long()
+                    if len(slot) == 0:
+                        continue
+                    assert (idx.flatten()[slot] == e0 + j).all()
+                    v, err = MR.expert(rows[slot // k], *(MR.values(m[j], s[j].t()) for m, s in zip(mats, scales)))
+                    _within(L["y"][off[j]:off[j + 1]], v, err + (v.abs() + err) * (2.0 ** -8 + 2 * MR.U), "expert rows")
+                y, w = L["y"].double(), L["gates"].double()
+                pos = torch.where((idx >= e0) & (idx < e0 + El), L["pos"].long(), -1)
+            want, err, _, _ = NR.after(y, pos, w, h.double(), L["after"].double(), L["channel"].double(), EPS, 1.0)
+            _within(L["out"], want, NR.stored(want, err, torch.bfloat16), "combined")
+            h = L["out"]
+            if i + 1 < len(self.layers):
+                after = self.layers[i + 1]
+                want, err, _, _ = NR.norm(h.double(), after["before"].double(), EPS)
+                _within(after["x"], want, NR.stored(want, err, torch.bfloat16), "next norm")
+
+
+@pytest.mark.parametrize("few,shape", [(False, (37, 384, 12, 3, 256, 0, 12)), (False, (701, 640, 10, 4, 384, 2, 7)),
+                                       (False, (1500, 256, 4, 2, 128, 0, 4)),
+                                       (True, (1, 384, 12, 3, 256, 0, 12)), (True, (13, 640, 20, 4, 384, 0, 20)), (True, (5, 256, 16, 2, 128, 4, 9))])
+def test_two_blocks(few, shape):
+    b = Blocks(*shape, seed=shape[0])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    b.run(few, stream=side)
+    side.synchronize()
+    b.check(few)
+    first = [t.clone() for t in b.tensors()]
+    b.run(few)
+    torch.cuda.synchronize()
+    for t, u in zip(b.tensors(), first):
+        if not (few and t.dtype == torch.uint8):
+            assert torch.equal(t.view(torch.uint8), u.view(torch.uint8))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.run(few)
+    g = _gen(5)
+    for _ in range(3):
+        b.h0.copy_(torch.randn(b.h0.shape, generator=g, device=DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        b.check(few)
+
+
+def test_backward_around_the_router():
+    """out = h + channel * norm(sum of gates(norm(h)) y) in float32: dh, dy and the vectors' gradients against float64
+    differentiation of the whole (expert rows given).  A float32 sum of n terms is off by n U of their magnitudes at the very
+    worst; the longest here are 384 (a row) and 53 (tokens), whose terms cancel to no less than a twentieth of their
+    magnitudes: 384 * 20 U < 5e-4 of a gradient's norm through each of the three sums that follow each other (row, softmax
+    of the gates, row)."""
+    T, d, E, k = 53, 384, 24, 3
+    g = _gen(11)
+    p = B.problem(T, d, E, k, 128, 0, E, "f32", "f32")
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    h, y, dout = r(T, d), r(T * k, d), r(T, d)
+    wb, wa, ch, wr = 1 + 0.2 * r(d), 1 + 0.2 * r(d), r(d), r(d, E) / d ** 0.5
+    e = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device=DEV)  # noqa: E731
+    x, rs, logits, idx, gates = e(T, d), e(T), e(T, E), e(T, k, t=torch.int32), e(T, k)
+    counts, offsets, order, pos = e(E, t=torch.int32), e(E + 1, t=torch.int32), e(T * k, t=torch.int32), e(T, k, t=torch.int32)
+    out, ra = e(T, d), e(T)
+    dy, dg, dwa, dch, dx, dwr, dh, dwb = e(T * k, d), e(T, k), e(d), e(d), e(T, d), e(d, E), e(T, d), e(d)
+    ws = {c: B.workspace(p, c, DEV) for c in (B.MOE_CALL_ROUTE, B.MOE_CALL_PERMUTE, B.MOE_CALL_COMBINE_NORM_BACKWARD,
+                                             B.MOE_CALL_ROUTE_BACKWARD, B.MOE_CALL_NORM_BACKWARD)}
+
+    def step():
+        B.moe_norm(p, h, wb, EPS, x, rs)
+        B.moe_route(p, x, wr, None, logits, idx, gates, ws[B.MOE_CALL_ROUTE])
+        B.moe_permute(p, idx, counts, offsets, order, pos, ws[B.MOE_CALL_PERMUTE])
+        B.moe_combine_norm(p, y=y, h=h, weight=wa, eps=EPS, out=out, slot_pos=pos, topk_w=gates, gate=ch, rstd=ra)
+        B.moe_combine_norm_backward(p, dout=dout, y=y, weight=wa, rstd=ra, slot_pos=pos, topk_w=gates, gate=ch, dy=dy, dtopk_w=dg,
+                                    dweight=dwa, dgate=dch, ws=ws[B.MOE_CALL_COMBINE_NORM_BACKWARD])
+        B.moe_route_backward(p, x=x, w_router=wr, topk_idx=idx, topk_w=gates, dtopk_w=dg, dx=dx, dw_router=dwr,
+                             ws=ws[B.MOE_CALL_ROUTE_BACKWARD])
+        B.moe_norm_backward(p, dx=dx, h=h, weight=wb, rstd=rs, dout=dout, dh=dh, dweight=dwb, ws=ws[B.MOE_CALL_NORM_BACKWARD])
+
+    def check():
+        leaf = [t.double().requires_grad_() for t in (h, y, wb, wa, ch, wr)]
+        H, Y, WB, WA, CH, WR = leaf
+        X = H * NR.rstd(H, EPS)[:, None] * WB
+        G = torch.softmax(torch.gather(X @ WR, 1, idx.long()), dim=1)
+        C = (Y[pos.long().flatten()].view(T, k, d) * G[..., None]).sum(dim=1)
+        O = H + CH * (C * NR.rstd(C, EPS)[:, None] * WA)
+        (O * dout.double()).sum().backward()
+        assert float((out.double() - O.detach()).norm() / O.detach().norm()) < 5e-4
+        for name, t, got in zip(("h", "y", "before", "after", "channel", "router"), leaf, (dh, dy, dwb, dwa, dch, dwr)):
+            rel = float((got.double() - t.grad).norm() / t.grad.norm())
+            assert rel < 3 * 5e-4, (name, rel)
+
+    step()
+    check()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        h.copy_(r(T, d))
+        y.copy_(r(T * k, d))
+        dout.copy_(r(T, d))
+        graph.replay()
+        torch.cuda.synchronize()
+        check()
+
+
+def test_few_tokens_of_more_column_groups_than_workgroups():
+    """d / 64 = 544 groups of output columns, 512 workgroups: a second turn for some of them."""
+    T, d, E, k, F = 3, 34816, 3, 2, 128
+    g = _gen(2)
+    p = B.problem(T, d, E, k, F, 0, E, "bf16", "bf16")
+    bf = torch.bfloat16
+    x = torch.randn(T, d, generator=g, device=DEV).to(bf)
+    wr = (torch.randn(d, E, generator=g, device=DEV) / d ** 0.5).to(bf)
+    mats = [(torch.randn(E, r, K, generator=g, device=DEV) / K ** 0.5).to(bf) for r, K in ((F, d), (F, d), (d, F))]
+    out, logits = torch.full((T, d), float("nan"), dtype=bf, device=DEV), torch.empty(T, E, device=DEV)
+    idx, gates = torch.empty(T, k, dtype=torch.int32, device=DEV), torch.empty(T, k, device=DEV)
+    ws = B.workspace(p, B.MOE_CALL_FORWARD_FEW, DEV).fill_(0xFF)
+    for _ in range(2):
+        B.moe_forward_few(p, x=x, w_router=wr, w_gate=mats[0], w_up=mats[1], w_down=mats[2], logits=logits, topk_idx=idx, topk_w=gates,
+                          out=out, ws=ws)
+        want, err = FR.layer(x, idx, gates, mats, [None] * 3, "bf16", bf, 0, E)
+        _within(out, want, err, "layer")
