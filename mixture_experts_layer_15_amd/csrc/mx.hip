@@ -813,10 +813,13 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
       for (int n = 0; n < 4; ++n) acc[m][n] = f32x16_t{};
     Item third = next;
     for (int s = 0; s < nS; ++s) {
-      // every wave has read the stage before this one, whose place the new one takes,
-      // and the row scales before the present ones
+      // Every wave has read the stage before this one, whose place the new one takes.
       int at = s + 2;
       if (at >= nS) at -= nS;
+      // Row scales four stages at a time (the next item's in the last stage), so late
+      // that every wave has read the last of those whose place they take: a stage
+      // back or more.
+      if (at == 1 || (s % 4 == 1 && s + 3 < nK)) issue_row_scales(at == 1 ? 0 : s + 3);
       if (at == 0 || at == nK) {  // the next item's first stages follow (or zeros)
         aim(next, slot, more && at == 0);
         if (at == 0) {
@@ -825,7 +828,6 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
           if (use_slots) load_slots(third, slot);
         }
       }
-      if (at == 0 || (s % 4 == 1 && s + 3 < nK)) issue_row_scales(at == 0 ? 0 : s + 3);
       uint32_t as[2];
 #pragma unroll
       for (int m = 0; m < 2; ++m) as[m] = s < nK ? rs[m] >> (8 * g) : 0;
