@@ -420,6 +420,10 @@ struct Format {
   // error as the rounding of the output): the remainders are columns 16 .. 31
   // of the operand, so they cost no load and no product of their own.
   static constexpr bool kPlanes = kDown && kFmt != kF32;
+  // In gate/up those columns are idle: their lanes load every second piece for
+  // the lanes 16 before them, which get it by a swap of 16-lane rows.
+  static constexpr bool kPairs = !kDown && kPieces > 1;
+  static constexpr int kXLoads = kPairs ? kPieces / 2 : kPieces;
   // The waves take turns of kRun loads along K: FP8 a scale block, of a
   // row-major matrix whole lines (MXFP4: half of one, as K may be 128).
   // Blocked, one load: adjacent waves on adjacent kilobytes stream 50 MB in 8.8
@@ -428,7 +432,7 @@ struct Format {
   // loads a wave keeps in flight per weight block (two of four KB each do:
   // 6.6 TB/s, as eight or twelve)
   static constexpr int kD = kFmt == kFP4 ? 4 : kFmt == kFP8 && !kDown ? 4 : 8;
-  static constexpr int kLoads = 2 + kPieces + (kFmt == kFP4 ? 2 : 0);  // of a step
+  static constexpr int kLoads = 2 + kXLoads + (kFmt == kFP4 ? 2 : 0);  // of a step
   static_assert(kD % kRun == 0 && kD * kLoads < 64, "whole runs in the ring, a countable number of loads");
 };
 
@@ -452,7 +456,7 @@ struct Stream {
   const uint32_t row_bytes, mat, smat, voff, svoff;
   const void* xbase;
   uint32_t x_bytes;
-  u32x4_t wb[C::kD][2], xb[C::kD][C::kPieces];
+  u32x4_t wb[C::kD][2], xb[C::kD][C::kXLoads];
   uint32_t sb[C::kD][2];
   f32x16_t acc[2], part[2];
 
@@ -524,8 +528,23 @@ struct Stream {
     const __amdgpu_buffer_rsrc_t rx = rsrc(xbase, within(j) && s.w_bytes ? x_bytes : 0);
     const uint32_t at = (uint32_t)load_of(j) * (2 * C::kV) * (C::kAct32 ? 4u : 2u);
 #pragma unroll
-    for (int q = 0; q < C::kPieces; ++q)
-      xb[e][q] = __builtin_amdgcn_raw_buffer_load_b128(rx, s.x + 16u * q, at, kDown ? kDevice : 0);
+    for (int q = 0; q < C::kXLoads; ++q)
+      xb[e][q] = __builtin_amdgcn_raw_buffer_load_b128(rx, s.x + 16u * q * (C::kPairs ? 2 : 1), at, kDown ? kDevice : 0);
+  }
+
+  // Piece q of step e's activations (in columns that nobody reads: any other).
+  __device__ __forceinline__ bf16x8_t activations(int e, int q) const {
+    if constexpr (C::kPairs) {
+      u32x4_t v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = xb[e][q / 2][i];
+        v[i] = q % 2 ? __builtin_amdgcn_permlane16_swap(x, x, false, false)[1] : x;
+      }
+      return __builtin_bit_cast(bf16x8_t, v);
+    } else {
+      return __builtin_bit_cast(bf16x8_t, xb[e][q]);
+    }
   }
 
   // Step j's products; q0, q1: the FP8 scales of the blocks' rows.
@@ -550,7 +569,7 @@ struct Stream {
           } else {
             w = e2m1x8_to_bf16x8(wb[e][b][q], sc);
           }
-          sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, __builtin_bit_cast(bf16x8_t, xb[e][q]), sum, 0, 0, 0);
+          sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, activations(e, q), sum, 0, 0, 0);
         }
       }
     }
@@ -643,7 +662,9 @@ __device__ __forceinline__ int up_items(const FewArgs& a, const Plan& p, Results
     }
     const int e = __builtin_amdgcn_readfirstlane(p.expert[in]);
     const uint32_t mask = p.tokens[e];
-    Source s = st.source(e, fbn, fbn, mask >> st.r & 1 ? st.r * xrow : kNowhere);
+    // (a pair's second piece: lanes 16 on)
+    const int t = C::kPairs ? st.r % kMaxTokens : st.r;
+    Source s = st.source(e, fbn, fbn, mask >> t & 1 ? t * xrow + (st.r - t) : kNowhere);
     --left;
     if (++fbn == nf) {
       fbn = 0;
