@@ -302,9 +302,11 @@ moe_status_t moe_forward_noalloc(const moe_problem_t* p, const moe_forward_args_
  * formats, layouts and arguments as moe_forward, with these differences:
  *  - counts, offsets, sorted_slot, slot_pos and events must be NULL: no
  *    dispatch order is formed (MOE_ERR_INVALID_ARGUMENT).
- *  - the experts' rows are not rounded before they are added, and sums run in
- *    another order, so results agree within rounding, not bit for bit (the
- *    selection is taken on the logits this call writes).  FP8 block scales
+ *  - the gates are applied to h, which is kept as a value and its remainder in
+ *    the activation format (float32 as it is), the experts' rows are not rounded
+ *    before they are added, and sums run in another order, so results agree
+ *    within rounding, not bit for bit (the selection is taken on the logits
+ *    this call writes).  FP8 block scales
  *    are applied to the sum of each 128-deep block: they need not lie within
  *    2^32 of each other.
  *  - T above MOE_FEW_MAX_TOKENS or T*k above MOE_FEW_MAX_SLOTS is

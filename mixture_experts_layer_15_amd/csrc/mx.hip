@@ -394,7 +394,11 @@ __device__ __forceinline__ void store_y(const MxArgs& a, const f32x16_t& v, int 
 // An item is a group of 32 rows and kNB weight blocks of 32 rows (gate/up: two
 // gate blocks and the up blocks of the same features); the four waves of a
 // workgroup take a quarter of K each and add their results through LDS, so
-// that a handful of experts still fills the chip.  A wave keeps kD steps of
+// that a handful of experts still fills the chip.  64 tokens of the Qwen3 shape:
+// gate/up 38.5 us for 214 MB (5.6 TB/s), down 24.8 us for 107 MB, of which 6 us
+// are the joining of the quarters (three steps of K each) at the start and end of
+// the chip's four turns of items.  Not bound by loads in flight: two, three or
+// four steps a wave take the same, six more (43 and 32 us).  A wave keeps kD steps of
 // 64 K values in flight; nothing passes LDS before the results.
 constexpr int kNB = 4;
 constexpr int kD = 3;
@@ -418,8 +422,8 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxArgs a) {
   const uint32_t unit = a.blocked ? 1024u : 32u;
   const uint32_t voffW = a.blocked ? 16u * l : (uint32_t)feat(r) * wrow + 16u * g;
   // Scales of a step: a lane loads four columns of a K block (down: 128 columns in
-  // a load, gate/up: 64 a matrix) and each block's are fetched from the lane that
-  // holds them; a byte a lane and block was a fifth of the time of the loads.
+  // a load, gate/up: 64 a matrix), and each block's are fetched from the lane that
+  // holds them.
   const uint32_t voffS = kGateUp ? (uint32_t)((l >> 4) & 1) * a.Nout + 4u * (l & 15)
                                  : (uint32_t)g * a.Nout + 4u * r;
   const int from = 4 * (g * (8 * H) + feat(r) / 4), shift = 8 * (r & 3);
@@ -565,6 +569,12 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxArgs a) {
 // not bytes: 32 bytes of 32 rows made it the bottleneck).  The rows' scales come
 // 16 bytes (four stages) at a time, for the same reason, and are read into
 // registers.
+// 8192 tokens of the Qwen3 shape: gate/up 145 us (2.84 PFLOP/s), down 111 us (1.86,
+// beside 268 MB of results).  The matrix instructions alone, nothing else running,
+// reach 6.5 PFLOP/s here (the clock falls under them); a wave's stage takes 1800
+// cycles or more, 1024 of them the matrix cores', an eighth of the tiles' rows
+// are padding, and the results' conversion takes 17 us of gate/up and, with its
+// stores, 40 of down.
 constexpr int kBM = 4;        // groups of 32 rows of a tile
 constexpr int kStages = 3;
 constexpr int kBlock = 2048;  // of 32 rows
@@ -902,8 +912,15 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
   __builtin_amdgcn_s_waitcnt((0 & 15) | (7 << 4) | (15 << 8));  // no LDS-DMA outlives the workgroup
 }
 
-// Which kernel takes a problem.
-bool use_tiles(const Shape& s) { return s.S >= 64LL * s.El; }
+// Which kernel takes a problem.  Streaming reads an expert's weights once per 32
+// rows, and its items are short: it is ahead with less than 24 rows an expert, and
+// with more as long as its gate/up items (32 rows x 64 features) do not fill the
+// 512 workgroups that are resident.  Measured, streamed / in tiles: 128 experts of
+// the Qwen3 shape with 16 rows 68 / 74 us, 24 rows 75 / 74, 32 rows 96 / 76, 64
+// rows 138 / 80; 16 experts of 2048 x 1024 with 24 rows (192 items) 21 / 32, 64
+// rows (512) 33 / 27; 2 of 1024 x 768 with 512 rows (384) 18 / 20, 1024 rows (768)
+// 24 / 21; one of 7168 x 2048 with 128 rows (128) 30 / 49, 512 rows (512) 55 / 51.
+bool use_tiles(const Shape& s) { return s.S >= 24LL * s.El && s.S * s.F >= 448LL * (32 * 64); }
 
 // Groups of 32 rows that the experts' segments can have.
 size_t max_groups(const Shape& s) {
@@ -931,6 +948,8 @@ hipError_t convert(int batch, int rows, int cols, int bf16, const void* src, voi
   ConvertArgs a{src, dst, codes, scales, rows, cols, 8, 0, 0, 0};
   a.col_tiles = (cols + kTileCols - 1) / kTileCols;
   // block-major scales in runs of 64 bytes where that leaves work for the chip
+  // (128 matrices of 768 x 2048 quantized: 82 us, in runs of 8 bytes 104; 4 of them,
+  // 384 tiles of 64 rows: equal)
   if (block_major && (long long)batch * ((rows + 63) / 64) * a.col_tiles >= 1024) a.rt = 64;
   a.row_tiles = (rows + a.rt - 1) / a.rt;
   a.tiles = (long long)batch * a.row_tiles * a.col_tiles;

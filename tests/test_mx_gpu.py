@@ -135,6 +135,8 @@ CASES = [
     (128, 128, 2, 1, 128, 0, 2, 0.0), (300, 384, 4, 2, 640, 0, 4, 0.5), (257, 640, 6, 3, 384, 1, 4, 1.0), (1001, 128, 20, 3, 128, 0, 20, 0.2),
     (513, 2048, 2, 1, 768, 0, 1, 0.0), (4099, 1152, 8, 4, 896, 0, 8, 0.1), (20000, 128, 8, 4, 128, 0, 8, 0.1), (9000, 256, 8, 8, 256, 0, 8, 0.0),
     (700, 256, 512, 100, 128, 3, 509, 0.05),
+    (2500, 384, 4, 2, 640, 0, 4, 0.5), (1700, 640, 6, 3, 384, 1, 4, 1.0), (3000, 128, 20, 3, 128, 0, 20, 0.2), (1300, 2048, 2, 1, 768, 0, 1, 0.0),
+    (1201, 1664, 64, 2, 512, 0, 64, 0.05),
 ]
 
 
@@ -177,7 +179,7 @@ def test_expert_network(T, d, E, k, F, e0, El, skew, blocked):
             assert rel < 2.0 ** -8, (j, rel)
 
 
-@pytest.mark.parametrize("T", [8, 300])
+@pytest.mark.parametrize("T", [8, 300, 2000])
 def test_wide_scales_and_nan(T):
     """Scales over the whole range that float32 sums hold, and a token with a NaN: its rows alone are NaN."""
     d, E, k, F = 256, 4, 2, 256
@@ -209,7 +211,7 @@ def test_wide_scales_and_nan(T):
 
 def test_rows_and_blocked_layouts_agree_and_captured():
     """Both layouts give the same bits; a captured graph with the conversion replays on new tokens as the eager calls do."""
-    for T in (16, 400):
+    for T in (16, 400, 1000):
         d, E, k, F = 640, 8, 4, 384
         g = _gen(T)
         p, pb = (B.problem(T, d, E, k, F, 0, E, "bf16", "mxfp4", b) for b in (False, True))
