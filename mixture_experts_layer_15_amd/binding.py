@@ -1,9 +1,9 @@
 """Thin ctypes binding of the C ABI in ``include/moe.h``.
 
 Argument marshalling: tensors become device pointers, the stream becomes the
-current HIP stream, status codes become exceptions (the router-training calls
-check their tensors too).  Every step of the
-layer runs in the HIP library; there is no fallback of any kind.  PyTorch is
+current HIP stream, status codes become exceptions (the calls for training the
+router, for the norms, for a few tokens and in 4 bits check their tensors too).
+Every step of the layer runs in the HIP library; there is no fallback of any kind.  PyTorch is
 used for device memory and streams.
 """
 from __future__ import annotations
