@@ -390,7 +390,7 @@ __device__ __forceinline__ void store_y(const MxArgs& a, const f32x16_t& v, int 
                                                bf16_pair(h[12], h[13]), bf16_pair(h[14], h[15])};
 }
 
-// -- few rows per expert: weights streamed by each wave into registers.
+// -- few rows per expert, blocked weights: streamed by each wave into registers.
 // An item is a group of 32 rows and kNB weight blocks of 32 rows (gate/up: two
 // gate blocks and the up blocks of the same features); the four waves of a
 // workgroup take a quarter of K each and add their results through LDS, so
@@ -419,8 +419,6 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxArgs a) {
   const int s0 = nS * wave / 4, s1 = nS * (wave + 1) / 4;
   const uint32_t wrow = (uint32_t)a.K / 2, wmat = (uint32_t)a.Nout * wrow;
   const uint32_t smat = (uint32_t)(a.K / 32) * a.Nout;
-  const uint32_t unit = a.blocked ? 1024u : 32u;
-  const uint32_t voffW = a.blocked ? 16u * l : (uint32_t)feat(r) * wrow + 16u * g;
   // Scales of a step: a lane loads four columns of a K block (down: 128 columns in
   // a load, gate/up: 64 a matrix), and each block's are fetched from the lane that
   // holds them.
@@ -459,8 +457,8 @@ __global__ __launch_bounds__(256, 2) void mx_stream_kernel(MxArgs a) {
 #pragma unroll
     for (int n = 0; n < kNB; ++n) {
       const int fb = i.nb * H + n % H;
-      wb[d][n] = __builtin_amdgcn_raw_buffer_load_b128(n >= H ? rW1 : rW0, voffW,
-                                                       (uint32_t)fb * 32u * wrow + s * unit, 2);
+      wb[d][n] = __builtin_amdgcn_raw_buffer_load_b128(n >= H ? rW1 : rW0, 16u * l,
+                                                       (uint32_t)fb * 32u * wrow + s * 1024u, 2);
     }
     const uint32_t at = (uint32_t)(2 * s) * a.Nout + i.nb * (32u * H);
     ws[d][0] = __builtin_amdgcn_raw_buffer_load_b32(rS0, voffS, at, 0);
@@ -920,7 +918,13 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
 // rows 138 / 80; 16 experts of 2048 x 1024 with 24 rows (192 items) 21 / 32, 64
 // rows (512) 33 / 27; 2 of 1024 x 768 with 512 rows (384) 18 / 20, 1024 rows (768)
 // 24 / 21; one of 7168 x 2048 with 128 rows (128) 30 / 49, 512 rows (512) 55 / 51.
-bool use_tiles(const Shape& s) { return s.S >= 24LL * s.El && s.S * s.F >= 448LL * (32 * 64); }
+// Row-major weights always come in tiles: a lane's pieces of its row, read straight
+// into registers, are 32 bytes of each of 32 rows a load (128 experts of the Qwen3
+// shape with 4 rows 149 us, in tiles 77; 8 of 4096 x 1536 with 1 row 42 and 35; the
+// other way round only for the smallest: 2 of 1024 x 768 16 and 18).
+bool use_tiles(const Shape& s) {
+  return !s.blocked || (s.S >= 24LL * s.El && s.S * s.F >= 448LL * (32 * 64));
+}
 
 // Groups of 32 rows that the experts' segments can have.
 size_t max_groups(const Shape& s) {
