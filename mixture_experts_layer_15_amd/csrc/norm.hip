@@ -200,6 +200,8 @@ struct NormGradArgs {
 template <bool kBF16, int L, int V>
 __global__ __launch_bounds__(L) void norm_backward_kernel(NormGradArgs a) {
   __shared__ float lds[2 * (L / kWave)];
+  // (as far as the registers of 1024 threads hold two rows)
+  constexpr bool kAhead = L < 1024 || V * (kBF16 ? 1 : 2) <= 2;
   Chunk<kBF16> dx[V], h[V], dout[V];
   float r = 0.0f;
   auto load = [&](int t) {
@@ -220,10 +222,11 @@ __global__ __launch_bounds__(L) void norm_backward_kernel(NormGradArgs a) {
   for (int j = 0; j < V; ++j)
 #pragma unroll
     for (int q = 0; q < 8; ++q) acc[j][q] = 0.0f;
-  load(blockIdx.x);
+  if constexpr (kAhead) load(blockIdx.x);
   int turn = 0;
   for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
     const long long row = (long long)t * a.d;
+    if constexpr (!kAhead) load(t);
     Chunk<kBF16> cdx[V], ch[V], cdo[V];
     const float cr = r;
 #pragma unroll
@@ -232,7 +235,7 @@ __global__ __launch_bounds__(L) void norm_backward_kernel(NormGradArgs a) {
       ch[j] = h[j];
       cdo[j] = dout[j];
     }
-    if (t + (int)gridDim.x < a.T) load(t + gridDim.x);
+    if (kAhead && t + (int)gridDim.x < a.T) load(t + gridDim.x);
     float s[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
