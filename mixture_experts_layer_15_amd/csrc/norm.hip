@@ -287,11 +287,12 @@ __global__ __launch_bounds__(L) void norm_backward_kernel(NormGradArgs a) {
 
 constexpr int kBatch = 8;  // slots whose rows are in flight together
 
-// Positions and gates of slots i0 .. i0 + 7 of token t; -1: not kept.
+// Positions and gates of slots i0 .. i0 + N - 1 of token t; -1: not kept.
+template <int N>
 __device__ __forceinline__ void slots8(const int32_t* pos, const float* w, long long t, int k,
-                                       int i0, long long S, int (&p)[kBatch], float (&g)[kBatch]) {
+                                       int i0, long long S, int (&p)[N], float (&g)[N]) {
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
+  for (int b = 0; b < N; ++b) {
     const long long s = t * k + i0 + b;
     p[b] = -1;
     g[b] = 1.0f;
@@ -303,19 +304,19 @@ __device__ __forceinline__ void slots8(const int32_t* pos, const float* w, long 
   }
 }
 
-template <bool kBF16>
-__device__ __forceinline__ void rows8(const void* y, const int (&p)[kBatch], int d, int c,
-                                      Chunk<kBF16> (&raw)[kBatch]) {
+template <bool kBF16, int N>
+__device__ __forceinline__ void rows8(const void* y, const int (&p)[N], int d, int c,
+                                      Chunk<kBF16> (&raw)[N]) {
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b)
+  for (int b = 0; b < N; ++b)
     if (p[b] >= 0) raw[b] = load8<kBF16, true>(y, (long long)p[b] * d + c);
 }
 
-template <bool kBF16>
-__device__ __forceinline__ void add8(const Chunk<kBF16> (&raw)[kBatch], const int (&p)[kBatch],
-                                     const float (&g)[kBatch], float* acc) {
+template <bool kBF16, int N>
+__device__ __forceinline__ void add8(const Chunk<kBF16> (&raw)[N], const int (&p)[N],
+                                     const float (&g)[N], float* acc) {
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
+  for (int b = 0; b < N; ++b) {
     if (p[b] < 0) continue;
 #pragma unroll
     for (int q = 0; q < 8; ++q) acc[q] = fmaf(at8(raw[b], q), g[b], acc[q]);
@@ -357,14 +358,14 @@ __global__ __launch_bounds__(L) void combine_norm_kernel(CombineNormArgs a) {
   for (int i0 = 0; i0 < a.k; i0 += kBatch) {
     int p[kBatch];
     float g[kBatch];
-    slots8(a.pos, a.topk_w, t, a.k, i0, a.S, p, g);
+    slots8<kBatch>(a.pos, a.topk_w, t, a.k, i0, a.S, p, g);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * L + threadIdx.x) * 8;
       if (c < a.d) {
         Chunk<kBF16> raw[kBatch];
-        rows8<kBF16>(a.y, p, a.d, c, raw);
-        add8<kBF16>(raw, p, g, acc[j]);
+        rows8<kBF16, kBatch>(a.y, p, a.d, c, raw);
+        add8<kBF16, kBatch>(raw, p, g, acc[j]);
       }
     }
   }
@@ -430,7 +431,13 @@ struct CombineNormGradArgs {
   int T, d, k;
 };
 
-// One pass over the y rows for k <= 8 (kOne): with a chunk's rows in registers
+// Slots whose rows are in flight together in the backward pass: what 1024 threads
+// have registers for beside the row.  (1463 x 11136, k = 2: float32 355 -> 84 us,
+// bfloat16 145 -> 48; with k = 8, whose rows are then read twice, 429 -> 261 and
+// 151 -> 173.)
+constexpr int batch_of(bool bf16, int threads) { return threads < 1024 ? kBatch : bf16 ? 4 : 2; }
+
+// One pass over the y rows where the slots are a batch (kOne): with a chunk's rows in registers
 // its c is complete, so <u, y_i> and <c, y_i> are summed at once and
 //    <dc, y_i> = r (<u, y_i> - r mean(n u) <c, y_i>)
 // needs no second look at y.  More slots read y twice, the second time from a
@@ -442,8 +449,9 @@ struct CombineNormGradArgs {
 template <bool kBF16, int L, int V, bool kOne>
 __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine_norm_backward_kernel(
     CombineNormGradArgs a) {
-  constexpr int kPairs = 2 * kBatch;  // <u, y_i> and <c, y_i>
-  constexpr int kSums = kOne ? 1 + kPairs : kBatch;
+  constexpr int kB = batch_of(kBF16, L);
+  constexpr int kPairs = 2 * kB;  // <u, y_i> and <c, y_i>
+  constexpr int kSums = kOne ? 1 + kPairs : kB;
   constexpr int kW = L / kWave;
   __shared__ float lds[2 * kW * kSums];
   float acc[V][8];  // column sums over the workgroup's rows
@@ -459,9 +467,9 @@ __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine
     float s[1] = {0.0f}, e[kOne ? kPairs : 1];
 #pragma unroll
     for (int n = 0; n < (kOne ? kPairs : 1); ++n) e[n] = 0.0f;
-    int p[kBatch];
-    float g[kBatch];
-    if constexpr (kOne) slots8(a.pos, a.topk_w, t, a.k, 0, a.S, p, g);
+    int p[kB];
+    float g[kB];
+    if constexpr (kOne) slots8<kB>(a.pos, a.topk_w, t, a.k, 0, a.S, p, g);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
 #pragma unroll
@@ -469,15 +477,15 @@ __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine
       const int c = (j * L + threadIdx.x) * 8;
       if (c < a.d) {
         const Chunk<kBF16> go = load8<kBF16>(a.dout, row + c);
-        Chunk<kBF16> raw[kBatch];
+        Chunk<kBF16> raw[kB];
         if constexpr (kOne) {
-          rows8<kBF16>(a.y, p, a.d, c, raw);
-          add8<kBF16>(raw, p, g, cc[j]);
+          rows8<kBF16, kB>(a.y, p, a.d, c, raw);
+          add8<kBF16, kB>(raw, p, g, cc[j]);
         } else {
-          for (int i0 = 0; i0 < a.k; i0 += kBatch) {
-            slots8(a.pos, a.topk_w, t, a.k, i0, a.S, p, g);
-            rows8<kBF16>(a.y, p, a.d, c, raw);
-            add8<kBF16>(raw, p, g, cc[j]);
+          for (int i0 = 0; i0 < a.k; i0 += kB) {
+            slots8<kB>(a.pos, a.topk_w, t, a.k, i0, a.S, p, g);
+            rows8<kBF16, kB>(a.y, p, a.d, c, raw);
+            add8<kBF16, kB>(raw, p, g, cc[j]);
           }
         }
         float w[8], f[8];
@@ -493,7 +501,7 @@ __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine
         if constexpr (kOne) {
           if (a.dtopk_w) {
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
+            for (int b = 0; b < kB; ++b) {
               if (p[b] < 0) continue;
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
@@ -533,7 +541,7 @@ __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine
           cy += at[w * kSums + 1];
         }
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
+        for (int b = 0; b < kB; ++b)
           if ((int)threadIdx.x == b && p[b] >= 0) v = r * (uy - r * m * cy);
         a.dtopk_w[t * a.k + threadIdx.x] = v;
       }
@@ -543,21 +551,21 @@ __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine
     for (int j = 0; j < V; ++j)
 #pragma unroll
       for (int q = 0; q < 8; ++q) cc[j][q] = r * (u[j][q] - cc[j][q] * r * m);  // dc
-    for (int i0 = 0; i0 < a.k; i0 += kBatch) {
-      if constexpr (!kOne) slots8(a.pos, a.topk_w, t, a.k, i0, a.S, p, g);
-      float dot[kBatch];
+    for (int i0 = 0; i0 < a.k; i0 += kB) {
+      if constexpr (!kOne) slots8<kB>(a.pos, a.topk_w, t, a.k, i0, a.S, p, g);
+      float dot[kB];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) dot[b] = 0.0f;
+      for (int b = 0; b < kB; ++b) dot[b] = 0.0f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int c = (j * L + threadIdx.x) * 8;
         if (c >= a.d) continue;
         if constexpr (!kOne) {
           if (a.dtopk_w) {
-            Chunk<kBF16> raw[kBatch];
-            rows8<kBF16>(a.y, p, a.d, c, raw);
+            Chunk<kBF16> raw[kB];
+            rows8<kBF16, kB>(a.y, p, a.d, c, raw);
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
+            for (int b = 0; b < kB; ++b) {
               if (p[b] < 0) continue;
 #pragma unroll
               for (int q = 0; q < 8; ++q) dot[b] = fmaf(cc[j][q], at8(raw[b], q), dot[b]);
@@ -566,7 +574,7 @@ __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine
         }
         if (a.dy) {
 #pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
+          for (int b = 0; b < kB; ++b) {
             if (p[b] < 0) continue;
             float o[8];
 #pragma unroll
@@ -579,10 +587,10 @@ __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine
         if (a.dtopk_w) {
           group_sum<L, kSums>(dot, lds, turn);
           turn ^= 1;
-          if ((int)threadIdx.x < kBatch && i0 + (int)threadIdx.x < a.k) {
+          if ((int)threadIdx.x < kB && i0 + (int)threadIdx.x < a.k) {
             float v = 0.0f;
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b)
+            for (int b = 0; b < kB; ++b)
               if ((int)threadIdx.x == b && p[b] >= 0) v = dot[b];
             a.dtopk_w[t * a.k + i0 + threadIdx.x] = v;
           }
@@ -738,10 +746,10 @@ hipError_t combine_norm_backward(const Shape& s, const moe_combine_norm_backward
         hipLaunchKernelGGL(kern, dim3(blocks), dim3(L.value), 0, st, a);
       };
       if (s.act == kBF16) {
-        if (s.k <= kBatch) launch(combine_norm_backward_kernel<true, L.value, V.value, true>);
+        if (s.k <= batch_of(true, L.value)) launch(combine_norm_backward_kernel<true, L.value, V.value, true>);
         else launch(combine_norm_backward_kernel<true, L.value, V.value, false>);
       } else {
-        if (s.k <= kBatch) launch(combine_norm_backward_kernel<false, L.value, V.value, true>);
+        if (s.k <= batch_of(false, L.value)) launch(combine_norm_backward_kernel<false, L.value, V.value, true>);
         else launch(combine_norm_backward_kernel<false, L.value, V.value, false>);
       }
     });
