@@ -3,6 +3,8 @@ dispatch, 4-bit conversion and experts, combine with the next block's norm (or
 the layer for a few tokens between two norms), eagerly on a stream of their
 own and replayed from a captured graph; and the backward pass of the norms
 around the router's."""
+import threading
+
 import pytest
 import torch
 
@@ -244,3 +246,34 @@ def test_few_tokens_of_more_column_groups_than_workgroups():
                           out=out, ws=ws)
         want, err = FR.layer(x, idx, gates, mats, [None] * 3, "bf16", bf, 0, E)
         _within(out, want, err, "layer")
+
+
+def test_two_host_threads():
+    """Blocks of many and of few tokens at once, each from a thread and on a stream of its own."""
+    runs = [(Blocks(701, 640, 10, 4, 384, 2, 7, seed=1), False), (Blocks(13, 640, 20, 4, 384, 0, 20, seed=2), True),
+            (Blocks(37, 384, 12, 3, 256, 0, 12, seed=3), False)]
+    want = []
+    for b, few in runs:
+        b.run(few)
+        torch.cuda.synchronize()
+        want.append([L["out"].clone() for L in b.layers])
+    streams, errors = [torch.cuda.Stream() for _ in runs], []
+
+    def work(b, few, stream):
+        try:
+            for _ in range(10):
+                b.run(few, stream=stream)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(b, few, s)) for (b, few), s in zip(runs, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for (b, _), outs in zip(runs, want):
+        for L, out in zip(b.layers, outs):
+            assert torch.equal(L["out"], out)

@@ -249,3 +249,19 @@ def test_rows_and_blocked_layouts_agree_and_captured():
             step(pb, kept, again, B.workspace(pb, B.MOE_CALL_EXPERT_FFN_MX, DEV), stream=side)
             side.synchronize()
             assert torch.equal(again, y)
+
+
+@pytest.mark.parametrize("layout", [B.MOE_MX_SCALES_ROW, B.MOE_MX_SCALES_BLOCK])
+def test_conversion_of_more_tiles_than_workgroups(layout):
+    """8.4 million rows of one block: each workgroup takes several tiles; pieces of it alone give the same."""
+    rows = 8_400_003
+    v = torch.randn(1, rows, 32, generator=_gen(3), device=DEV).to(torch.bfloat16)
+    codes, scales = _convert(v, layout)
+    back = torch.empty_like(v)
+    B.moe_mx_dequantize(codes.contiguous(), scales.contiguous(), back, layout)
+    flat = scales.reshape(-1)                  # (one block a row: the layouts are alike)
+    for lo in (0, 4_194_304, rows - 1001):
+        part = v[:, lo:lo + 1001].contiguous()
+        c, s = _convert(part, B.MOE_MX_SCALES_ROW)
+        assert torch.equal(codes[:, lo:lo + 1001], c) and torch.equal(flat[lo:lo + 1001], s.reshape(-1))
+        assert torch.equal(back[0, lo:lo + 1001].double(), R.values(c[0], s[0]))
