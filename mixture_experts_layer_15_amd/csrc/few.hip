@@ -790,8 +790,10 @@ __device__ __forceinline__ int claim_share(const FewArgs& a, Plan& p, int free) 
 // One token of the Qwen3 shape (75 MB of bfloat16 weights, blocked) 20 us: 4.5 us
 // until the plan stands, 10 of gate/up and down at 6 TB/s and more, and the chip's
 // filling and draining twice.  Sixteen tokens of a rank of the DeepSeek-V3 shape
-// (565 MB of FP8) 106 us.  Five tokens with MXFP4 weights (89 MB) 39 us: bound by
-// the conversion to bfloat16 and the products' idle columns.
+// (565 MB of FP8) 106 us.  Five tokens with MXFP4 weights (89 MB) 39 us: not bound
+// by the number of loads or by those in flight (neither fewer nor more change it);
+// a step's conversion and its products, half of whose columns are idle, come to
+// more than the time of its 2 KB.
 template <int kFmt, bool kBlocked>
 __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   constexpr bool kAct32 = kFmt == kF32;

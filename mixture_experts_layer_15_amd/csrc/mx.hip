@@ -396,8 +396,7 @@ __device__ __forceinline__ void store_y(const MxArgs& a, const f32x16_t& v, int 
 // workgroup take a quarter of K each and add their results through LDS, so
 // that a handful of experts still fills the chip.  64 tokens of the Qwen3 shape:
 // gate/up 38.5 us for 214 MB (5.6 TB/s), down 24.8 us for 107 MB, of which 6 us
-// are the joining of the quarters (three steps of K each) at the start and end of
-// the chip's four turns of items.  Not bound by loads in flight: two, three or
+// are the joining of the quarters (three steps of K each).  Not bound by loads in flight: two, three or
 // four steps a wave take the same, six more (43 and 32 us).  A wave keeps kD steps of
 // 64 K values in flight; nothing passes LDS before the results.
 constexpr int kNB = 4;
