@@ -922,9 +922,17 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
         for (int q = tid; q < a.T * 64; q += kThreads) {
           const int t = q / 64, col = c * 64 + q % 64;
           float sum = 0.0f;
-#pragma unroll 8
-          for (int m = 0; m < parts; ++m)
-            sum += __hip_atomic_load(a.y + ((long long)m * a.T + t) * a.d + col, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          for (int m = 0; m < parts; m += 8) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[i] = __hip_atomic_load(a.y + ((long long)min(m + i, parts - 1) * a.T + t) * a.d + col, __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+            __builtin_amdgcn_sched_barrier(0);  // (all loads before the first sum: one by one,
+                                                // as the compiler may leave them, MXFP4 blocked, 16 tokens, takes 77 us, not 64)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += m + i < parts ? v[i] : 0.0f;
+          }
           if constexpr (kAct32) static_cast<float*>(a.out)[(long long)t * a.d + col] = sum;
           else static_cast<uint16_t*>(a.out)[(long long)t * a.d + col] = f32_to_bf16(sum);
         }
