@@ -313,6 +313,8 @@ moe_status_t moe_forward_noalloc(const moe_problem_t* p, const moe_forward_args_
  *    MOE_ERR_UNSUPPORTED.  Arrays are 16-byte aligned (checked).
  *  - the logits, where given, are written (or read) in place; they are
  *    distinct from the other arrays.
+ * As there, an infinity or a NaN in an expert's weights reaches the tokens that
+ * chose that expert and no others (a down product that meets one is taken twice).
  *  ws, ws_bytes: scratch of moe_workspace_size(p, MOE_CALL_FORWARD_FEW).  The
  *  workgroups of the second kernel wait for each other's results only where
  *  those are under way, so the call needs no share of the device to itself. */

@@ -755,7 +755,9 @@ __device__ __forceinline__ int up_items(const FewArgs& a, const Plan& p, Results
       } else {
         const float h = silu_f32(z) * u * gate;
         const uint32_t hi = f32_to_bf16(h);
-        const uint32_t v = hi | (uint32_t)f32_to_bf16(h - bf16_to_f32(hi)) << 16;
+        // (an h that is infinite as bfloat16 has no remainder: it stays infinite)
+        const float rest = __builtin_isinf(bf16_to_f32(hi)) ? 0.0f : h - bf16_to_f32(hi);
+        const uint32_t v = hi | (uint32_t)f32_to_bf16(rest) << 16;
         const uint32_t w = (uint32_t)__shfl_xor((int)v, 1, kWave);
         // the even lane stores both features' values, the odd one their remainders
         uint16_t* to = static_cast<uint16_t*>(a.h) + (f % 2 ? (long long)p.rows * a.F - 1 : 0) + at;
@@ -799,9 +801,11 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   constexpr bool kAct32 = kFmt == kF32;
   __shared__ Plan p;
   __shared__ __attribute__((aligned(16))) Results red[8];
-  __shared__ int mine;  // whether this workgroup's own share is its
+  __shared__ int mine;     // whether this workgroup's own share is its
+  __shared__ int spoiled;  // whether a result of the down item under way is not finite
   // shares are a power of two, and so are the parts of a column group
   const int tid = threadIdx.x, shares = gridDim.x, log_shares = __builtin_ctz(gridDim.x);
+  if (tid == 0) spoiled = 0;
   // (by the last wave: the first one's loads would wait behind it)
   if (tid == kThreads - 1)
     mine = __hip_atomic_exchange(claim(a, blockIdx.x), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0;
@@ -845,18 +849,34 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   const int n_down = a.d / 64 * parts;
   // Down item (column group c, part j of the list): those experts' sums for 64
   // columns of every token; the last part's workgroup adds the parts.
+  // Tokens that did not choose an expert enter its product as zeros, which add
+  // nothing as long as the weights are finite.  Where a result is not finite, the
+  // item is taken again, expert by expert: between them the sums wait in `red`,
+  // where only the lanes of tokens that chose the expert renew theirs.  So an
+  // infinity or a NaN stays with those tokens, and the others get the bits that
+  // they get without it.
   Stream<kFmt, kBlocked, true> st(a);
   using C = typename Stream<kFmt, kBlocked, true>::C;
   const uint32_t hrow = (uint32_t)a.F * (kAct32 ? 4u : 2u);
   st.xbase = a.h;
   st.x_bytes = (uint32_t)rows * hrow * (kAct32 ? 1 : 2);
   int c = 0, i0 = 0, i1 = 0;
+  int single = -1;  // an item taken again: which of its experts is under way
+  bool more = false;  // and whether others follow
   auto place = [&](int item) {
     c = item >> log_parts;
     const int j = item & (parts - 1);
     i0 = n * j >> log_parts;
     i1 = n * (j + 1) >> log_parts;
+    more = false;
+    if (__builtin_expect(single >= 0, 0)) {
+      i0 += single;
+      more = i0 + 1 < i1;
+      i1 = i0 + 1;
+    }
   };
+  f32x4_t* const kept = reinterpret_cast<f32x4_t*>(red) + tid;  // this lane's sums, four at a time
+  static_assert(sizeof(red) >= 8 * kThreads * sizeof(f32x4_t), "32 sums a lane");
   auto source = [&](int i) {
     const int ii = min(i, n - 1);
     const int e = __builtin_amdgcn_readfirstlane(p.expert[ii]);
@@ -891,6 +911,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
       __builtin_amdgcn_sched_barrier(0);
     }
     st.clear();
+    if (__builtin_expect(single > 0, 0)) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st.acc[q / 4][q % 4 * 4 + j] = kept[q * kThreads][j];
+    }
     int i = i0, s = 0;
     auto turn = [&] {
       const float *q0 = src.q0, *q1 = src.q1;
@@ -902,45 +928,76 @@ __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
     };
     turn();  // (stands apart, as its loads were issued in another order)
     while (i < i1) turn();
-    to_lds<C::kPlanes>(red, st.acc);
-    __syncthreads();
-    const int j = item & (parts - 1);
-    for (int q = tid; q < a.T * 64; q += kThreads) {
-      const int t = q / 64, col = c * 64 + q % 64;
-      float v = all_waves(red, q / 32 % 2, t, q % 32);
-      if constexpr (C::kPlanes) v += all_waves(red + 4, q / 32 % 2, t, q % 32);
-      if (parts > 1) device_store(a.y + ((long long)j * a.T + t) * a.d + col, v);
-      else if constexpr (kAct32) static_cast<float*>(a.out)[(long long)t * a.d + col] = v;
-      else static_cast<uint16_t*>(a.out)[(long long)t * a.d + col] = f32_to_bf16(v);
+    if (__builtin_expect(single >= 0, 0)) {
+      const bool chosen = p.tokens[p.expert[i0]] >> (kAct32 ? st.r : st.r % kMaxTokens) & 1;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const f32x16_t& v = st.acc[q / 4];
+        const f32x4_t sums = {v[q % 4 * 4], v[q % 4 * 4 + 1], v[q % 4 * 4 + 2], v[q % 4 * 4 + 3]};
+        if (chosen) kept[q * kThreads] = sums;
+        else if (single == 0) kept[q * kThreads] = f32x4_t{0, 0, 0, 0};
+      }
+      if (more) {
+        ++single;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) st.acc[q / 4][q % 4 * 4 + j] = kept[q * kThreads][j];
+        __syncthreads();  // (the results take the place of the kept sums)
+      }
     }
-    if (parts > 1) {
-      wait_memory<0>();
+    bool again = true;
+    if (!more) {
+      to_lds<C::kPlanes>(red, st.acc);
       __syncthreads();
-      if (tid == 0) p.last = device_add(column_counter(a, c)) == (uint32_t)(parts - 1);
+      const int j = item & (parts - 1);
+      for (int q = tid; q < a.T * 64; q += kThreads) {
+        const int t = q / 64, col = c * 64 + q % 64;
+        float v = all_waves(red, q / 32 % 2, t, q % 32);
+        if constexpr (C::kPlanes) {
+          // (a product that is not finite is so in the values' sum; the remainders
+          // would make a NaN of an infinity)
+          const float rest = all_waves(red + 4, q / 32 % 2, t, q % 32);
+          if (__builtin_isfinite(rest)) v += rest;
+        }
+        if (single < 0 && !__builtin_isfinite(v)) spoiled = 1;
+        if (parts > 1) device_store(a.y + ((long long)j * a.T + t) * a.d + col, v);
+        else if constexpr (kAct32) static_cast<float*>(a.out)[(long long)t * a.d + col] = v;
+        else static_cast<uint16_t*>(a.out)[(long long)t * a.d + col] = f32_to_bf16(v);
+      }
+      if (parts > 1) wait_memory<0>();  // (the sums are stored)
       __syncthreads();
-      if (p.last) {
-        for (int q = tid; q < a.T * 64; q += kThreads) {
-          const int t = q / 64, col = c * 64 + q % 64;
-          float sum = 0.0f;
-          for (int m = 0; m < parts; m += 8) {
-            float v[8];
+      again = single < 0 && __builtin_amdgcn_readfirstlane(spoiled);
+      single = again ? 0 : -1;
+      if (parts > 1 && !again) {
+        if (tid == 0) p.last = device_add(column_counter(a, c)) == (uint32_t)(parts - 1);
+        __syncthreads();
+        if (p.last) {
+          for (int q = tid; q < a.T * 64; q += kThreads) {
+            const int t = q / 64, col = c * 64 + q % 64;
+            float sum = 0.0f;
+            for (int m = 0; m < parts; m += 8) {
+              float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              v[i] = __hip_atomic_load(a.y + ((long long)min(m + i, parts - 1) * a.T + t) * a.d + col, __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_AGENT);
-            __builtin_amdgcn_sched_barrier(0);  // (all loads before the first sum: one by one,
-                                                // as the compiler may leave them, MXFP4 blocked, 16 tokens, takes 77 us, not 64)
+              for (int i = 0; i < 8; ++i)
+                v[i] = __hip_atomic_load(a.y + ((long long)min(m + i, parts - 1) * a.T + t) * a.d + col, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+              __builtin_amdgcn_sched_barrier(0);  // (all loads before the first sum: one by one,
+                                                  // as the compiler may leave them, MXFP4 blocked, 16 tokens, takes 77 us, not 64)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += m + i < parts ? v[i] : 0.0f;
+              for (int i = 0; i < 8; ++i) sum += m + i < parts ? v[i] : 0.0f;
+            }
+            if constexpr (kAct32) static_cast<float*>(a.out)[(long long)t * a.d + col] = sum;
+            else static_cast<uint16_t*>(a.out)[(long long)t * a.d + col] = f32_to_bf16(sum);
           }
-          if constexpr (kAct32) static_cast<float*>(a.out)[(long long)t * a.d + col] = sum;
-          else static_cast<uint16_t*>(a.out)[(long long)t * a.d + col] = f32_to_bf16(sum);
         }
       }
     }
-    item += shares;
+    if (!again) item += shares;
     if (item < n_down) {
       __syncthreads();
+      if (tid == 0) spoiled = 0;
       begin();
     }
   }
