@@ -438,10 +438,11 @@ struct CombineNormGradArgs {
 constexpr int batch_of(bool bf16, int threads) { return threads < 1024 ? kBatch : bf16 ? 4 : 2; }
 
 // One pass over the y rows where the slots are a batch (kOne): with a chunk's rows in registers
-// its c is complete, so <u, y_i> and <c, y_i> are summed at once and
-//    <dc, y_i> = r (<u, y_i> - r mean(n u) <c, y_i>)
-// needs no second look at y.  More slots read y twice, the second time from a
-// cache.
+// its c is complete, so <u, r y_i> and <n, r y_i> are summed at once and
+//    <dc, y_i> = <u, r y_i> - mean(n u) <n, r y_i>
+// needs no second look at y.  (Terms of the result's size: <c, y_i> leaves the
+// float32 range where a large y_i meets a small gate.)  More slots read y twice, the
+// second time from a cache.
 // Narrow bfloat16 rows keep to 128 registers: four workgroups of 256 a compute
 // unit, which hide each other's loads (4099 x 2048, k = 8, of 286 MB: 75 -> 64.6
 // us).  Wider rows do not fit there: held to 168 registers 8192 x 4096, k = 4
@@ -450,7 +451,7 @@ template <bool kBF16, int L, int V, bool kOne>
 __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine_norm_backward_kernel(
     CombineNormGradArgs a) {
   constexpr int kB = batch_of(kBF16, L);
-  constexpr int kPairs = 2 * kB;  // <u, y_i> and <c, y_i>
+  constexpr int kPairs = 2 * kB;  // <u, r y_i> and <n, r y_i>
   constexpr int kSums = kOne ? 1 + kPairs : kB;
   constexpr int kW = L / kWave;
   __shared__ float lds[2 * kW * kSums];
@@ -463,7 +464,7 @@ __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine
   for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
     const long long row = t * a.d;
     const float r = a.rstd[t];
-    float cc[V][8], u[V][8];
+    float cc[V][8], u[V][8];  // c, then n, then dc; u
     float s[1] = {0.0f}, e[kOne ? kPairs : 1];
 #pragma unroll
     for (int n = 0; n < (kOne ? kPairs : 1); ++n) e[n] = 0.0f;
@@ -497,6 +498,7 @@ __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine
           u[j][q] = w[q] * (a.gate ? o * f[q] : o);
           s[0] = fmaf(n, u[j][q], s[0]);
           acc[j][q] = fmaf(o, n, acc[j][q]);
+          cc[j][q] = n;
         }
         if constexpr (kOne) {
           if (a.dtopk_w) {
@@ -505,7 +507,7 @@ __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine
               if (p[b] < 0) continue;
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
-                const float v = at8(raw[b], q);
+                const float v = r * at8(raw[b], q);
                 e[2 * b] = fmaf(u[j][q], v, e[2 * b]);
                 e[2 * b + 1] = fmaf(cc[j][q], v, e[2 * b + 1]);
               }
@@ -534,15 +536,15 @@ __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine
     if constexpr (kOne) {
       if (a.dtopk_w && (int)threadIdx.x < a.k) {
         const float* at = lds + turn * (kW * kSums) + 1 + 2 * threadIdx.x;
-        float uy = at[0], cy = at[1], v = 0.0f;
+        float uy = at[0], ny = at[1], v = 0.0f;
 #pragma unroll
         for (int w = 1; w < kW; ++w) {
           uy += at[w * kSums];
-          cy += at[w * kSums + 1];
+          ny += at[w * kSums + 1];
         }
 #pragma unroll
         for (int b = 0; b < kB; ++b)
-          if ((int)threadIdx.x == b && p[b] >= 0) v = r * (uy - r * m * cy);
+          if ((int)threadIdx.x == b && p[b] >= 0) v = uy - m * ny;
         a.dtopk_w[t * a.k + threadIdx.x] = v;
       }
     }
@@ -550,7 +552,7 @@ __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) cc[j][q] = r * (u[j][q] - cc[j][q] * r * m);  // dc
+      for (int q = 0; q < 8; ++q) cc[j][q] = r * (u[j][q] - cc[j][q] * m);  // dc
     for (int i0 = 0; i0 < a.k; i0 += kB) {
       if constexpr (!kOne) slots8<kB>(a.pos, a.topk_w, t, a.k, i0, a.S, p, g);
       float dot[kB];
