@@ -650,9 +650,10 @@ moe_status_t moe_mx_dequantize(int32_t batch, int32_t rows, int32_t cols, int32_
  * scale byte 255 (and one whose h holds an infinity or a NaN) gives NaN.
  *  p: act MOE_BF16 (the format of y), weight MOE_MXFP4, either layout.
  *  x_codes [T][d / 2], x_scales [T][d / 32] (MOE_MX_SCALES_ROW).
- *  The other arguments are those of moe_expert_ffn; segment bounds in offsets
- *  are held inside [0, T*k].  Rows of y behind the last kept row are not
- *  written.  Arrays are 16-byte aligned.
+ *  The other arguments are those of moe_expert_ffn.  Segment bounds in offsets
+ *  are held inside [0, T*k]; where they do not ascend, rows of y are unspecified,
+ *  but nothing other than y and ws is written.  Rows of y behind the last kept
+ *  row are not written.  Arrays are 16-byte aligned.
  *  ws, ws_bytes: scratch of moe_workspace_size(p, MOE_CALL_EXPERT_FFN_MX). */
 moe_status_t moe_expert_ffn_mx(const moe_problem_t* p, const void* x_codes, const void* x_scales,
                                const int32_t* sorted_slot, const int32_t* offsets,

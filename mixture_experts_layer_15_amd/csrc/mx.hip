@@ -26,6 +26,7 @@
 
 #include "moe_device.h"
 #include "moe_internal.h"
+#include "mx_plan.h"
 
 namespace moe {
 namespace {
@@ -226,6 +227,7 @@ struct MxArgs {
   uint8_t* h;                  // gate/up: h units
   uint8_t* hs;                 // gate/up: h scales
   int El, S;
+  int max_groups;              // that h has room for
   int K, Nout;
   int blocked;
 };
@@ -236,8 +238,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint32_
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
 }
 
-// Segment bounds as the caller gives them, held inside [0, S] so that no row
-// of another array is touched whatever they are.
+// Segment bounds as the caller gives them, held inside [0, S], so that rows of y
+// are in bounds whatever they are (bounds that do not ascend: group_table).
 __device__ __forceinline__ int bound(const MxArgs& a, int e) {
   return max(0, min(a.offsets[e], a.S));
 }
@@ -255,37 +257,36 @@ __device__ __forceinline__ int uniform_bound(const MxArgs& a, int e) {
 
 // groups[e] = number of groups of 32 rows of experts before e (groups[El]: of
 // all), each expert's counted up to a multiple of kUnit, by one workgroup of
-// kThreads threads.
+// kThreads threads.  Never more than the workspace holds (as long as the segments
+// do not overlap, it holds all; the sums stop there, so they cannot overflow).
 template <int kThreads, int kUnit>
 __device__ __forceinline__ void group_table(const MxArgs& a, int* groups) {
   constexpr int kPer = kMaxExperts / kThreads;
   __shared__ int waves[kThreads / kWave];
+  const int limit = a.max_groups / kUnit * kUnit;
   int n[kPer], sum = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = threadIdx.x * kPer + i;
-    n[i] = 0;
-    if (e < a.El) {
-      const int rows = max(0, bound(a, e + 1) - bound(a, e));
-      n[i] = rows / (32 * kUnit) * kUnit + (rows % (32 * kUnit) ? kUnit : 0);
-    }
-    sum += n[i];
+    n[i] = e < a.El ? mx_groups(max(0, bound(a, e + 1) - bound(a, e)), kUnit) : 0;
+    sum = mx_add_groups(sum, n[i], limit);
   }
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) {
     const int v = __shfl_up(incl, o, kWave);
-    if (lane_id() >= o) incl += v;
+    if (lane_id() >= o) incl = mx_add_groups(incl, v, limit);
   }
   if (lane_id() == kWave - 1) waves[threadIdx.x / kWave] = incl;
+  int before = __shfl_up(incl, 1, kWave);
+  if (lane_id() == 0) before = 0;
   __syncthreads();
-  int before = incl - sum;
-  for (int w = 0; w < (int)threadIdx.x / kWave; ++w) before += waves[w];
+  for (int w = 0; w < (int)threadIdx.x / kWave; ++w) before = mx_add_groups(before, waves[w], limit);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = threadIdx.x * kPer + i;
     if (e <= a.El) groups[e] = before;
-    before += n[i];
+    before = mx_add_groups(before, n[i], limit);
   }
   if (a.El == kMaxExperts && threadIdx.x == kThreads - 1) groups[kMaxExperts] = before;
   __syncthreads();
@@ -767,8 +768,9 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
   const bool use_slots = kGateUp || a.topk_w;
   auto load_gates = [&](float (&w)[2]) {
     if (kGateUp || !a.topk_w) return;
-    w[0] = a.topk_w[slot[0]];
-    w[1] = a.topk_w[slot[1]];
+    // (slots behind the last kept one may be anything)
+    w[0] = a.topk_w[min((uint32_t)slot[0], (uint32_t)a.S - 1)];
+    w[1] = a.topk_w[min((uint32_t)slot[1], (uint32_t)a.S - 1)];
   };
   auto after = [&](const Item& t, bool there) { return there ? place(t.e, t.in + slots) : t; };
   if (use_slots) load_slots(cur, slot);
@@ -926,9 +928,7 @@ bool use_tiles(const Shape& s) {
 }
 
 // Groups of 32 rows that the experts' segments can have.
-size_t max_groups(const Shape& s) {
-  return (size_t)(s.S / 32 + std::min<long long>(s.S, s.El) * (use_tiles(s) ? kBM : 1));
-}
+size_t max_groups(const Shape& s) { return (size_t)mx_max_groups(s.S, s.El, use_tiles(s) ? kBM : 1); }
 
 template <bool kGateUp>
 hipError_t launch_products(const Shape& s, const MxArgs& a, hipStream_t st) {
@@ -1013,6 +1013,7 @@ hipError_t expert_ffn_mx(const Shape& s, const uint8_t* x, const uint8_t* xs, co
   a.hs = hs;
   a.El = s.El;
   a.S = (int)s.S;
+  a.max_groups = (int)max_groups(s);
   a.K = s.d;
   a.Nout = s.F;
   a.blocked = s.blocked;
