@@ -64,7 +64,7 @@ __device__ __forceinline__ uint32_t mx_codes8(const float* v, float inv) {
 // Tiles of kTileCols columns and `rt` rows (a multiple of 8): 32 threads of 8
 // values for a row, 8 rows a pass.  Block-major scales pass through LDS, so
 // that they are written and read in runs of rt bytes.
-constexpr int kTileCols = 256;
+constexpr int kTileCols = kMxTileCols;
 
 struct ConvertArgs {
   const void* src;
@@ -948,14 +948,9 @@ hipError_t launch_products(const Shape& s, const MxArgs& a, hipStream_t st) {
 template <bool kQuantize>
 hipError_t convert(int batch, int rows, int cols, int bf16, const void* src, void* dst, uint8_t* codes,
                    uint8_t* scales, int block_major, hipStream_t st) {
-  ConvertArgs a{src, dst, codes, scales, rows, cols, 8, 0, 0, 0};
-  a.col_tiles = (cols + kTileCols - 1) / kTileCols;
-  // block-major scales in runs of 64 bytes where that leaves work for the chip
-  // (128 matrices of 768 x 2048 quantized: 82 us, in runs of 8 bytes 104; 4 of them,
-  // 384 tiles of 64 rows: equal)
-  if (block_major && (long long)batch * ((rows + 63) / 64) * a.col_tiles >= 1024) a.rt = 64;
-  a.row_tiles = (rows + a.rt - 1) / a.rt;
-  a.tiles = (long long)batch * a.row_tiles * a.col_tiles;
+  const MxConvertPlan plan = mx_convert_plan(batch, rows, cols, block_major);
+  const ConvertArgs a{src,  dst,     codes,          scales,         rows,
+                      cols, plan.rt, plan.row_tiles, plan.col_tiles, plan.tiles};
   const unsigned grid = (unsigned)std::min(a.tiles, 1LL << 20);
   auto go = [&](auto b, auto m, auto p) {
     if constexpr (kQuantize)

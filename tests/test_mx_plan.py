@@ -1,6 +1,7 @@
-"""How the 4-bit calls count groups of rows (csrc/mx_plan.h, compiled here as
-host code): segments that do not overlap keep all of their groups, and no
-bounds whatever get more than the workspace holds."""
+"""How the 4-bit calls count (csrc/mx_plan.h, compiled here as host code):
+segments that do not overlap keep all of their groups of rows, no bounds
+whatever get more than the workspace holds, and the tiles of a conversion
+cover matrices up to the limits without an overflow."""
 import os
 import random
 import shutil
@@ -33,6 +34,18 @@ int main() {
       before = moe::mx_add_groups(before, moe::mx_groups((int)std::max(0LL, b[e + 1] - b[e]), unit), limit);
     }
     std::printf(" %d\n", before);
+  }
+}
+"""
+
+CONVERT = r"""
+#include <cstdio>
+#include "mx_plan.h"
+int main() {
+  int batch, rows, cols, block;
+  while (std::scanf("%d %d %d %d", &batch, &rows, &cols, &block) == 4) {
+    const moe::MxConvertPlan p = moe::mx_convert_plan(batch, rows, cols, block);
+    std::printf("%d %d %d %lld\n", p.rt, p.row_tiles, p.col_tiles, p.tiles);
   }
 }
 """
@@ -78,3 +91,19 @@ def test_groups_of_any_bounds_fit_the_workspace(tmp_path):
         else:
             held += want[-1] > most
     assert held > 100     # (bounds that would pass the end of the workspace are among them)
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs a host compiler")
+def test_tiles_of_a_conversion(tmp_path):
+    top = 2 ** 31 - 1
+    shapes = [(b, r, c) for b, r in ((1, 1), (1, 7), (1, 8), (1, 9), (1, 63), (1, 64), (1, 65), (3, 1000), (128, 768), (4, 768), (top, 1), (65535, 32767),
+                                     (1, top), (1, top - 1), (1, top - 7), (1, top - 8), (1, top - 62), (1, top - 63), (1, top - 64))
+              for c in (32, 256, 288, 2048, 65536)]
+    cases = [(b, r, c, block) for b, r, c in shapes for block in (0, 1)]
+    rows = _ask(tmp_path, "convert", CONVERT, [" ".join(map(str, c)) for c in cases], "-fsanitize=undefined", "-fno-sanitize-recover=all")
+    assert len(rows) == len(cases)
+    for (b, r, c, block), (rt, row_tiles, col_tiles, tiles) in zip(cases, rows):
+        assert col_tiles == -(-c // 256)
+        assert rt == (64 if block and b * -(-r // 64) * col_tiles >= 1024 else 8)
+        assert row_tiles == -(-r // rt) and tiles == b * row_tiles * col_tiles
+        assert (row_tiles - 1) * rt + rt - 1 <= top       # the last tile's last row, an int in the kernels
