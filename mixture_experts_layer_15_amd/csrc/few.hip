@@ -441,7 +441,8 @@ struct Format {
   // what belongs to each other's rows: four lanes that read 16 bytes of a row
   // each pass the cache at a quarter of the rate.  (So K comes in another order:
   // piece 4 g + j of a run in its step j.  Sixteen tokens of the Qwen3 shape in
-  // bfloat16 236 -> 169 us, in FP8 155 -> 115, five in float32 242 -> 146.)
+  // bfloat16 236 -> 169 us, in FP8 155 -> 115 (102 since the
+  // parts' sums are loaded together), five in float32 242 -> 146.)
   static constexpr bool kQuads = !kBlocked && kRun == 4;
   // loads a wave keeps in flight per weight block (two of four KB each do:
   // 6.6 TB/s, as eight or twelve)
@@ -792,10 +793,11 @@ __device__ __forceinline__ int claim_share(const FewArgs& a, Plan& p, int free) 
 // One token of the Qwen3 shape (75 MB of bfloat16 weights, blocked) 20 us: 4.5 us
 // until the plan stands, 10 of gate/up and down at 6 TB/s and more, and the chip's
 // filling and draining twice.  Sixteen tokens of a rank of the DeepSeek-V3 shape
-// (565 MB of FP8) 106 us.  Five tokens with MXFP4 weights (89 MB) 39 us: not bound
-// by the number of loads or by those in flight (neither fewer nor more change it);
-// a step's conversion and its products, half of whose columns are idle, come to
-// more than the time of its 2 KB.
+// (565 MB of FP8) 102 us in a steady loop, 111 to 124 traced.  Five tokens with MXFP4
+// weights (89 MB) 35 us blocked and 42 row-major, sixteen (200 MB) 59 and 81: 1.5 to
+// 2.5 times their bytes' time.  There the matrix cores are busy for 14 to 23 % of the
+// cycles and the vector units for 25 to 34; a wave waits for 35 to 43 % of its own.
+// Neither fewer nor more loads in flight change it; what it waits for is not known.
 template <int kFmt, bool kBlocked>
 __global__ __launch_bounds__(kThreads, 2) void few_layer_kernel(FewArgs a) {
   constexpr bool kAct32 = kFmt == kF32;

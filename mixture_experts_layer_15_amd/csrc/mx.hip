@@ -581,7 +581,7 @@ constexpr int kStageWS = kStageW + 8 * kBlock;     // their scales [4 K blocks][
 constexpr int kStage = kStageWS + 4 * 256;
 constexpr int kRowScales = kStages * kStage;       // [2][128 rows][16]
 constexpr int kTileTable = kRowScales + 2 * kBM * 512;  // groups before each expert, El + 1
-// (up to 251 experts two workgroups fit a compute unit)
+// (up to 251 experts two workgroups fit a compute unit, with more of them one)
 inline int tile_lds(int El) { return kTileTable + (El + 1) * 4; }
 
 // One LDS-DMA load per active lane: lane i's 16 (4) bytes, from voff + soff in
@@ -923,6 +923,8 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxArgs a) {
 // into registers, are 32 bytes of each of 32 rows a load (128 experts of the Qwen3
 // shape with 4 rows 149 us, in tiles 77; 8 of 4096 x 1536 with 1 row 42 and 35; the
 // other way round only for the smallest: 2 of 1024 x 768 16 and 18).
+// Rows are counted over all T k slots, as the host knows no more: where a rank holds
+// a part of the experts, those named here are all its slots', of which it keeps some.
 bool use_tiles(const Shape& s) {
   return !s.blocked || (s.S >= 24LL * s.El && s.S * s.F >= 448LL * (32 * 64));
 }

@@ -11,8 +11,11 @@
 //            dw = g S, dg = w S  with  S = sum_t dout n   (w and g are per channel)
 //
 // Every kernel gives a row to a group of L threads (one workgroup) that holds
-// it in registers, V chunks of 8 columns a thread, so that every array passes
-// HBM once: these are HBM-bound passes.  Sums are float32 in a fixed order (a
+// it, V chunks of 8 columns a thread, so that every array passes HBM once: these
+// are HBM-bound passes.  Registers hold all of it up to 16384
+// columns, in combine_norm_backward up to 4096 (float32: 44 of them spilled beyond;
+// bfloat16 in two passes: 79 beyond 8192); at four chunks a thread up to 166 are
+// spilled, at eight up to 555.  Sums are float32 in a fixed order (a
 // wave's butterfly, then the waves in order; over tokens each workgroup adds
 // its rows in order and a second kernel the workgroups).  Nothing is rounded
 // but what is stored.
@@ -445,7 +448,7 @@ constexpr int batch_of(bool bf16, int threads) { return threads < 1024 ? kBatch 
 // second time from a cache.
 // Narrow bfloat16 rows keep to 128 registers: four workgroups of 256 a compute
 // unit, which hide each other's loads (4099 x 2048, k = 8, of 286 MB: 75 -> 64.6
-// us).  Wider rows do not fit there: held to 168 registers 8192 x 4096, k = 4
+// us; 6 registers are spilled for it, 30 to 37 in two passes).  Wider rows do not fit there: held to 168 registers 8192 x 4096, k = 4
 // takes 190 us rather than 154.
 template <bool kBF16, int L, int V, bool kOne>
 __global__ __launch_bounds__(L, kBF16&& V == 1 && L <= 256 ? 4 : 1) void combine_norm_backward_kernel(
